@@ -59,7 +59,9 @@ enum {
 enum {
     SPG_FMT_E4M3_ROW = 0,    /* E4M3 codes; fp32 scale per row of A and of W  */
     SPG_FMT_E4M3_TENSOR = 1, /* E4M3 codes; one fp32 scale per matrix         */
-    SPG_FMT_NVFP4 = 2        /* E2M1 codes 2/byte + E4M3 scale per 16 + fp32  */
+    SPG_FMT_NVFP4 = 2,       /* E2M1 codes 2/byte + E4M3 scale per 16 + fp32  */
+    SPG_FMT_E4M3_BLOCK128 = 3 /* E4M3 codes; fp32 scale per row and 128       */
+                             /* K-elements of A, per 128 x 128 block of W    */
 };
 
 /* ---- fused epilogues (ninfer: linear, linear_add, linear_swiglu) -------- */
@@ -171,6 +173,34 @@ int quantize_block16(const void *x, int64_t rows, int64_t K, uint8_t *q, uint8_t
  */
 int quantize_block16_noalloc(const void *x, int64_t rows, int64_t K, uint8_t *q, uint8_t *bscale,
                              float *tscale, int scale_layout, void *stream);
+
+/*
+ * quantize_block128 - FP8 E4M3 with one fp32 scale per 128 elements, the
+ * operands of SPG_FMT_E4M3_BLOCK128.  With the arithmetic of
+ * quantize_rowwise over each group: s = fl32(amax / 448), q = E4M3(fl32(x /
+ * s)).  Groups at the right and lower edge are smaller.
+ *   tiling SPG_BLOCK_ROW    : 1 x 128 (A of a product along the rows);
+ *                             scale [ceil(K / 128), rows], group-major
+ *          SPG_BLOCK_COLUMN : 128 x 1 (A of a product along the columns: a
+ *                             K-major A); scale [ceil(rows / 128), K]
+ *          SPG_BLOCK_BLOCK  : 128 x 128 (W of either);
+ *                             scale [ceil(rows / 128), ceil(K / 128)]
+ *   x     : bf16, `batch` matrices [rows, K], row stride ldx, batch stride
+ *           bstride (elements)
+ *   q     : uint8 codes, row stride ldq, batch stride qbstride (bytes)
+ *   scale : fp32, one contiguous plane per matrix, planes back to back
+ *   K % 16 == 0, ldx >= K, ldq >= K, ldx % 8 == 0, ldq % 16 == 0; with batch >
+ *   1 bstride >= (rows - 1) * ldx + K and % 8 == 0, qbstride >= (rows - 1) *
+ *   ldq + K and % 16 == 0.  rows == 0 is a no-op; rows > 0 with K == 0 is
+ *   invalid.  One launch, no workspace; every byte is read once.
+ */
+enum {
+    SPG_BLOCK_ROW = 0,
+    SPG_BLOCK_COLUMN = 1,
+    SPG_BLOCK_BLOCK = 2
+};
+int quantize_block128(const void *x, int64_t batch, int64_t rows, int64_t K, int64_t ldx, int64_t bstride,
+                      uint8_t *q, int64_t ldq, int64_t qbstride, float *scale, int tiling, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* GEMM                                                                      */
@@ -295,7 +325,14 @@ void spg_gemm_desc_init(spg_gemm_desc *d, int64_t M, int64_t N, int64_t K, int32
  *              unless that operand's batch stride is 0);
  *              E4M3_TENSOR: fp32 [batch] each (index 0 when broadcast);
  *              NVFP4: E4M3 block-scale planes [M, K/16] and [N, K/16] in
- *              d->scale_layout (NVFP4 requires batch == 1)
+ *              d->scale_layout (NVFP4 requires batch == 1);
+ *              E4M3_BLOCK128: fp32 planes as quantize_block128 writes them,
+ *              sa [ceil(K/128), M] (row groups of A, or column groups of a
+ *              K-major A), sw the 128 x 128 blocks of W as it is stored:
+ *              [ceil(N/128), ceil(K/128)], K-major [ceil(K/128),
+ *              ceil(N/128)]; batch entries back to back unless that
+ *              operand's batch stride is 0.  SWIGLU needs N % 256 == 0: the
+ *              up rows start on a block boundary
  *   residual : bf16 [M, N] (or one row [N] when ldr == 0; E4M3 codes [N]
  *              when d->bias_scale is set), required for SPG_EPI_ADD, NULL
  *              otherwise; it may be the output itself (residual == out,
@@ -311,11 +348,152 @@ void spg_gemm_desc_init(spg_gemm_desc *d, int64_t M, int64_t N, int64_t K, int32
  *   stride_o >= (M - 1) * ldo + n_out, else SPG_EINVAL.
  * Results: each element within 2^-8 |y| + 2^-12 S of the exact value y,
  * where S is the scaled sum of |products| (fp32 accumulation order is free).
+ * E4M3_BLOCK128 forms the factor sa * sw of each group in fp32: the bound
+ * holds while these products stay in fp32's normal range.
  */
 size_t gemm_scaled_workspace_bytes(const spg_gemm_desc *d, int epilogue);
 int gemm_scaled(void *out, const void *A, const void *sa, const void *W, const void *sw,
                 const void *residual, int epilogue, const spg_gemm_desc *d,
                 void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Experts: routing, one product per expert, the weighted sum                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * gemm_grouped - one E4M3_BLOCK128 product per expert over rows that are
+ * grouped by expert: for expert e and every output row r in
+ * [offsets[e], offsets[e + 1])
+ *     out[r] = epilogue(A[row_index[r]] W_e^T)      (A[r] without row_index)
+ * with the scales of SPG_FMT_E4M3_BLOCK128.  An expert may have any number of
+ * rows, none included.
+ *   rows      : output rows; rows outside every expert's range are left as
+ *               they were
+ *   a_rows    : rows of A and columns of its scale plane sa [ceil(K/128),
+ *               a_rows]; without row_index at least `rows`
+ *   A         : codes [a_rows, K], row stride lda; with row_index a_rows *
+ *               lda < 2^31 (else SPG_EUNSUPPORTED)
+ *   W, sw     : codes [experts, N, K], row stride ldw, expert stride
+ *               stride_w (bytes); sw [experts, ceil(N/128), ceil(K/128)]
+ *   offsets   : device int32 [experts + 1], not decreasing, within [0, rows].
+ *               The call cannot check device data: offsets are clamped to
+ *               that range and a decreasing pair is an empty expert, so
+ *               nothing outside the operands is read or written; where
+ *               ranges overlap after that, those rows hold either expert's
+ *               values
+ *   row_index : device int32 [rows] or NULL; the row of A that output row r
+ *               is made from (an index outside [0, a_rows) stands for a row
+ *               of zeros); the same row may serve any number of output rows
+ *   out       : bf16 [rows, N], or [rows, N/2] for SWIGLU, row stride ldo;
+ *               it must not overlap an input
+ *   epilogue  : SPG_EPI_STORE or SPG_EPI_SWIGLU (N % 256 == 0); ADD:
+ *               SPG_EUNSUPPORTED
+ * K % 16 == 0, lda, ldw, stride_w % 16 == 0, lda, ldw <= 2^23, 1 <= experts
+ * <= 65536.  One launch, no workspace.  Accuracy as gemm_scaled.
+ */
+typedef struct spg_grouped_desc {
+    int64_t rows, a_rows, N, K;
+    int64_t lda, ldw, stride_w, ldo;
+    int32_t experts, reserved;
+} spg_grouped_desc;
+
+int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const float *sw, const int32_t *offsets,
+                 const int32_t *row_index, int epilogue, const spg_grouped_desc *d, void *stream);
+
+/* Rows of the tiles gemm_grouped takes for `d` (16, 32, 128 or 256), chosen
+ * from rows / experts; 0 for an invalid call.  Host query. */
+int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
+
+/*
+ * expert_route - the experts of each token, their weights, and the row order
+ * of the experts' products.  For a token with logits l:
+ *   p = softmax(l) or 1 / (1 + exp(-l)); c = p + bias
+ *   groups of E / groups consecutive experts, scored by the sum of their two
+ *   largest c (one where a group has only one): the top_groups best stay
+ *   experts : the `top` largest c in the groups that stay, largest first,
+ *             ties (experts' and groups') to the lowest index
+ *   weights : scale p / (sum of the chosen p) with renormalize, else scale p
+ * The bias steers the choice only.  p and c are computed and compared in 64
+ * bits (without bias and with one group, the logits are compared).
+ * A logit or c of -inf is never chosen: where fewer than `top` experts are
+ * left, the remaining places get expert -1 and weight 0, so a token whose
+ * logits are all -inf has no expert.  A NaN logit is never chosen and makes
+ * its token's weights NaN.
+ *   logits  : [T, E], fp32 or (logits_bf16) bf16, row stride ld elements
+ *   bias    : fp32 [E] or NULL
+ *   weights : fp32 [T, top]
+ *   experts : int32 [T, top]
+ *   offsets, rows, slots : the row order, all three or (all NULL) none:
+ *             offsets int32 [E + 1], rows of expert e are [offsets[e],
+ *             offsets[e + 1]) ordered by token; rows int32 [T * top], the
+ *             token of each row (-1 from row offsets[E] on); slots int32
+ *             [T, top], the row of each (token, place), -1 where there is no
+ *             expert.  They are gemm_grouped's offsets and row_index and
+ *             expert_combine's slots.
+ *   ws      : device workspace of at least expert_route_workspace_bytes(T, E)
+ *             (any contents; not used without row order; 0 for up to 64
+ *             tokens, whose routing is one launch)
+ * 1 <= E <= 1024, 1 <= top <= min(E, 32), 1 <= groups <= 64 dividing E,
+ * 1 <= top_groups <= groups, T * top < 2^31; beyond: SPG_EUNSUPPORTED for
+ * E, top and groups too large, else SPG_EINVAL.  scale is any finite number.
+ */
+enum {
+    SPG_SCORE_SOFTMAX = 0,
+    SPG_SCORE_SIGMOID = 1
+};
+typedef struct spg_route_desc {
+    int64_t T, ld;
+    int32_t E, top, groups, top_groups;
+    int32_t score, renormalize, logits_bf16;
+    float scale;
+} spg_route_desc;
+
+size_t expert_route_workspace_bytes(int64_t T, int32_t E);
+int expert_route(const void *logits, const float *bias, float *weights, int32_t *experts, int32_t *offsets,
+                 int32_t *rows, int32_t *slots, const spg_route_desc *d, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * expert_sort - the row order of experts chosen elsewhere: offsets, rows and
+ * slots as expert_route gives them for experts [T, top] (contiguous; values
+ * outside [0, E) stand for no expert).  ws as for expert_route.
+ */
+int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32_t E, int32_t *offsets, int32_t *rows,
+                int32_t *slots, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * expert_route_backward - the gradient of the logits from that of the
+ * weights: grad_weights fp32 [T, top], logits and experts of expert_route,
+ * the same desc (bias and groups have no gradient: the choice is constant);
+ * grad_logits [T, E] contiguous in the logits' type, written whole.  fp32
+ * arithmetic, one rounding.  With renormalize a softmax's gradient reaches
+ * the chosen experts only (the others cancel).
+ */
+int expert_route_backward(const float *grad_weights, const void *logits, const int32_t *experts, void *grad_logits,
+                          const spg_route_desc *d, void *stream);
+
+/*
+ * expert_combine - out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]]:
+ * fp32 sums in the order of j, one rounding to bf16.
+ *   y        : bf16 [R, H], row stride ldy
+ *   weights  : fp32 [T, top]; slots int32 [T, top] (outside [0, R): no term)
+ *   residual : bf16 [T, H], row stride ldr, or NULL; it may be the output
+ *              itself (ldr == ldo), any other overlap is SPG_EINVAL
+ *   out      : bf16 [T, H], row stride ldo
+ * Strides are at least H; 16-byte aligned rows (H % 8 == 0) move as vectors.
+ * 1 <= top <= 32.  T == 0 or H == 0 is a no-op.
+ *
+ * expert_combine_backward - its gradients: grad_y[slots[t, j]] = weights[t, j]
+ * grad_out[t] (bf16 [R, H], row stride ldgy; rows that no slot names are left
+ * as they were; the slots must be distinct, as expert_route's are) and
+ * grad_weights[t, j] = <grad_out[t], y[slots[t, j]]> in fp32 (0 without a
+ * row).  The residual's gradient is grad_out.  grad_y must not overlap an
+ * input.
+ */
+int expert_combine(const void *y, int64_t R, int64_t ldy, const float *weights, const int32_t *slots, int64_t T,
+                   int32_t top, int64_t H, const void *residual, int64_t ldr, void *out, int64_t ldo, void *stream);
+int expert_combine_backward(const void *grad_out, int64_t ldg, const void *y, int64_t R, int64_t ldy,
+                            const float *weights, const int32_t *slots, int64_t T, int32_t top, int64_t H,
+                            void *grad_y, int64_t ldgy, float *grad_weights, void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* Tile / route selection (host only, no device access)                     */
@@ -364,7 +542,9 @@ typedef struct spg_plan {
                              /* the tail) * split_k, or at most one per       */
                              /* compute unit when the FP8 kernel runs an      */
                              /* unsplit product persistently                  */
-    int32_t kernel;          /* 0: FP8 256 x 256 tiles; 1: NVFP4; 2: FP8      */
+    int32_t kernel;          /* 4 - 6: E4M3_BLOCK128 (256 x 256 tiles, 128 x  */
+                             /* 256 tiles, decode width as kernel 3), else    */
+                             /* 0: FP8 256 x 256 tiles; 1: NVFP4; 2: FP8      */
                              /* 128 x 256 tiles (bm = 128) over the product,  */
                              /* one workgroup each (tiles counts 128-row      */
                              /* tiles);                                       */

@@ -9,28 +9,35 @@ fails loudly when the library is not built.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
+import math
 import os
 
 import torch
 
 __all__ = [
-    "quantize_rowwise", "quantize_tensor", "quantize_block16", "gemm_scaled",
+    "quantize_rowwise", "quantize_tensor", "quantize_block16", "quantize_block128", "gemm_scaled", "gemm_grouped",
+    "expert_route", "expert_sort", "expert_route_backward", "expert_combine", "expert_combine_backward",
+    "ExpertRoute", "expert_workspace", "grouped_tile_rows", "block128_scale_shape",
     "gemm_plan", "gemm_workspace", "route_select", "route_cost", "probe_mfma", "probe_read", "probe_fp4_rounding",
     "lib", "LIB_PATH",
-    "FMT_E4M3_ROW", "FMT_E4M3_TENSOR", "FMT_NVFP4", "EPI_STORE", "EPI_ADD", "EPI_SWIGLU",
+    "FMT_E4M3_ROW", "FMT_E4M3_TENSOR", "FMT_NVFP4", "FMT_E4M3_BLOCK128", "EPI_STORE", "EPI_ADD", "EPI_SWIGLU",
     "SpgError", "check_operands", "block16_scale_shape", "SCALES_ROW_MAJOR", "SCALES_BLOCKED", "QUANT_SINGLE_LAUNCH",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspg.so")
 
-FMT_E4M3_ROW, FMT_E4M3_TENSOR, FMT_NVFP4 = 0, 1, 2
+FMT_E4M3_ROW, FMT_E4M3_TENSOR, FMT_NVFP4, FMT_E4M3_BLOCK128 = 0, 1, 2, 3
 EPI_STORE, EPI_ADD, EPI_SWIGLU = 0, 1, 2
 SCALES_ROW_MAJOR, SCALES_BLOCKED = 0, 1
 QUANT_SINGLE_LAUNCH = 0x100
 _LAYOUT = {"row": SCALES_ROW_MAJOR, "blocked": SCALES_BLOCKED}
 _EPI = {"store": EPI_STORE, "add": EPI_ADD, "swiglu": EPI_SWIGLU}
-_FMT = {"e4m3_row": FMT_E4M3_ROW, "e4m3_tensor": FMT_E4M3_TENSOR, "nvfp4": FMT_NVFP4}
+_FMT = {"e4m3_row": FMT_E4M3_ROW, "e4m3_tensor": FMT_E4M3_TENSOR, "nvfp4": FMT_NVFP4,
+        "e4m3_block128": FMT_E4M3_BLOCK128}
+_TILING = {"row": 0, "column": 1, "block": 2}
+_SCORE = {"softmax": 0, "sigmoid": 1}
 
 
 class SpgError(RuntimeError):
@@ -78,9 +85,35 @@ class RouteCandidate(ctypes.Structure):
                 ("factor", ctypes.c_double)]
 
 
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("a_rows", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("lda", ctypes.c_int64), ("ldw", ctypes.c_int64), ("stride_w", ctypes.c_int64), ("ldo", ctypes.c_int64),
+        ("experts", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("E", ctypes.c_int32), ("top", ctypes.c_int32), ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+        ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("logits_bf16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 # Exported symbols and their signatures (mirrors include/spg.h).
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 SIGNATURES = {
+    "quantize_block128": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_int, _P]),
+    "gemm_grouped": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.POINTER(GroupedDesc), _P]),
+    "spg_grouped_tile_rows": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), ctypes.c_int]),
+    "expert_route_workspace_bytes": (_SZ, [_I64, _I32]),
+    "expert_route": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P, _SZ, _P]),
+    "expert_sort": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "expert_route_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P]),
+    "expert_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _I64, _P]),
+    "expert_combine_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _P]),
     "spg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "quantize_rowwise": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _P]),
     "quantize_tensor_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -198,6 +231,54 @@ def quantize_block16(x: torch.Tensor, layout="row", single_launch=False):
     return q, bs, t
 
 
+def block128_scale_shape(R: int, K: int, tiling="row") -> tuple:
+    """Shape of quantize_block128's scale plane for one [R, K] matrix: row
+    groups [ceil(K/128), R], column groups [ceil(R/128), K], blocks
+    [ceil(R/128), ceil(K/128)]."""
+    gr, gk = (R + 127) // 128, (K + 127) // 128
+    return {"row": (gk, R), "column": (gr, K), "block": (gr, gk)}[tiling]
+
+
+def quantize_block128(x: torch.Tensor, tiling="row", out: torch.Tensor | None = None,
+                      scale: torch.Tensor | None = None):
+    """E4M3 with an fp32 scale per 128 elements: x bf16 [R, K] or [B, R, K] ->
+    (codes uint8 like x, scales fp32).  tiling "row": 1 x 128 (activations;
+    scales group-major [ceil(K/128), R]); "column": 128 x 1 (a K-major A, as
+    the weight-gradient product reads it; [ceil(R/128), K]); "block": 128 x
+    128 (weights; [ceil(R/128), ceil(K/128)])."""
+    _need(isinstance(x, torch.Tensor) and x.dtype == torch.bfloat16 and x.dim() in (2, 3),
+          "x must be a 2-D or 3-D bf16 tensor")
+    _need(tiling in _TILING, f"unknown tiling {tiling}")
+    _need(x.numel() == 0 or x.stride(-1) == 1, "x rows must be contiguous")
+    R, K = x.shape[-2:]
+    lead = tuple(x.shape[:-2])
+    B = lead[0] if lead else 1
+    _need(B >= 1, "x must hold at least one matrix")
+    _need(K % 16 == 0, "rows must be a multiple of 16 elements")
+    _need(R <= 1 or x.stride(-2) % 8 == 0 and x.stride(-2) >= K, "the row stride must be a multiple of 8, at least K")
+    _need(B == 1 or x.stride(0) % 8 == 0 and x.stride(0) >= (R - 1) * x.stride(-2) + K,
+          "matrices must not overlap, their stride a multiple of 8")
+    shape = lead + block128_scale_shape(R, K, tiling)
+    for name, t, want, dt in (("out", out, tuple(x.shape), torch.uint8), ("scale", scale, shape, torch.float32)):
+        _need(t is None or (isinstance(t, torch.Tensor) and t.device == x.device and t.dtype == dt
+                            and tuple(t.shape) == want), f"{name} must be {dt} {want} on {x.device}")
+    if out is not None:
+        _need((out.stride(-1) == 1 or K <= 1) and (R <= 1 or out.stride(-2) % 16 == 0 and out.stride(-2) >= K)
+              and (B == 1 or out.stride(0) % 16 == 0 and out.stride(0) >= (R - 1) * out.stride(-2) + K),
+              "out rows must be contiguous, 16-byte aligned and must not overlap")
+    _need(scale is None or scale.is_contiguous(), "scale must be contiguous")
+    _need(x.is_cuda, "x must be a CUDA tensor")
+    q = out if out is not None else torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    s = scale if scale is not None else torch.empty(shape, dtype=torch.float32, device=x.device)
+    if R > 0:
+        ldx, ldq = max(x.stride(-2), K) if R > 1 else K, max(q.stride(-2), K) if R > 1 else K
+        with torch.cuda.device(x.device):
+            _check(lib.quantize_block128(_ptr(x), B, R, K, ldx, x.stride(0) if B > 1 else 0, _ptr(q), ldq,
+                                         q.stride(0) if B > 1 else 0, _ptr(s), _TILING[tiling], _stream(x)),
+                   "quantize_block128")
+    return q, s
+
+
 # ---------------------------------------------------------------------------
 # GEMM
 # ---------------------------------------------------------------------------
@@ -288,7 +369,7 @@ def check_operands(A, sa, W, sw, fmt, epilogue, out=None, residual=None, tscale_
     bounds."""
     fmt = _FMT.get(fmt, fmt)
     epi = _EPI.get(epilogue, epilogue)
-    _need(fmt in (FMT_E4M3_ROW, FMT_E4M3_TENSOR, FMT_NVFP4), f"unknown format {fmt}")
+    _need(fmt in (FMT_E4M3_ROW, FMT_E4M3_TENSOR, FMT_NVFP4, FMT_E4M3_BLOCK128), f"unknown format {fmt}")
     _need(epi in (EPI_STORE, EPI_ADD, EPI_SWIGLU), f"unknown epilogue {epilogue}")
     _need(isinstance(A, torch.Tensor) and isinstance(W, torch.Tensor), "A and W must be tensors")
     _need(A.dtype == torch.uint8 and W.dtype == torch.uint8, "A and W must be uint8 code tensors")
@@ -319,6 +400,15 @@ def check_operands(A, sa, W, sw, fmt, epilogue, out=None, residual=None, tscale_
         _need(sa.dtype == torch.float32 and sw.dtype == torch.float32, "tensor scales must be fp32")
         _need(sa.is_contiguous() and sa.numel() == Ab, f"sa must hold {Ab} fp32 tensor scale(s)")
         _need(sw.is_contiguous() and sw.numel() == Wb, f"sw must hold {Wb} fp32 tensor scale(s)")
+    elif fmt == FMT_E4M3_BLOCK128:
+        _need(sa.dtype == torch.float32 and sw.dtype == torch.float32, "block scales must be fp32")
+        _need(epi != EPI_SWIGLU or N % 256 == 0, "block-scaled SwiGLU needs N to be a multiple of 256")
+        sa_shape = A.shape[:-2] + ((Kc + 127) // 128, M)
+        sw_shape = W.shape[:-2] + block128_scale_shape(W.shape[-2], W.shape[-1], "block")
+        _need(tuple(sa.shape) == tuple(sa_shape) and sa.is_contiguous(),
+              f"sa must be a contiguous {tuple(sa_shape)} plane")
+        _need(tuple(sw.shape) == tuple(sw_shape) and sw.is_contiguous(),
+              f"sw must be a contiguous {tuple(sw_shape)} plane")
     else:
         _need(not batched, "NVFP4 takes one product (2-D operands)")
         _need(sa.dtype == torch.uint8 and sw.dtype == torch.uint8, "NVFP4 block scales are uint8 E4M3 codes")
@@ -373,6 +463,11 @@ def gemm_scaled(A, sa, W, sw, epilogue="store", residual=None, fmt="e4m3_row",
     nvfp4: A uint8 [M,K/2], sa uint8 [M,K/16]; W [N,K/2], sw [N,K/16];
            tscale_a, tscale_w fp32 [1]; scale_layout "row" or "blocked" (both
            planes, as quantize_block16 wrote them)
+    e4m3_block128: A uint8 [M,K], sa fp32 [ceil(K/128),M]; W [N,K], sw fp32
+           [ceil(N/128),ceil(K/128)] ([B, ...] each when batched), as
+           quantize_block128 wrote them with tiling "row" (a K-major A:
+           "column") and "block" (a K-major W keeps the blocks of its stored
+           [K,N]: sw [ceil(K/128),ceil(N/128)]); "swiglu" needs N % 256 == 0
     clock_probe: optional int64 tensor of 4 elements on the same device; the
            main GEMM launch records its clock counters there (see
            spg_gemm_desc.clock_probe): shader clock in GHz =
@@ -510,6 +605,257 @@ def gemm_plan(M, N, K, fmt="e4m3_row", epilogue="store", batch=1, units=256) -> 
     p = Plan()
     _check(lib.spg_gemm_plan(ctypes.byref(d), epi, units, ctypes.byref(p)), "spg_gemm_plan")
     return {f: getattr(p, f) for f, _ in Plan._fields_}
+
+
+# ---------------------------------------------------------------------------
+# Experts: routing, one product per expert, the weighted sum
+# ---------------------------------------------------------------------------
+
+ExpertRoute = collections.namedtuple("ExpertRoute", "weights experts offsets rows slots")
+
+
+def _index(name, t, shape, dev):
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == dev and tuple(t.shape) == tuple(shape)
+          and t.is_contiguous(), f"{name} must be a contiguous int32 {tuple(shape)} tensor on {dev}")
+
+
+def _rows_ok(name, t, dt, dev):
+    _need(isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype == dt and t.device == dev,
+          f"{name} must be a 2-D {dt} tensor on {dev}")
+    _need(t.numel() == 0 or t.shape[1] == 1 or t.stride(1) == 1, f"rows of {name} must be contiguous")
+    _need(t.numel() == 0 or t.shape[0] == 1 or t.stride(0) >= t.shape[1], f"rows of {name} must not overlap")
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor; the row length where it has at most one row."""
+    return t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+
+
+def _grouped(A, sa, W, sw, offsets, epilogue, rows, out):
+    epi = _EPI.get(epilogue, epilogue)
+    _need(epi in (EPI_STORE, EPI_SWIGLU), "the epilogue of experts' products is store or swiglu")
+    _need(isinstance(A, torch.Tensor), "A must be a tensor")
+    dev = A.device
+    _rows_ok("A", A, torch.uint8, dev)
+    _need(isinstance(W, torch.Tensor) and W.dim() == 3 and W.dtype == torch.uint8 and W.device == dev,
+          f"W must be uint8 codes [experts, N, K] on {dev}")
+    E, N, K = W.shape
+    a_rows = A.shape[0]
+    _need(E >= 1 and A.shape[1] == K, "A and W disagree on K, or W holds no expert")
+    _need(K % 16 == 0, "K must be a multiple of 16")
+    _need(epi != EPI_SWIGLU or N % 256 == 0, "block-scaled SwiGLU needs N to be a multiple of 256")
+    _need(W.stride(2) == 1 or K <= 1, "rows of W must be contiguous")
+    for name, t, ld in (("A", A, _ld(A)), ("W", W, W.stride(1) if N > 1 else K)):
+        _need(ld % 16 == 0 and ld >= K and t.data_ptr() % 16 == 0, f"rows of {name} must be 16-byte aligned")
+    _need(E == 1 or N == 0 or W.stride(0) % 16 == 0 and
+          (W.stride(0) == 0 or W.stride(0) >= (N - 1) * (W.stride(1) if N > 1 else K) + K),
+          "experts' weights must be 16-byte aligned and must not overlap")
+    G = (K + 127) // 128
+    for name, t, want in (("sa", sa, (G, a_rows)), ("sw", sw, (E, (N + 127) // 128, G))):
+        _need(isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.device == dev and tuple(t.shape) == want
+              and t.is_contiguous(), f"{name} must be a contiguous fp32 {want} plane on {dev}")
+    _index("offsets", offsets, (E + 1,), dev)
+    R = a_rows
+    if rows is not None:
+        _need(isinstance(rows, torch.Tensor) and rows.dim() == 1, "rows must be a 1-D int32 tensor")
+        R = rows.shape[0]
+        _index("rows", rows, (R,), dev)
+    n_out = N // 2 if epi == EPI_SWIGLU else N
+    if out is not None:
+        _rows_ok("out", out, torch.bfloat16, dev)
+        _need(tuple(out.shape) == (R, n_out), f"out must have shape {(R, n_out)}")
+    d = GroupedDesc(R, a_rows, N, K, _ld(A), W.stride(1) if N > 1 else K, W.stride(0) if E > 1 else 0,
+                    n_out if out is None else _ld(out), E, 0)
+    return d, epi, n_out
+
+
+def gemm_grouped(A, sa, W, sw, offsets, epilogue="store", rows=None, out=None):
+    """One e4m3_block128 product per expert over rows grouped by expert: for
+    r in [offsets[e], offsets[e + 1]), out[r] = epilogue(A[rows[r]] W[e]^T)
+    (A[r] without rows), bf16 [R, N] ("store") or [R, N/2] ("swiglu").
+
+    A uint8 [T, K], sa fp32 [ceil(K/128), T] (quantize_block128 "row"); W uint8
+    [E, N, K], sw fp32 [E, ceil(N/128), ceil(K/128)] ("block"); offsets int32
+    [E + 1] and rows int32 [R] as expert_route returns them.  Rows of no
+    expert are left as they were (undefined in an output allocated here)."""
+    d, epi, n_out = _grouped(A, sa, W, sw, offsets, epilogue, rows, out)
+    _need(A.is_cuda, "operands must be CUDA tensors")
+    if out is None:
+        out = torch.empty((d.rows, n_out), dtype=torch.bfloat16, device=A.device)
+    if d.rows > 0 and n_out > 0:
+        with torch.cuda.device(A.device):
+            _check(lib.gemm_grouped(_ptr(out), _ptr(A), _ptr(sa), _ptr(W), _ptr(sw), _ptr(offsets), _ptr(rows), epi,
+                                    ctypes.byref(d), _stream(A)), "gemm_grouped")
+    return out
+
+
+def grouped_tile_rows(rows: int, experts: int, N: int, K: int, epilogue="store") -> int:
+    """Rows of the tiles gemm_grouped takes (16, 32, 128 or 256)."""
+    epi = _EPI.get(epilogue, epilogue)
+    d = GroupedDesc(rows, rows, N, K, K, K, N * K, N // 2 if epi == EPI_SWIGLU else N, experts, 0)
+    return lib.spg_grouped_tile_rows(ctypes.byref(d), epi)
+
+
+def expert_workspace(T: int, E: int, device="cuda"):
+    """A device workspace for the row order of T tokens over E experts, or
+    None when it needs none."""
+    n = lib.expert_route_workspace_bytes(T, E)
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def _route_desc(logits, top, score, groups, top_groups, renormalize, scale):
+    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16),
+          "logits must be a 2-D fp32 or bf16 tensor")
+    _rows_ok("logits", logits, logits.dtype, logits.device)
+    T, E = logits.shape
+    _need(score in _SCORE, f"unknown score {score}")
+    _need(1 <= top <= E, "top must be between 1 and the number of experts")
+    _need(1 <= top_groups <= groups and E % groups == 0, "groups must divide the experts, top_groups be 1 .. groups")
+    _need(math.isfinite(scale), "scale must be finite")
+    return RouteDesc(T, _ld(logits), E, top, groups, top_groups, _SCORE[score], int(bool(renormalize)),
+                     int(logits.dtype == torch.bfloat16), scale)
+
+
+def _order_ws(workspace, T, E, dev):
+    n = lib.expert_route_workspace_bytes(T, E)
+    if n == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
+    _need(isinstance(workspace, torch.Tensor) and workspace.device == dev and workspace.is_contiguous()
+          and workspace.numel() * workspace.element_size() >= n, f"the workspace must hold {n} bytes on {dev}")
+    return workspace, n
+
+
+def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, renormalize=True, scale=1.0,
+                 order=True, workspace=None):
+    """Experts and weights of each token, and the row order of the experts'
+    products, from logits [T, E] (fp32 or bf16): ExpertRoute(weights fp32 [T,
+    top], experts int32 [T, top], offsets int32 [E + 1], rows int32 [T top],
+    slots int32 [T, top]); the last three None with order=False.
+
+    p = softmax or sigmoid of the logits, c = p + bias (fp32 [E]); of `groups`
+    runs of consecutive experts, scored by their two largest c, the top_groups
+    best stay; experts are the `top` largest c among them, ties to the lowest
+    index; weights are scale p / sum p (renormalize) or scale p.  Logits of
+    -inf mask an expert: places that no expert is left for hold expert -1,
+    weight 0, slot -1."""
+    d = _route_desc(logits, top, score, groups, top_groups, renormalize, scale)
+    dev = logits.device
+    _need(bias is None or (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32 and bias.device == dev
+                           and tuple(bias.shape) == (d.E,) and bias.is_contiguous()),
+          f"bias must be a contiguous fp32 [{d.E}] tensor on {dev}")
+    _need(logits.is_cuda, "logits must be a CUDA tensor")
+    T = d.T
+    ws, nws = _order_ws(workspace, T, d.E, dev) if order else (None, 0)
+    weights = torch.empty((T, top), dtype=torch.float32, device=dev)
+    # one allocation for the integers
+    ints = torch.empty((T * top * (3 if order else 1) + (d.E + 1 if order else 0),), dtype=torch.int32, device=dev)
+    n = T * top
+    experts = ints[:n].view(T, top)
+    rows, slots, offsets = (ints[n:2 * n], ints[2 * n:3 * n].view(T, top), ints[3 * n:]) if order else (None,) * 3
+    with torch.cuda.device(dev):
+        # an empty tensor's pointer may be null: rows and slots of no token
+        _check(lib.expert_route(_ptr(logits), _ptr(bias), _ptr(weights), _ptr(experts), _ptr(offsets),
+                                (_ptr(rows) or _ptr(offsets)) if order else None,
+                                (_ptr(slots) or _ptr(offsets)) if order else None,
+                                ctypes.byref(d), _ptr(ws), nws, _stream(logits)), "expert_route")
+    return ExpertRoute(weights, experts, offsets, rows, slots)
+
+
+def expert_sort(experts, n_experts, workspace=None):
+    """(offsets, rows, slots) of experts int32 [T, top] chosen elsewhere, as
+    expert_route gives them; values outside [0, n_experts) are no expert."""
+    _need(isinstance(experts, torch.Tensor) and experts.dim() == 2, "experts must be a 2-D int32 tensor")
+    T, top = experts.shape
+    dev = experts.device
+    _index("experts", experts, (T, top), dev)
+    _need(top >= 1 and n_experts >= 1, "at least one expert")
+    _need(experts.is_cuda, "experts must be a CUDA tensor")
+    ws, nws = _order_ws(workspace, T, n_experts, dev)
+    offsets = torch.empty((n_experts + 1,), dtype=torch.int32, device=dev)
+    rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
+    slots = torch.empty((T, top), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.expert_sort(_ptr(experts), T, top, n_experts, _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(ws), nws,
+                               _stream(experts)), "expert_sort")
+    return offsets, rows, slots
+
+
+def expert_route_backward(grad_weights, logits, experts, score="softmax", renormalize=True, scale=1.0):
+    """The gradient of the logits ([T, E], their type) from that of
+    expert_route's weights (fp32 [T, top]), for the same logits, options and
+    the experts it chose."""
+    _need(isinstance(experts, torch.Tensor) and experts.dim() == 2, "experts must be a 2-D int32 tensor")
+    d = _route_desc(logits, experts.shape[1], score, 1, 1, renormalize, scale)
+    dev, T = logits.device, d.T
+    _index("experts", experts, (T, d.top), dev)
+    _need(isinstance(grad_weights, torch.Tensor) and grad_weights.dtype == torch.float32 and grad_weights.device == dev
+          and tuple(grad_weights.shape) == (T, d.top) and grad_weights.is_contiguous(),
+          f"grad_weights must be a contiguous fp32 {(T, d.top)} tensor on {dev}")
+    _need(logits.is_cuda, "logits must be a CUDA tensor")
+    grad = torch.empty((T, d.E), dtype=logits.dtype, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.expert_route_backward(_ptr(grad_weights), _ptr(logits), _ptr(experts), _ptr(grad), ctypes.byref(d),
+                                         _stream(logits)), "expert_route_backward")
+    return grad
+
+
+def _combine_args(y, weights, slots, T):
+    _need(isinstance(y, torch.Tensor), "y must be a tensor")
+    dev = y.device
+    _rows_ok("y", y, torch.bfloat16, dev)
+    _need(isinstance(slots, torch.Tensor) and slots.dim() == 2 and slots.shape[1] >= 1, "slots must be int32 [T, top]")
+    _need(T is None or slots.shape[0] == T, "slots and the other operands disagree on the tokens")
+    _index("slots", slots, slots.shape, dev)
+    _need(isinstance(weights, torch.Tensor) and weights.dtype == torch.float32 and weights.device == dev
+          and weights.shape == slots.shape and weights.is_contiguous(),
+          f"weights must be a contiguous fp32 {tuple(slots.shape)} tensor on {dev}")
+    return dev
+
+
+def expert_combine(y, weights, slots, residual=None, out=None):
+    """out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]] in bf16 [T, H]
+    (fp32 sums, one rounding): y bf16 [R, H] the experts' rows, weights and
+    slots of expert_route; residual bf16 [T, H], which may be out itself."""
+    dev = _combine_args(y, weights, slots, None)
+    (T, top), (R, H) = slots.shape, y.shape
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            _rows_ok(name, t, torch.bfloat16, dev)
+            _need(tuple(t.shape) == (T, H), f"{name} must have shape {(T, H)}")
+    _need(y.is_cuda, "y must be a CUDA tensor")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.expert_combine(_ptr(y), R, _ld(y), _ptr(weights), _ptr(slots), T, top, H, _ptr(residual),
+                                  _ld(residual) if residual is not None else 0, _ptr(out), _ld(out), _stream(y)),
+               "expert_combine")
+    return out
+
+
+def expert_combine_backward(grad_out, y, weights, slots, grad_y=None):
+    """(grad_y bf16 [R, H], grad_weights fp32 [T, top]) of expert_combine from
+    grad_out bf16 [T, H] (which is the residual's gradient as it is).  Rows of
+    grad_y that no slot names are left as they were (undefined in one
+    allocated here); the slots must be distinct, as expert_route's are."""
+    _need(isinstance(grad_out, torch.Tensor) and grad_out.dim() == 2, "grad_out must be a 2-D bf16 tensor")
+    dev = _combine_args(y, weights, slots, grad_out.shape[0])
+    (T, top), (R, H) = slots.shape, y.shape
+    _rows_ok("grad_out", grad_out, torch.bfloat16, dev)
+    _need(grad_out.shape[1] == H, f"grad_out must have shape {(T, H)}")
+    if grad_y is not None:
+        _rows_ok("grad_y", grad_y, torch.bfloat16, dev)
+        _need(tuple(grad_y.shape) == (R, H), f"grad_y must have shape {(R, H)}")
+    _need(y.is_cuda, "y must be a CUDA tensor")
+    if grad_y is None:
+        grad_y = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
+    grad_weights = torch.empty((T, top), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib.expert_combine_backward(_ptr(grad_out), _ld(grad_out), _ptr(y), R, _ld(y), _ptr(weights),
+                                           _ptr(slots), T, top, H, _ptr(grad_y), _ld(grad_y), _ptr(grad_weights),
+                                           _stream(y)), "expert_combine_backward")
+    return grad_y, grad_weights
 
 
 def route_cost(bm, bn, per_unit, factor, M, N, batch, units) -> float:

@@ -6,13 +6,14 @@
 #include <math.h>
 #include <string.h>
 
-#include "spg_common.h"
+#include "spg_gemm_block.h"
 
 using namespace spg;
 
 namespace {
 
 constexpr int64_t kTile = 256;
+constexpr int64_t kMaxScaleWords = INT64_C(1) << 29;   // floats within a 31-bit byte range
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
@@ -35,7 +36,8 @@ int64_t n_out_of(const spg_gemm_desc *d, int epi) { return epi == SPG_EPI_SWIGLU
 int validate_desc(const spg_gemm_desc *d, int epi)
 {
     if (!d) return SPG_EINVAL;
-    if (d->format != SPG_FMT_E4M3_ROW && d->format != SPG_FMT_E4M3_TENSOR && d->format != SPG_FMT_NVFP4)
+    if (d->format != SPG_FMT_E4M3_ROW && d->format != SPG_FMT_E4M3_TENSOR && d->format != SPG_FMT_NVFP4 &&
+        d->format != SPG_FMT_E4M3_BLOCK128)
         return SPG_EINVAL;
     if (epi != SPG_EPI_STORE && epi != SPG_EPI_ADD && epi != SPG_EPI_SWIGLU) return SPG_EINVAL;
     if (d->M < 0 || d->N < 0 || d->K < 0 || d->batch < 1) return SPG_EINVAL;
@@ -63,6 +65,14 @@ int validate_desc(const spg_gemm_desc *d, int epi)
             const int64_t blocks = cdiv(d->K, 64) * (cdiv(d->M, 64) + cdiv(d->N, 64)) * d->batch;
             if (blocks >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
         }
+    }
+    if (d->format == SPG_FMT_E4M3_BLOCK128) {
+        // the up rows' scale blocks start where the up rows do
+        if (epi == SPG_EPI_SWIGLU && (d->N % 256)) return SPG_EINVAL;
+        // scale planes are addressed with 32-bit byte offsets
+        if (d->M >= kMaxScaleWords || d->N >= kMaxScaleWords || d->K >= kMaxScaleWords ||
+            cdiv(d->N, 128) * cdiv(d->K, 128) >= kMaxScaleWords)
+            return SPG_EUNSUPPORTED;
     }
     if (d->layout < 0 || d->layout > (SPG_LAYOUT_A_KMAJOR | SPG_LAYOUT_W_KMAJOR)) return SPG_EINVAL;
     if ((d->lda & 15) || (d->ldw & 15)) return SPG_EINVAL;
@@ -189,10 +199,49 @@ bool narrow_route(const spg_gemm_desc *d, int64_t nout, bool aligned_scales = tr
     return true;
 }
 
+// Block-scaled FP8 (kernels 4 - 6): decode width as for the other formats,
+// else tiles of 128 or 256 rows, split along K when they leave compute units
+// idle.
+void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
+{
+    const int64_t nout = n_out_of(d, epi);
+    p->tail_split = 1;
+    p->tail_bm = (int32_t)kTile;
+    p->bk = 128;
+    p->split_k = 1;
+    if (narrow_route(d, nout)) {
+        p->kernel = 6;
+        p->bm = d->M <= 16 ? 16 : 32;
+        p->bn = narrow_cols(epi);
+        p->tiles = p->workgroups = d->batch * cdiv(nout, p->bn);
+        return;
+    }
+    p->bn = (int32_t)kTile;
+    const int64_t tiles_n = epi == SPG_EPI_SWIGLU ? cdiv(nout, kTile / 2) : cdiv(d->N, kTile);
+    const int64_t t256 = d->batch * cdiv(d->M, 256) * tiles_n, t128 = d->batch * cdiv(d->M, 128) * tiles_n;
+    const bool half = t128 < (INT64_C(1) << 31) && 0.6 * (double)cdiv(t128, units) < (double)cdiv(t256, units);
+    p->kernel = half ? 5 : 4;
+    p->bm = half ? 128 : 256;
+    p->tiles = half ? t128 : t256;
+    if (p->tiles > 0 && d->K > 0) {
+        double best = (double)cdiv(p->tiles, units);
+        for (int s = 2; s <= 8 && d->K / s >= 1024; ++s) {
+            if ((int64_t)(s - 1) * (cdiv(cdiv(d->K, s), 128) * 128) >= d->K) continue;   // a slice would be empty
+            const double cost = (double)cdiv(p->tiles * s, units) / s;
+            if (p->tiles * 2 <= units && cost < best - 1e-9) {
+                best = cost;
+                p->split_k = s;
+            }
+        }
+    }
+    p->workgroups = p->tiles * p->split_k;
+}
+
 void make_plan(const spg_gemm_desc *d, int epi, int units, spg_plan *p, bool aligned_scales = true)
 {
     memset(p, 0, sizeof(*p));
     const int64_t nout = n_out_of(d, epi);
+    if (d->format == SPG_FMT_E4M3_BLOCK128) return make_plan_block(d, epi, units, p);
     if (narrow_route(d, nout, aligned_scales)) {
         p->kernel = 3;
         p->bm = d->M <= 16 ? 16 : 32;
@@ -315,7 +364,7 @@ size_t transpose_bytes(const spg_gemm_desc *d, size_t *a_bytes)
 
 size_t plan_workspace(const spg_plan *p)
 {
-    if (p->split_k > 1) return (size_t)p->tiles * p->split_k * kTile * kTile * sizeof(float);
+    if (p->split_k > 1) return (size_t)p->tiles * p->split_k * (size_t)p->bm * kTile * sizeof(float);
     if (p->tail_split > 1) return (size_t)p->tail_tiles * p->tail_split * kTile * kTile * sizeof(float);
     return 0;
 }
@@ -419,6 +468,37 @@ int validate_split(const spg_out_split *sp, const spg_gemm_desc *d, int64_t nout
         for (int t = s + 1; t < sp->count; ++t)
             if (ext[s].o0 < ext[t].o1 && ext[t].o0 < ext[s].o1) return SPG_EINVAL;
     return SPG_OK;
+}
+
+// The launches of a block-scaled product, from the generic arguments.
+static int run_block(const spg_gemm_desc *d, const spg_plan &p, const GemmArgs &g, hipStream_t s)
+{
+    BlockArgs a;
+    memset(&a, 0, sizeof(a));
+    a.g = g;
+    const int64_t groups = cdiv(d->K, 128), blocks = cdiv(d->N, 128);
+    a.a_rows = d->M;
+    a.groups = (int32_t)groups;
+    a.sw_words = (int32_t)(blocks * groups);
+    // W's scales lie as W is stored
+    a.sw_rs = (int32_t)((d->layout & SPG_LAYOUT_W_KMAJOR) ? 1 : groups);
+    a.sw_gs = (int32_t)((d->layout & SPG_LAYOUT_W_KMAJOR) ? blocks : 1);
+    a.g.sa_bstride = groups * d->M;
+    a.g.sw_bstride = blocks * groups;
+    a.g.clocks = d->clock_probe;
+    if (p.kernel == 6) {
+        a.g.tiles_m = 1;
+        a.g.tiles_n = cdiv(n_out_of(d, g.epilogue), p.bn);
+        return launch_gemm_block_narrow(a, p.bm, p.workgroups, s) == hipSuccess ? SPG_OK : SPG_EHIP;
+    }
+    a.g.tiles_m = cdiv(d->M, p.bm);
+    a.g.div_per = make_fastdiv((uint32_t)(a.g.tiles_m * a.g.tiles_n));
+    a.g.div_gm_last = make_fastdiv(a.g.tiles_m % 8 ? (uint32_t)(a.g.tiles_m % 8) : 8u);
+    a.g.tile_begin = 0;
+    a.g.tile_count = p.tiles;
+    hipError_t e = launch_gemm_block_tiles(a, p.bm, p.workgroups, s);
+    if (e == hipSuccess && p.split_k > 1) e = launch_gemm_block_reduce(a, p.bm, s);
+    return e == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 
 SPG_EXPORT int gemm_scaled(void *out, const void *A, const void *sa, const void *W, const void *sw,
@@ -565,6 +645,7 @@ SPG_EXPORT int gemm_scaled(void *out, const void *A, const void *sa, const void 
     g.div_span = make_fastdiv((uint32_t)(8 * g.tiles_n));
     g.div_gm_last = make_fastdiv(g.tiles_m % 8 ? (uint32_t)(g.tiles_m % 8) : 8u);
     if (p.split_k > 1) g.partials = (float *)((uint8_t *)ws + t_bytes);
+    if (d->format == SPG_FMT_E4M3_BLOCK128) return run_block(d, p, g, s);
     if (p.kernel == 3) {
         g.tiles_m = 1;
         g.tiles_n = cdiv(nout, narrow_cols(epilogue));

@@ -1,0 +1,389 @@
+// Exported C ABI (include/spg.h) of the block-128 quantizer and of the
+// experts' layer: argument validation and launches.
+#include <math.h>
+#include <string.h>
+
+#include "spg_experts.h"
+#include "spg_gemm_block.h"
+
+using namespace spg;
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+bool aligned2(const void *p) { return ((uintptr_t)p & 1u) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxWords = INT64_C(1) << 29;        // floats within a 31-bit byte range
+constexpr int64_t kMaxGrid = INT64_C(1) << 31;
+constexpr int64_t kMaxGridYZ = 65535;
+
+// [a0, a1) and [b0, b1) share a byte.
+bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes)
+{
+    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+int64_t extent(int64_t rows, int64_t ld, int64_t cols) { return rows > 0 ? (rows - 1) * ld + cols : 0; }
+
+}  // namespace
+
+SPG_EXPORT int quantize_block128(const void *x, int64_t batch, int64_t rows, int64_t K, int64_t ldx, int64_t bstride,
+                                 uint8_t *q, int64_t ldq, int64_t qbstride, float *scale, int tiling, void *stream)
+{
+    if (tiling != SPG_BLOCK_ROW && tiling != SPG_BLOCK_COLUMN && tiling != SPG_BLOCK_BLOCK) return SPG_EINVAL;
+    if (batch < 1 || rows < 0 || K < 0 || (K % 16)) return SPG_EINVAL;
+    if (rows == 0) return SPG_OK;
+    if (K == 0) return SPG_EINVAL;                     // a scale of an empty row is undefined
+    if (!x || !q || !scale) return SPG_EINVAL;
+    if (ldx < K || ldq < K || (ldx & 7) || (ldq & 15)) return SPG_EINVAL;
+    if (batch > 1 && (bstride < extent(rows, ldx, K) || (bstride & 7) || qbstride < extent(rows, ldq, K) ||
+                      (qbstride & 15)))
+        return SPG_EINVAL;
+    if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return SPG_EINVAL;
+    if (batch > kMaxGridYZ) return SPG_EUNSUPPORTED;
+    if (tiling == SPG_BLOCK_ROW ? (cdiv(rows, 16) >= kMaxGrid || cdiv(K, 512) > kMaxGridYZ)
+                                : (cdiv(K, 128) >= kMaxGrid || cdiv(rows, 128) > kMaxGridYZ))
+        return SPG_EUNSUPPORTED;
+    const hipError_t e = launch_quantize_block128((const uint16_t *)x, batch, rows, K, ldx, bstride, q, ldq, qbstride,
+                                                  scale, tiling, (hipStream_t)stream);
+    return e == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// grouped product
+// ---------------------------------------------------------------------------
+
+namespace {
+
+int64_t grouped_nout(const spg_grouped_desc *d, int epi) { return epi == SPG_EPI_SWIGLU ? d->N / 2 : d->N; }
+
+// Tile rows from the mean rows of an expert; tiles of 16 and 32 rows stream
+// the weights (decode), the larger ones feed the matrix cores.
+int tile_rows(const spg_grouped_desc *d)
+{
+    const double mean = (double)d->rows / d->experts;
+    if (mean <= 12) return 16;
+    if (mean <= 28) return 32;
+    return mean <= 160 ? 128 : 256;
+}
+
+// Upper bound of the row tiles: every expert adds at most one partial tile,
+// and no tile is empty.
+int64_t most_tiles(const spg_grouped_desc *d, int bm)
+{
+    const int64_t most = d->rows / bm + d->experts;
+    return most < d->rows ? most : d->rows;
+}
+
+int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
+{
+    return bm <= 32 ? cdiv(grouped_nout(d, epi), narrow_cols(epi))
+                    : (epi == SPG_EPI_SWIGLU ? cdiv(d->N / 2, 128) : cdiv(d->N, 256));
+}
+
+int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
+{
+    if (!d) return SPG_EINVAL;
+    if (epi != SPG_EPI_STORE && epi != SPG_EPI_ADD && epi != SPG_EPI_SWIGLU) return SPG_EINVAL;
+    if (epi == SPG_EPI_ADD) return SPG_EUNSUPPORTED;
+    if (d->rows < 0 || d->a_rows < 0 || d->N < 0 || d->K < 0 || (d->K % 16)) return SPG_EINVAL;
+    if (d->experts < 1) return SPG_EINVAL;
+    if (d->experts > 65536) return SPG_EUNSUPPORTED;
+    if (epi == SPG_EPI_SWIGLU && (d->N % 256)) return SPG_EINVAL;
+    if (!indexed && d->a_rows < d->rows) return SPG_EINVAL;
+    if (d->lda < d->K || d->ldw < d->K || (d->lda & 15) || (d->ldw & 15)) return SPG_EINVAL;
+    if (d->lda > (INT64_C(1) << 23) || d->ldw > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
+    if (d->stride_w < 0 || (d->stride_w & 15)) return SPG_EINVAL;
+    if (d->experts > 1 && d->stride_w != 0 && d->stride_w < extent(d->N, d->ldw, d->K)) return SPG_EINVAL;
+    if (d->ldo < grouped_nout(d, epi)) return SPG_EINVAL;
+    if (d->ldo >= (INT64_C(1) << 26)) return SPG_EUNSUPPORTED;
+    if (d->rows >= kMaxWords || d->a_rows >= kMaxWords || d->N >= kMaxWords || d->K >= kMaxWords ||
+        cdiv(d->N, 128) * cdiv(d->K, 128) >= kMaxWords)
+        return SPG_EUNSUPPORTED;
+    if (indexed && d->a_rows * d->lda >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
+    const int bm = tile_rows(d);
+    if (most_tiles(d, bm) * grouped_columns(d, epi, bm) >= kMaxGrid) return SPG_EUNSUPPORTED;
+    return SPG_OK;
+}
+
+}  // namespace
+
+SPG_EXPORT int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue)
+{
+    return validate_grouped(d, epilogue, false) == SPG_OK ? tile_rows(d) : 0;
+}
+
+SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const float *sw,
+                            const int32_t *offsets, const int32_t *row_index, int epilogue, const spg_grouped_desc *d,
+                            void *stream)
+{
+    const int v = validate_grouped(d, epilogue, row_index != nullptr);
+    if (v != SPG_OK) return v;
+    const int64_t nout = grouped_nout(d, epilogue);
+    if (d->rows == 0 || nout == 0) return SPG_OK;
+    if (!out || !A || !sa || !W || !sw || !offsets) return SPG_EINVAL;
+    if (!aligned16(A) || !aligned16(W) || !aligned2(out) || !aligned4(sa) || !aligned4(sw) || !aligned4(offsets) ||
+        !aligned4(row_index))
+        return SPG_EINVAL;
+    const int64_t groups = cdiv(d->K, 128), blocks = cdiv(d->N, 128), E = d->experts;
+    const int64_t obytes = 2 * extent(d->rows, d->ldo, nout);
+    if (overlap(out, obytes, A, extent(d->a_rows, d->lda, d->K)) ||
+        overlap(out, obytes, W, (E - 1) * d->stride_w + extent(d->N, d->ldw, d->K)) ||
+        overlap(out, obytes, sa, 4 * groups * d->a_rows) || overlap(out, obytes, sw, 4 * E * blocks * groups) ||
+        overlap(out, obytes, offsets, 4 * (E + 1)) || (row_index && overlap(out, obytes, row_index, 4 * d->rows)))
+        return SPG_EINVAL;
+    BlockArgs a;
+    memset(&a, 0, sizeof(a));
+    GemmArgs &g = a.g;
+    g.out = out;
+    g.A = (const uint8_t *)A;
+    g.W = (const uint8_t *)W;
+    g.sa = sa;
+    g.sw = sw;
+    g.M = d->rows;
+    g.N = d->N;
+    g.K = d->K;
+    g.batch = 1;
+    g.lda = d->lda;
+    g.ldw = d->ldw;
+    g.ldo = d->ldo;
+    g.stride_w = d->stride_w;
+    g.sw_bstride = blocks * groups;
+    g.format = SPG_FMT_E4M3_BLOCK128;
+    g.epilogue = epilogue;
+    g.split_k = 1;
+    a.a_rows = d->a_rows;
+    a.groups = (int32_t)groups;
+    a.sw_words = (int32_t)(blocks * groups);
+    a.sw_rs = (int32_t)groups;
+    a.sw_gs = 1;
+    a.offsets = offsets;
+    a.row_index = row_index;
+    a.experts = d->experts;
+    const int bm = tile_rows(d);
+    g.tiles_n = grouped_columns(d, epilogue, bm);
+    g.div_per = make_fastdiv((uint32_t)g.tiles_n);
+    const int64_t workgroups = most_tiles(d, bm) * g.tiles_n;
+    const hipError_t e = bm <= 32 ? launch_gemm_block_narrow(a, bm, workgroups, (hipStream_t)stream)
+                                  : launch_gemm_block_tiles(a, bm, workgroups, (hipStream_t)stream);
+    return e == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// routing
+// ---------------------------------------------------------------------------
+
+namespace {
+
+int validate_route(const spg_route_desc *d)
+{
+    if (!d) return SPG_EINVAL;
+    if (d->T < 0 || d->E < 1 || d->top < 1 || d->top > d->E || d->ld < d->E) return SPG_EINVAL;
+    if (d->groups < 1 || d->top_groups < 1 || d->top_groups > d->groups || d->E % d->groups) return SPG_EINVAL;
+    if (d->score != SPG_SCORE_SOFTMAX && d->score != SPG_SCORE_SIGMOID) return SPG_EINVAL;
+    if (!isfinite(d->scale)) return SPG_EINVAL;
+    if (d->E > kRouteMaxExperts || d->top > kRouteMaxTop || d->groups > kRouteMaxGroups) return SPG_EUNSUPPORTED;
+    if (d->T >= kMaxGrid / d->top) return SPG_EUNSUPPORTED;
+    return SPG_OK;
+}
+
+// The counts of every chunk; none for what one workgroup orders.
+size_t route_ws(int64_t T, int32_t E)
+{
+    return T <= kRouteOneLaunch ? 0 : (size_t)cdiv(T, route_chunk(T)) * (size_t)E * sizeof(int32_t);
+}
+
+RouteArgs route_args(const spg_route_desc *d)
+{
+    RouteArgs a;
+    memset(&a, 0, sizeof(a));
+    a.ld = d->ld;
+    a.T = d->T;
+    a.E = d->E;
+    a.top = d->top;
+    a.groups = d->groups;
+    a.top_groups = d->top_groups;
+    a.score = d->score;
+    a.bf16 = d->logits_bf16 != 0;
+    a.renorm = d->renormalize != 0;
+    a.scale = d->scale;
+    a.chunk = (int32_t)route_chunk(d->T);
+    a.chunks = (int32_t)cdiv(d->T, a.chunk);
+    a.div_top = make_fastdiv((uint32_t)d->top);
+    a.div_group = make_fastdiv((uint32_t)(d->E / d->groups));
+    return a;
+}
+
+}  // namespace
+
+SPG_EXPORT size_t expert_route_workspace_bytes(int64_t T, int32_t E)
+{
+    if (T <= 0 || E < 1 || E > kRouteMaxExperts || T >= kMaxGrid) return 0;
+    return route_ws(T, E);
+}
+
+SPG_EXPORT int expert_route(const void *logits, const float *bias, float *weights, int32_t *experts, int32_t *offsets,
+                            int32_t *rows, int32_t *slots, const spg_route_desc *d, void *ws, size_t ws_bytes,
+                            void *stream)
+{
+    const int v = validate_route(d);
+    if (v != SPG_OK) return v;
+    const bool order = offsets || rows || slots;
+    if (order && (!offsets || !rows || !slots)) return SPG_EINVAL;
+    if (d->T > 0) {
+        if (!logits || !weights || !experts) return SPG_EINVAL;
+        if (d->logits_bf16 ? !aligned2(logits) : !aligned4(logits)) return SPG_EINVAL;
+    }
+    if (!aligned4(bias) || !aligned4(weights) || !aligned4(experts) || !aligned4(offsets) || !aligned4(rows) ||
+        !aligned4(slots))
+        return SPG_EINVAL;
+    RouteArgs a = route_args(d);
+    a.logits = logits;
+    a.bias = bias;
+    a.weights = weights;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.slots = slots;
+    // no token: the row order is that of no rows
+    if (d->T == 0 && !order) return SPG_OK;
+    if (order && route_ws(d->T, d->E) > 0) {
+        if (!ws || ws_bytes < route_ws(d->T, d->E) || !aligned4(ws)) return SPG_EWORKSPACE;
+        a.hist = (int32_t *)ws;
+    }
+    return launch_expert_route(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+SPG_EXPORT int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32_t E, int32_t *offsets, int32_t *rows,
+                           int32_t *slots, void *ws, size_t ws_bytes, void *stream)
+{
+    if (T < 0 || top < 1 || E < 1) return SPG_EINVAL;
+    if (E > kRouteMaxExperts) return SPG_EUNSUPPORTED;
+    if (T >= kMaxGrid / top) return SPG_EUNSUPPORTED;
+    if (!offsets || (T > 0 && (!experts || !rows || !slots))) return SPG_EINVAL;
+    if (!aligned4(experts) || !aligned4(offsets) || !aligned4(rows) || !aligned4(slots)) return SPG_EINVAL;
+    if (route_ws(T, E) > 0 && (!ws || ws_bytes < route_ws(T, E) || !aligned4(ws))) return SPG_EWORKSPACE;
+    spg_route_desc d;
+    memset(&d, 0, sizeof(d));
+    d.T = T;
+    d.E = E;
+    d.top = top;
+    d.groups = d.top_groups = 1;
+    RouteArgs a = route_args(&d);
+    a.experts = (int32_t *)experts;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.slots = slots;
+    a.hist = (int32_t *)ws;
+    return launch_expert_sort(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+SPG_EXPORT int expert_route_backward(const float *grad_weights, const void *logits, const int32_t *experts,
+                                     void *grad_logits, const spg_route_desc *d, void *stream)
+{
+    const int v = validate_route(d);
+    if (v != SPG_OK) return v;
+    if (d->T == 0) return SPG_OK;
+    if (!grad_weights || !logits || !experts || !grad_logits) return SPG_EINVAL;
+    if (!aligned4(grad_weights) || !aligned4(experts)) return SPG_EINVAL;
+    if (d->logits_bf16 ? !aligned2(logits) || !aligned2(grad_logits) : !aligned4(logits) || !aligned4(grad_logits))
+        return SPG_EINVAL;
+    const int64_t size = d->logits_bf16 ? 2 : 4;
+    if (overlap(grad_logits, size * d->T * d->E, logits, size * extent(d->T, d->ld, d->E))) return SPG_EINVAL;
+    RouteArgs a = route_args(d);
+    a.logits = logits;
+    a.grad = grad_weights;
+    a.experts = (int32_t *)experts;
+    a.grad_logits = grad_logits;
+    return launch_expert_route_backward(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// combine
+// ---------------------------------------------------------------------------
+
+namespace {
+
+int validate_combine(int64_t T, int64_t R, int32_t top, int64_t H)
+{
+    if (T < 0 || R < 0 || H < 0 || top < 1) return SPG_EINVAL;
+    if (top > kRouteMaxTop) return SPG_EUNSUPPORTED;
+    if (T >= kMaxGrid / top || R >= kMaxGrid || H >= kMaxGridYZ * 256) return SPG_EUNSUPPORTED;
+    return SPG_OK;
+}
+
+}  // namespace
+
+SPG_EXPORT int expert_combine(const void *y, int64_t R, int64_t ldy, const float *weights, const int32_t *slots,
+                              int64_t T, int32_t top, int64_t H, const void *residual, int64_t ldr, void *out,
+                              int64_t ldo, void *stream)
+{
+    const int v = validate_combine(T, R, top, H);
+    if (v != SPG_OK) return v;
+    if (ldy < H || ldo < H || (residual && ldr < H)) return SPG_EINVAL;
+    if (T == 0 || H == 0) return SPG_OK;
+    if ((R > 0 && !y) || !weights || !slots || !out) return SPG_EINVAL;
+    if (!aligned2(y) || !aligned2(residual) || !aligned2(out) || !aligned4(weights) || !aligned4(slots))
+        return SPG_EINVAL;
+    const int64_t obytes = 2 * extent(T, ldo, H);
+    if (overlap(out, obytes, y, 2 * extent(R, ldy, H)) || overlap(out, obytes, weights, 4 * T * top) ||
+        overlap(out, obytes, slots, 4 * T * top))
+        return SPG_EINVAL;
+    if (residual && overlap(out, obytes, residual, 2 * extent(T, ldr, H)) && !(residual == out && ldr == ldo))
+        return SPG_EINVAL;
+    CombineArgs a;
+    memset(&a, 0, sizeof(a));
+    a.y = (const uint16_t *)y;
+    a.weights = weights;
+    a.slots = slots;
+    a.residual = (const uint16_t *)residual;
+    a.out = (uint16_t *)out;
+    a.T = T;
+    a.R = R;
+    a.H = H;
+    a.ldy = ldy;
+    a.ldr = ldr;
+    a.ldo = ldo;
+    a.top = top;
+    return launch_expert_combine(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+SPG_EXPORT int expert_combine_backward(const void *grad_out, int64_t ldg, const void *y, int64_t R, int64_t ldy,
+                                       const float *weights, const int32_t *slots, int64_t T, int32_t top, int64_t H,
+                                       void *grad_y, int64_t ldgy, float *grad_weights, void *stream)
+{
+    const int v = validate_combine(T, R, top, H);
+    if (v != SPG_OK) return v;
+    if (ldg < H || ldy < H || ldgy < H) return SPG_EINVAL;
+    if (T == 0) return SPG_OK;
+    if (!weights || !slots || !grad_weights) return SPG_EINVAL;
+    if (H > 0 && (!grad_out || (R > 0 && (!y || !grad_y)))) return SPG_EINVAL;
+    if (!aligned2(grad_out) || !aligned2(y) || !aligned2(grad_y) || !aligned4(weights) || !aligned4(slots) ||
+        !aligned4(grad_weights))
+        return SPG_EINVAL;
+    const int64_t gbytes = 2 * extent(R, ldgy, H), wbytes = 4 * T * top;
+    if (overlap(grad_y, gbytes, y, 2 * extent(R, ldy, H)) || overlap(grad_y, gbytes, grad_out, 2 * extent(T, ldg, H)) ||
+        overlap(grad_y, gbytes, weights, wbytes) || overlap(grad_y, gbytes, slots, wbytes) ||
+        overlap(grad_y, gbytes, grad_weights, wbytes) || overlap(grad_weights, wbytes, weights, wbytes) ||
+        overlap(grad_weights, wbytes, slots, wbytes) || overlap(grad_weights, wbytes, y, 2 * extent(R, ldy, H)) ||
+        overlap(grad_weights, wbytes, grad_out, 2 * extent(T, ldg, H)))
+        return SPG_EINVAL;
+    CombineArgs a;
+    memset(&a, 0, sizeof(a));
+    a.y = (const uint16_t *)y;
+    a.weights = weights;
+    a.slots = slots;
+    a.grad = (const uint16_t *)grad_out;
+    a.out = (uint16_t *)grad_y;
+    a.grad_weights = grad_weights;
+    a.T = T;
+    a.R = R;
+    a.H = H;
+    a.ldy = ldy;
+    a.ldr = ldg;
+    a.ldo = ldgy;
+    a.top = top;
+    return launch_expert_combine_backward(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
+}
