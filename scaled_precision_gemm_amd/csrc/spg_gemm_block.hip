@@ -2,21 +2,23 @@
 // spg_gemm_block_common.h for the arithmetic).
 //
 // Design for CDNA4:
-//  * Tiles of BM x 256 (BM = 256 or 128 token rows, 256 weight rows), waves
-//    2 (weight halves) x BM / 64 (token strips): each wave holds 64 tokens x
-//    128 weight rows = 2 x 4 blocks of v_mfma_f32_32x32x64_f8f6f4, 128
-//    accumulators per lane.  With BM = 256 that is two waves per SIMD, so one
-//    wave's multiply-adds (acc += P s) run under the other's MFMAs; the 128 x
-//    128 wave tiles of the row-scaled kernel would need 256 accumulators in
-//    vector registers (the vector unit cannot add into accumulation
-//    registers), which leaves no room for P.
-//  * W fragments are the first MFMA operand, so a lane holds one token's
-//    column of a block: its factor sa[token] sw[block] is one register per
-//    block, the same for all 16 of its accumulators.
+//  * Tiles of BM x 256 (BM = 256 or 128 token rows, 256 weight rows) over
+//    eight waves, four token strips x two weight halves, two waves per SIMD:
+//    while one wave waits (for LDS, a barrier, its own results) the other
+//    feeds the matrix core.  A wave holds BM / 4 tokens x 128 weight rows,
+//    at most 128 accumulators per lane: the vector unit adds into them, so
+//    they must sit in vector registers, where the 256 accumulators of the
+//    row-scaled kernel's 128 x 128 wave tiles would leave no room.
+//  * v_mfma_f32_16x16x128_f8f6f4: one instruction per 16 x 16 block and
+//    group, so a partial product P is four registers.  (32 x 32 blocks need
+//    two instructions and sixteen registers per P; with the fragments read
+//    ahead that spilled 60 registers.)
+//  * W fragments are the first MFMA operand, so a lane holds one token of a
+//    block and its factor sa[token] sw[block] is one register for all four
+//    values of P.
 //  * K advances one group (128 bytes) per stage.  Codes and scales go
 //    straight into LDS (buffer loads to LDS), DEPTH slots, one barrier per
-//    stage: behind it stage s has landed for all waves and every wave is done
-//    with stage s - 1, whose slot takes the copies of stage s + DEPTH - 1.
+//    stage (see the schedule below).
 //  * Experts' products: a workgroup finds its (expert, rows) tile from the
 //    offsets in device memory, and gathers A rows by index with per-lane copy
 //    addresses; the grid is the largest that the row count allows, and
@@ -31,32 +33,37 @@ using namespace block;
 
 constexpr int kBK = 128;
 
-template <int WM>
+template <int BM>
 struct Geometry {
-    static constexpr int kRows = 64 * WM;                   // token rows of a tile
-    static constexpr int kWaves = 2 * WM;
-    static constexpr int kThreads = 64 * kWaves;
-    static constexpr int kA = kRows * kBK;                  // code bytes of a slot: A
+    static constexpr int kWaves = 8, kThreads = 64 * kWaves;
+    static constexpr int kStrip = BM / 4;                   // token rows of a wave
+    static constexpr int kY = kStrip / 16;                  // 16-token blocks of a wave
+    static constexpr int kA = BM * kBK;                     // code bytes of a slot: A
     static constexpr int kW = 256 * kBK;                    // and W
-    static constexpr int kSa = kRows * 4;                   // token scales
-    static constexpr int kSw = kWaves * 256;                // one 256-byte row of weight scales per wave
-    static constexpr int kSlot = kA + kW + kSa + kSw;
-    static constexpr int kDepth = WM == 4 ? 2 : 3;
-    static constexpr int kCopyA = kRows / kWaves / 8;       // copy instructions of a wave per stage: A
-    static constexpr int kCopyW = 256 / kWaves / 8;         // and W
-    static constexpr int kCopies = kCopyA + kCopyW + 2;     // and the two scale copies
+    static constexpr int kScales = kWaves * 256;            // per wave one 256-byte line of token scales, one of
+    static constexpr int kSlot = kA + kW + 2 * kScales;     // weight scales
+    static constexpr int kDepth = BM == 256 ? 2 : 3;
+    static constexpr int kCopyA = BM / kWaves / 8;          // copy instructions of a wave per stage: A
+    static constexpr int kCopyW = 256 / kWaves / 8;         // W
+    static constexpr int kCopies = kCopyA + kCopyW + 2;     // and the two scale lines
+    // weight blocks read ahead: one block is kY MFMAs, and an LDS read takes
+    // longer than two of them
+    static constexpr int kAhead = kY == 4 ? 1 : 2;
+    static constexpr int kLds = kDepth * kSlot;
+    // after the main loop: a staging region of kY 4 KiB passes per wave, a
+    // row of ones (the scales that the shared epilogue applies) and biases
+    static constexpr int kRegion = kY * 4096, kOnes = kWaves * kRegion, kBias = kOnes + 1024;
+    static_assert(kBias + kWaves * 512 <= kLds, "the epilogue's LDS fits in the slots");
     static_assert(kSlot % 256 == 0, "a slot starts on LDS bank 0");
 };
 
-template <int EPI, int WM, bool EXPERTS, bool SPLIT, bool SO>
-__global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_kernel(const BlockArgs a)
+template <int EPI, int BM, bool EXPERTS, bool SPLIT, bool SO>
+__global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_block_kernel(
+    const BlockArgs a)
 {
-    using G = Geometry<WM>;
-    constexpr int BM = G::kRows;
+    using G = Geometry<BM>;
     constexpr bool SW = EPI == SPG_EPI_SWIGLU;
-    __shared__ __attribute__((aligned(2048))) uint8_t lds[G::kDepth * G::kSlot];
-    __shared__ __attribute__((aligned(16))) float lds_one[256];
-    __shared__ __attribute__((aligned(16))) float lds_bias[EPI == SPG_EPI_ADD ? G::kWaves * 128 : 4];
+    __shared__ __attribute__((aligned(2048))) uint8_t lds[G::kLds];
     const GemmArgs &g = a.g;
     clock_mark(g.clocks, 0);
 
@@ -129,16 +136,15 @@ __global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_kernel(cons
     uint32_t vw[2];
     vw[0] = (uint32_t)(w_in + (int)rib) * (uint32_t)g.ldw + c_even * 16u;
     vw[1] = (uint32_t)(w_in + (int)rib) * (uint32_t)g.ldw + c_odd * 16u;
-    // scales: lane l the token scale of row 64 wm + l (both waves of a strip
-    // copy it: the same values to the same place), lanes 0 .. 3 the weight
-    // scales of the wave's four 32-row blocks
+    // scales: lane l the token scale of the wave's row l, lanes 0 .. 3 the
+    // weight scales of its four 32-row blocks
     const float *sa = (const float *)g.sa + ((!EXPERTS && g.stride_a) ? T.b * g.sa_bstride : 0);
     const float *sw = (const float *)g.sw + (g.stride_w ? T.b * g.sw_bstride : 0);
     uint32_t vsa, vsw = kOOB;
     {
-        const uint32_t r = (uint32_t)(wm * 64 + ln);
+        const uint32_t r = (uint32_t)(wm * G::kStrip + ln);
         uint32_t src = r;
-        bool ok = (int64_t)r < a_rows;
+        bool ok = ln < G::kStrip && (int64_t)r < a_rows;
         if (gather) {
             const int32_t x = ok ? a.row_index[T.m0 + r] : -1;
             ok = x >= 0 && (int64_t)x < a.a_rows;
@@ -156,104 +162,194 @@ __global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_kernel(cons
     const v4i rs_sw = make_rsrc(sw, (uint32_t)a.sw_words * 4u);
 
     const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
-    // stage kt (0 .. nk - 1; others copy zeros, so that every wait counts the
-    // same) into slot `slot`
-    auto issue = [&](int kt, int slot) {
-        const bool live = kt < nk;
-        const int64_t k0 = live ? (int64_t)(k0g + kt) * kBK : 0;
-        const bool in_e = live && k0 + (int64_t)c_even * 16 < g.K;
-        const bool in_o = live && k0 + (int64_t)c_odd * 16 < g.K;
-        const uint32_t soff = (uint32_t)k0;
+    // Copies of stage kt (0 .. nk - 1; others copy zeros, so that every wait
+    // counts the same): the lane conditions and scalar offsets, then copy
+    // instruction idx (A, W, token scales, weight scales) into slot `slot`.
+    struct StageCopy {
+        uint32_t soff, sw_off;
+        bool live, in_e, in_o;
+        v4i rs_sa;
+    };
+    auto plan = [&](int kt) -> StageCopy {
+        StageCopy c;
+        c.live = kt < nk;
+        const int64_t k0 = c.live ? (int64_t)(k0g + kt) * kBK : 0;
+        c.in_e = c.live && k0 + (int64_t)c_even * 16 < g.K;
+        c.in_o = c.live && k0 + (int64_t)c_odd * 16 < g.K;
+        c.soff = (uint32_t)k0;
+        const int64_t kg = c.live ? k0g + kt : 0;
+        c.sw_off = (uint32_t)kg * (uint32_t)a.sw_gs * 4u;
+        c.rs_sa = make_rsrc(sa_tile + kg * a.a_rows, sa_bytes);
+        return c;
+    };
+    auto issue_one = [&](const StageCopy &c, int slot, int idx) {
         const uint32_t base = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_base + (uint32_t)(slot * G::kSlot)));
-#pragma unroll
-        for (int i = 0; i < G::kCopyA; ++i)
-            dma16(base + (uint32_t)((wave * 8 * G::kCopyA + 8 * i) * kBK), ((i & 1) ? in_o : in_e) ? va[i] : kOOB, rs_a, soff);
-#pragma unroll
-        for (int i = 0; i < G::kCopyW; ++i)
+        if (idx < G::kCopyA)
+            dma16(base + (uint32_t)((wave * 8 * G::kCopyA + 8 * idx) * kBK),
+                  ((idx & 1) ? c.in_o : c.in_e) ? va[idx < G::kCopyA ? idx : 0] : kOOB, rs_a, c.soff);
+        else if (idx < G::kCopyA + G::kCopyW) {
+            const int i = idx - G::kCopyA;
             dma16(base + (uint32_t)(G::kA + (wave * kWRows + 8 * i) * kBK),
-                  ((i & 1) ? in_o : in_e) ? vw[i & 1] + (uint32_t)(8 * i) * (uint32_t)g.ldw : kOOB, rs_w, soff);
-        const int64_t kg = live ? k0g + kt : 0;
-        dma4(base + (uint32_t)(G::kA + G::kW + wm * 256), live ? vsa : kOOB,
-             make_rsrc(sa_tile + kg * a.a_rows, sa_bytes), 0);
-        dma4(base + (uint32_t)(G::kA + G::kW + G::kSa + wave * 256), live ? vsw : kOOB, rs_sw,
-             (uint32_t)kg * (uint32_t)a.sw_gs * 4u);
+                  ((i & 1) ? c.in_o : c.in_e) ? vw[i & 1] + (uint32_t)(8 * i) * (uint32_t)g.ldw : kOOB, rs_w, c.soff);
+        } else if (idx == G::kCopyA + G::kCopyW)
+            dma4(base + (uint32_t)(G::kA + G::kW + wave * 256), c.live ? vsa : kOOB, c.rs_sa, 0);
+        else
+            dma4(base + (uint32_t)(G::kA + G::kW + G::kScales + wave * 256), c.live ? vsw : kOOB, rs_sw, c.sw_off);
     };
 
     // ---- fragments ------------------------------------------------------------
-    const uint32_t l32 = (uint32_t)ln & 31, khalf = (uint32_t)ln >> 5, fx = (l32 >> 1) & 7u;
-    uint32_t foff[2][2];
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            foff[ks][h] = l32 * kBK + ((((uint32_t)ks * 4 + khalf * 2 + (uint32_t)h) ^ fx) << 4);
-    auto frag = [&](const uint8_t *rows, int ks) -> v8i {
-        const uint4 lo = *reinterpret_cast<const uint4 *>(rows + foff[ks][0]);
-        const uint4 hi = *reinterpret_cast<const uint4 *>(rows + foff[ks][1]);
+    // v_mfma_f32_16x16x128_f8f6f4: lane l holds row l % 16 and the 32 bytes at
+    // 32 (l / 16) of the group.  Weight rows are taken with bits 2 and 3 of
+    // the row swapped, which makes the results of two token blocks one lane
+    // exchange away from the 32 x 32 layout that the epilogue takes (below).
+    const uint32_t r16 = (uint32_t)ln & 15, kq = (uint32_t)ln >> 4;
+    const uint32_t wr16 = (r16 & 3u) | ((r16 & 4u) << 1) | ((r16 & 8u) >> 1);
+    const uint32_t foa = r16 * kBK + (((kq * 2) ^ ((r16 >> 1) & 7u)) << 4);      // second half: ^ 16
+    const uint32_t fow = wr16 * kBK + (((kq * 2) ^ ((wr16 >> 1) & 7u)) << 4);
+    auto frag = [&](const uint8_t *rows, uint32_t off) -> v8i {
+        const uint4 lo = *reinterpret_cast<const uint4 *>(rows + off);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(rows + (off ^ 16u));
         return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
     };
 
-    Acc acc;                                               // blocks acc[x][0..1]
+    v4f acc4[8][G::kY];                                    // [16 weight rows][16 tokens]
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < 8; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[x][y][e] = 0.0f;
+        for (int y = 0; y < G::kY; ++y) acc4[x][y] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto compute = [&](int slot) {
-        const uint8_t *la = &lds[slot * G::kSlot + wm * 64 * kBK];
-        const uint8_t *lw = &lds[slot * G::kSlot + G::kA];
-        const float *ls = reinterpret_cast<const float *>(&lds[slot * G::kSlot + G::kA + G::kW]);
-        v8i fa[2][2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) fa[y][ks] = frag(la + y * 32 * kBK, ks);
-        const float s0 = ls[wm * 64 + l32], s1 = ls[wm * 64 + 32 + l32];
-        const v4f swv = *reinterpret_cast<const v4f *>(ls + G::kRows + wave * 64);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint8_t *rows = lw + wtile_row0<EPI>(wn, x) * kBK;
-            const v8i f0 = frag(rows, 0), f1 = frag(rows, 1);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                v16f p = {};
-                p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f0, fa[y][0], p, 0, 0, 0, 0, 0, 0);
-                p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f1, fa[y][1], p, 0, 0, 0, 0, 0, 0);
-                const float f = (y ? s1 : s0) * swv[x];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[x][y][e] = __builtin_fmaf(p[e], f, acc[x][y][e]);
-            }
-        }
+    // One stage is 8 kY MFMAs, m = kY X + Y: weight block X (16 rows) times
+    // token block Y.  The partial product of MFMA m joins its accumulators -
+    // four multiply-adds - under MFMA m + 3, so neither unit waits for the
+    // other, and weight fragments are read kAhead blocks ahead:
+    //   block X, first MFMA : weight block X + kAhead (X < 8 - kAhead)
+    //   before block 8 - kAhead : all of this stage's weight fragments are in
+    //                   registers and this wave's copies of the next stage
+    //                   have landed -> barrier: the slot is free, the next
+    //                   stage is published
+    //   from there on : the copies of stage kt + DEPTH into the freed slot,
+    //                   spread over the MFMAs left; the next stage's first
+    //                   weight blocks; its token block Y once the last MFMA
+    //                   has taken this stage's; its scales
+    // Empty assembly statements pin the order (the compiler otherwise gathers
+    // MFMAs and multiply-adds into runs that wait for each other); hazards and
+    // waits are still the compiler's.
+    constexpr int Y_ = G::kY, kM = 8 * Y_, kBar = (8 - G::kAhead) * Y_, kBufs = 2 * G::kAhead;
+    v8i fa[Y_], fw[kBufs];
+    v4f P[4];
+    float sv[Y_], fy[Y_], sw_lo, sw_hi;                    // token scales, factors, weight scales (SWIGLU: gate, up)
+    auto read_a = [&](int slot, int y) {
+        fa[y] = frag(&lds[slot * G::kSlot] + (wm * G::kStrip + y * 16) * kBK, foa);
     };
-
-    if (tid < 256) lds_one[tid] = 1.0f;
-    if (G::kThreads < 256)
-        for (int i = tid + G::kThreads; i < 256; i += G::kThreads) lds_one[i] = 1.0f;
+    auto read_w = [&](int slot, int x) {
+        fw[x % kBufs] = frag(&lds[slot * G::kSlot] + G::kA + (wtile_row0<EPI>(wn, x >> 1) + (x & 1) * 16) * kBK, fow);
+    };
+    auto read_s = [&](int slot) {
+        const float *ls = reinterpret_cast<const float *>(&lds[slot * G::kSlot] + G::kA + G::kW + wave * 256);
 #pragma unroll
-    for (int i = 0; i < G::kDepth - 1; ++i) issue(i, i);
+        for (int y = 0; y < Y_; ++y) sv[y] = ls[y * 16 + r16];
+        sw_lo = ls[G::kScales / 4];
+        sw_hi = SW ? ls[G::kScales / 4 + 2] : 0.0f;
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) P[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};   // before stage 0: nothing to add
+#pragma unroll
+    for (int y = 0; y < Y_; ++y) fy[y] = 0.0f;
+    if (nk > 0) {
+#pragma unroll
+        for (int i = 0; i < G::kDepth; ++i) {
+            const StageCopy c = plan(i);
+#pragma unroll
+            for (int idx = 0; idx < G::kCopies; ++idx) issue_one(c, i, idx);
+        }
+        wait_vmem<(G::kDepth - 1) * G::kCopies>();
+        wait_lds();
+        block_barrier();
+#pragma unroll
+        for (int x = 0; x < G::kAhead; ++x) read_w(0, x);
+#pragma unroll
+        for (int y = 0; y < Y_; ++y) read_a(0, y);
+        read_s(0);
+    }
+    auto add = [&](int m) {                                // MFMA m's product into its accumulators
+        v4f &c = acc4[m / Y_][m % Y_];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(P[m & 3][e], fy[m % Y_], c[e]);
+        asm volatile("" : "+v"(c));
+    };
     int slot = 0;
     for (int kt = 0; kt < nk; ++kt) {
-        wait_vmem<(G::kDepth - 2) * G::kCopies>();         // stage kt landed (this wave's copies)
-        wait_lds();
-        block_barrier();                                    // ... and all waves'; stage kt - 1 is done with
-        const int free_slot = slot == 0 ? G::kDepth - 1 : slot - 1;
-        issue(kt + G::kDepth - 1, free_slot);
-        compute(slot);
-        slot = slot + 1 == G::kDepth ? 0 : slot + 1;
+        const int next = slot + 1 == G::kDepth ? 0 : slot + 1;
+        const StageCopy c = plan(kt + G::kDepth);
+#pragma unroll
+        for (int m = 0; m < kM; ++m) {
+            const int X = m / Y_, Y = m % Y_;
+            if (m == kBar) {
+                wait_lds();
+                wait_vmem<(G::kDepth - 2) * G::kCopies>();
+                block_barrier();
+            }
+            P[m & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[X % kBufs], fa[Y], v4f{0.0f, 0.0f, 0.0f, 0.0f},
+                                                                        0, 0, 0, 0, 0, 0);
+            asm volatile("" : "+v"(P[m & 3]));
+            if (Y == 0 && X + G::kAhead < 8) read_w(slot, X + G::kAhead);
+            if (Y == 0 && X + G::kAhead >= 8) read_w(next, X + G::kAhead - 8);
+            if (X == 7) read_a(next, Y);
+#pragma unroll
+            for (int idx = 0; idx < G::kCopies; ++idx)
+                if (m >= kBar && idx * (kM - kBar) / G::kCopies == m - kBar) issue_one(c, slot, idx);
+            add((m + kM - 3) % kM);                        // MFMA m - 3
+            // the factors change once the last product that takes the old
+            // ones is added: here for the weight rows' first half and, gate
+            // and up rows having their own, for the second
+            if (m == 2 || (SW && m == 4 * Y_ + 2)) {
+#pragma unroll
+                for (int y = 0; y < Y_; ++y) fy[y] = sv[y] * (m == 2 ? sw_lo : sw_hi);
+            }
+            if (m == kM - 1) read_s(next);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        slot = next;
+    }
+    if (nk > 0) {
+        add(kM - 3);
+        add(kM - 2);
+        add(kM - 1);
     }
     wait_vmem<0>();
     wait_lds();
-    block_barrier();                                        // the slots become the epilogue's staging regions
+    block_barrier();                                        // the slots become the epilogue's
+    float *const lds_one = reinterpret_cast<float *>(&lds[G::kOnes]);
+    if (tid < 256) lds_one[tid] = 1.0f;
+    wait_lds();
+    block_barrier();
+
+    // Lane l of a 16 x 16 result holds token l % 16 and weight rows 4 (l / 16)
+    // + e as taken; exchanging the odd 16-lane rows of token block 2 y with
+    // the even rows of block 2 y + 1 leaves, with the rows' swapped bits, lane
+    // l with token l % 32 and rows 8 q + 4 (l / 32) + e: the 32 x 32 layout.
+    Acc acc;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int y = 0; y < Y_ / 2; ++y)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc4[2 * x + h][2 * y][e]),
+                                                                    __float_as_uint(acc4[2 * x + h][2 * y + 1][e]), false, false);
+                    acc[x][y][8 * h + e] = __uint_as_float(t[0]);
+                    acc[x][y][8 * h + 4 + e] = __uint_as_float(t[1]);
+                }
 
     if constexpr (SPLIT) {
-        // partial tile: float4 q of block 4 y' + x of thread i at
-        // ((y' * 4 + x) * 4 + q) * threads * 4 + 4 i, whole lines per store
+        // partial tile: float4 q of block 4 y + x of thread i at
+        // ((y * 4 + x) * 4 + q) * threads * 4 + 4 i, whole lines per store
         float *base = g.partials + ((T.global * g.split_k + split) * (int64_t)(BM * 256)) + tid * 4;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            if (T.m0 + wm * 64 + y * 32 + l32 >= g.M) continue;
+        for (int y = 0; y < Y_ / 2; ++y) {
+            if (T.m0 + wm * G::kStrip + y * 32 + (ln & 31) >= g.M) continue;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -265,7 +361,8 @@ __global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_kernel(cons
         GemmArgs ge = g;
         ge.M = m_end;
         if (EXPERTS) ge.stride_o = 0;
-        epilogue<EPI, 2, true, true, SO>(ge, T, acc, lds_one, lds_one, lds_bias, &lds[wave * 16384], wave);
+        epilogue<EPI, Y_ / 2, true, true, SO>(ge, T, acc, lds_one, lds_one, reinterpret_cast<float *>(&lds[G::kBias]),
+                                              &lds[wave * G::kRegion], wave);
     }
     clock_mark(g.clocks, 1);
 }
@@ -273,24 +370,25 @@ __global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_kernel(cons
 // Sums the K slices' partial tiles and applies the epilogue: one workgroup
 // per (tile, block x, block y) of every wave (SWIGLU: a gate block and its up
 // block), each thread the 16 accumulators that it held in the product.
-template <int EPI, int WM>
-__global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_reduce_kernel(const BlockArgs a)
+template <int EPI, int BM>
+__global__ __launch_bounds__(Geometry<BM>::kThreads) void gemm_block_reduce_kernel(const BlockArgs a)
 {
-    using G = Geometry<WM>;
+    using G = Geometry<BM>;
     constexpr bool SW = EPI == SPG_EPI_SWIGLU;
+    constexpr int kYB = G::kY / 2;
     __shared__ __attribute__((aligned(16))) float lds_one[256];
     const GemmArgs &g = a.g;
     const int tid = threadIdx.x;
-    for (int i = tid; i < 256; i += G::kThreads) lds_one[i] = 1.0f;
+    if (tid < 256) lds_one[tid] = 1.0f;
     __syncthreads();
-    const Tile T = tile_from_id<EPI, G::kRows>(g, blockIdx.x);
-    const int x = (int)blockIdx.y >> 1, y = (int)blockIdx.y & 1;
+    const Tile T = tile_from_id<EPI, BM>(g, blockIdx.x);
+    const int x = (int)blockIdx.y / kYB, y = (int)blockIdx.y % kYB;
     const int wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-    if (T.m0 + wm * 64 + y * 32 + (tid & 31) >= g.M) return;
-    const float *base = g.partials + (int64_t)blockIdx.x * g.split_k * (G::kRows * 256) + tid * 4;
+    if (T.m0 + wm * G::kStrip + y * 32 + (tid & 31) >= g.M) return;
+    const float *base = g.partials + (int64_t)blockIdx.x * g.split_k * (BM * 256) + tid * 4;
     v16f sum = {}, up = {};
     for (int s = 0; s < g.split_k; ++s) {
-        const float *p = base + (int64_t)s * (G::kRows * 256);
+        const float *p = base + (int64_t)s * (BM * 256);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const v4f v = __builtin_nontemporal_load(
@@ -305,26 +403,27 @@ __global__ __launch_bounds__(Geometry<WM>::kThreads) void gemm_block_reduce_kern
             }
         }
     }
-    // epilogue_block places wave strip wm at 128 wm + 32 y: shift y by -2 wm
-    // for strips of 64 rows.  Its own wm is the same thread index >> 7.
-    epilogue_block<EPI>(g, T, epi_out<EPI>(g, T), wtile_row0<EPI>(wn, x), y - 2 * wm, sum, up, lds_one, lds_one);
+    // epilogue_block places 32-row block y of strip wm at row 128 wm + 32 y
+    // of the tile; strips here are kStrip rows
+    epilogue_block<EPI>(g, T, epi_out<EPI>(g, T), wtile_row0<EPI>(wn, x), y - wm * (128 - G::kStrip) / 32, sum, up,
+                        lds_one, lds_one);
 }
 
-template <int EPI, int WM>
+template <int EPI, int BM>
 hipError_t launch_geometry(const BlockArgs &a, int64_t workgroups, hipStream_t s)
 {
-    const dim3 grid((unsigned)workgroups), threads(Geometry<WM>::kThreads);
+    const dim3 grid((unsigned)workgroups), threads(Geometry<BM>::kThreads);
     if (a.experts > 0) {
         if constexpr (EPI != SPG_EPI_ADD)
-            gemm_block_kernel<EPI, WM, true, false, false><<<grid, threads, 0, s>>>(a);
+            gemm_block_kernel<EPI, BM, true, false, false><<<grid, threads, 0, s>>>(a);
         else
             return hipErrorInvalidValue;
     } else if (a.g.split_k > 1) {
-        gemm_block_kernel<EPI, WM, false, true, false><<<grid, threads, 0, s>>>(a);
+        gemm_block_kernel<EPI, BM, false, true, false><<<grid, threads, 0, s>>>(a);
     } else if (a.g.nseg != 0) {
-        gemm_block_kernel<EPI, WM, false, false, true><<<grid, threads, 0, s>>>(a);
+        gemm_block_kernel<EPI, BM, false, false, true><<<grid, threads, 0, s>>>(a);
     } else {
-        gemm_block_kernel<EPI, WM, false, false, false><<<grid, threads, 0, s>>>(a);
+        gemm_block_kernel<EPI, BM, false, false, false><<<grid, threads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -332,18 +431,21 @@ hipError_t launch_geometry(const BlockArgs &a, int64_t workgroups, hipStream_t s
 template <int EPI>
 hipError_t launch_epi(const BlockArgs &a, int bm, int64_t workgroups, hipStream_t s)
 {
-    return bm == 256 ? launch_geometry<EPI, 4>(a, workgroups, s) : launch_geometry<EPI, 2>(a, workgroups, s);
+    return bm == 256 ? launch_geometry<EPI, 256>(a, workgroups, s) : launch_geometry<EPI, 128>(a, workgroups, s);
+}
+
+template <int EPI, int BM>
+hipError_t launch_reduce(const BlockArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)a.g.tile_count, (EPI == SPG_EPI_SWIGLU ? 2u : 4u) * (Geometry<BM>::kY / 2));
+    gemm_block_reduce_kernel<EPI, BM><<<grid, Geometry<BM>::kThreads, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <int EPI>
-hipError_t launch_reduce(const BlockArgs &a, int bm, hipStream_t s)
+hipError_t launch_reduce_epi(const BlockArgs &a, int bm, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.g.tile_count, EPI == SPG_EPI_SWIGLU ? 4u : 8u);
-    if (bm == 256)
-        gemm_block_reduce_kernel<EPI, 4><<<grid, Geometry<4>::kThreads, 0, s>>>(a);
-    else
-        gemm_block_reduce_kernel<EPI, 2><<<grid, Geometry<2>::kThreads, 0, s>>>(a);
-    return hipGetLastError();
+    return bm == 256 ? launch_reduce<EPI, 256>(a, s) : launch_reduce<EPI, 128>(a, s);
 }
 
 }  // namespace
@@ -360,9 +462,9 @@ hipError_t launch_gemm_block_tiles(const BlockArgs &a, int bm, int64_t workgroup
 hipError_t launch_gemm_block_reduce(const BlockArgs &a, int bm, hipStream_t s)
 {
     switch (a.g.epilogue) {
-    case SPG_EPI_STORE: return launch_reduce<SPG_EPI_STORE>(a, bm, s);
-    case SPG_EPI_ADD: return launch_reduce<SPG_EPI_ADD>(a, bm, s);
-    default: return launch_reduce<SPG_EPI_SWIGLU>(a, bm, s);
+    case SPG_EPI_STORE: return launch_reduce_epi<SPG_EPI_STORE>(a, bm, s);
+    case SPG_EPI_ADD: return launch_reduce_epi<SPG_EPI_ADD>(a, bm, s);
+    default: return launch_reduce_epi<SPG_EPI_SWIGLU>(a, bm, s);
     }
 }
 
