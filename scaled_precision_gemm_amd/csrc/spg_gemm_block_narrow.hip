@@ -151,9 +151,10 @@ __global__ __launch_bounds__(kNarrowThreads) void gemm_block_narrow_kernel(const
         dma4(base + ROWS * kChunk + 256, live ? vsw : kOOB, rsw, (uint32_t)cg * (uint32_t)a.sw_gs * 4u);
     };
 
-    const uint32_t fsw = (uint32_t)((r >> 1) & 7);
-    const uint32_t fo0 = (uint32_t)r * kChunk + ((((uint32_t)kq * 2) ^ fsw) << 4);
-    const uint32_t fo1 = (uint32_t)r * kChunk + ((((uint32_t)kq * 2 + 1) ^ fsw) << 4);
+    // chunks of a lane's 32 bytes chosen against bank conflicts (see
+    // spg_gemm_block.hip)
+    const uint32_t fsw = (uint32_t)((r >> 1) & 7), q0 = (uint32_t)((kq & 1) | ((kq & 2) << 1));
+    const uint32_t fo0 = (uint32_t)r * kChunk + ((q0 ^ fsw) << 4), fo1 = fo0 ^ 32u;
     auto frag = [&](const uint8_t *rows) -> v8i {
         const uint4 lo = *reinterpret_cast<const uint4 *>(rows + fo0);
         const uint4 hi = *reinterpret_cast<const uint4 *>(rows + fo1);
