@@ -200,8 +200,18 @@ bool narrow_route(const spg_gemm_desc *d, int64_t nout, bool aligned_scales = tr
 }
 
 // Block-scaled FP8 (kernels 4 - 6): decode width as for the other formats,
-// else tiles of 128 or 256 rows, split along K when they leave compute units
-// idle.
+// else the cheapest of 256- and 128-row tiles with K in s slices, priced in
+// microseconds on MI355X as
+//   rounds (stages S + 5) + [s > 1] (7 + partial tiles written and read at 5 TB/s)
+// with S = 1.5 us a stage of 256-row tiles and 0.92 of 128-row tiles, 5 us a
+// tile's fill and epilogue, 7 us the reduction's launch and latency.  Measured
+// against the model (us): 1024 x 5120 x 17408 in 256-row tiles s = 1, 2, 3, 4:
+// 179, 116, 100, 133 (209, 129, 106, 140), 128-row tiles s = 1, 3: 131, 119
+// (130, 126); 512 x 5120 x 17408 128-row s = 1, 2, 3, 4: 122, 75, 62, 85; 128 x
+// 5120 x 17408 s = 4, 8, 12: 42, 31, 32; 512 x 2048 x 2048 s = 1, 2, 4: 19, 21,
+// 21; 1024 x 7168 x 5120 128- and 256-row: 44 and 59; 2048 x 7168 x 5120 90 and
+// 68.  A last round of 256-row tiles that fills at most half of the units runs
+// as 128-row halves in a second launch (kernel's tail), when that is cheaper.
 void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
 {
     const int64_t nout = n_out_of(d, epi);
@@ -217,24 +227,44 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
         return;
     }
     p->bn = (int32_t)kTile;
+    p->kernel = 4;
+    p->bm = (int32_t)kTile;
     const int64_t tiles_n = epi == SPG_EPI_SWIGLU ? cdiv(nout, kTile / 2) : cdiv(d->N, kTile);
-    const int64_t t256 = d->batch * cdiv(d->M, 256) * tiles_n, t128 = d->batch * cdiv(d->M, 128) * tiles_n;
-    const bool half = t128 < (INT64_C(1) << 31) && 0.6 * (double)cdiv(t128, units) < (double)cdiv(t256, units);
-    p->kernel = half ? 5 : 4;
-    p->bm = half ? 128 : 256;
-    p->tiles = half ? t128 : t256;
-    if (p->tiles > 0 && d->K > 0) {
-        double best = (double)cdiv(p->tiles, units);
-        for (int s = 2; s <= 8 && d->K / s >= 1024; ++s) {
-            if ((int64_t)(s - 1) * (cdiv(cdiv(d->K, s), 128) * 128) >= d->K) continue;   // a slice would be empty
-            const double cost = (double)cdiv(p->tiles * s, units) / s;
-            if (p->tiles * 2 <= units && cost < best - 1e-9) {
+    constexpr double kStage[2] = {1.5, 0.92}, kTileCost = 5.0, kReduce = 7.0, kHalfLaunch = 2.0;
+    double best = INFINITY;
+    for (int half = 0; half < 2; ++half) {
+        const int64_t bm = half ? 128 : 256, tiles = d->batch * cdiv(d->M, bm) * tiles_n;
+        if (tiles >= (INT64_C(1) << 31)) continue;                // 32-bit tile ids
+        if (!half) p->tiles = tiles;
+        for (int s = 1; s <= 16; ++s) {
+            const int64_t stages = cdiv(cdiv(d->K, s), 128);
+            // slices of at least 4 stages, none empty, at most two rounds
+            if (s > 1 && (d->K == 0 || stages < 4 || (int64_t)(s - 1) * stages * 128 >= d->K || tiles * s > 2 * units)) continue;
+            const double tile = (double)stages * kStage[half] + kTileCost;
+            double cost = (double)cdiv(tiles * s, units) * tile;
+            if (s > 1)
+                cost += kReduce + 2.0 * (double)(tiles * s) * (double)(d->M < bm ? d->M : bm) * kTile * 4.0 / 5e6;
+            int64_t tail = 0;
+            const int64_t rem = tiles % units;
+            if (!half && s == 1 && tiles > units && rem > 0 && 2 * rem <= units) {
+                const double t = (double)(tiles / units) * tile + (double)stages * kStage[1] + kTileCost + kHalfLaunch;
+                if (t < cost) {
+                    cost = t;
+                    tail = rem;
+                }
+            }
+            if (cost < best) {
                 best = cost;
+                p->kernel = half ? 5 : 4;
+                p->bm = (int32_t)bm;
+                p->tiles = tiles;
                 p->split_k = s;
+                p->tail_tiles = tail;
+                p->tail_bm = tail ? 128 : (int32_t)kTile;
             }
         }
     }
-    p->workgroups = p->tiles * p->split_k;
+    p->workgroups = (p->tiles - p->tail_tiles) * p->split_k;
 }
 
 void make_plan(const spg_gemm_desc *d, int epi, int units, spg_plan *p, bool aligned_scales = true)
@@ -494,10 +524,18 @@ static int run_block(const spg_gemm_desc *d, const spg_plan &p, const GemmArgs &
     a.g.tiles_m = cdiv(d->M, p.bm);
     a.g.div_per = make_fastdiv((uint32_t)(a.g.tiles_m * a.g.tiles_n));
     a.g.div_gm_last = make_fastdiv(a.g.tiles_m % 8 ? (uint32_t)(a.g.tiles_m % 8) : 8u);
+    a.g.rows128 = p.bm == 128;
     a.g.tile_begin = 0;
-    a.g.tile_count = p.tiles;
+    a.g.tile_count = p.tiles - p.tail_tiles;
     hipError_t e = launch_gemm_block_tiles(a, p.bm, p.workgroups, s);
     if (e == hipSuccess && p.split_k > 1) e = launch_gemm_block_reduce(a, p.bm, s);
+    if (e == hipSuccess && p.tail_tiles > 0) {
+        // the tail: the last tail_tiles tiles as two 128-row halves each
+        a.g.clocks = nullptr;
+        a.g.tile_begin = a.g.tile_count;
+        a.g.tile_count = p.tail_tiles;
+        e = launch_gemm_block_tiles(a, 128, 2 * p.tail_tiles, s);
+    }
     return e == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 

@@ -92,9 +92,18 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         T.c0 = T.n0;
         m_end = t.end;
     } else {
-        const WorkItem wi = work_item(g);
-        split = wi.split;
-        T = tile_from_id<EPI, BM>(g, wi.tile);
+        if (BM == 128 && !SPLIT && !g.rows128) {
+            // the tail of a product in 256-row tiles: half v % 2 of tile
+            // tile_begin + v / 2 (neighbouring halves share their W panel)
+            const uint32_t v = (uint32_t)xcd_remap(blockIdx.x, 2 * g.tile_count);
+            T = tile_from_id<EPI, 256>(g, g.tile_begin + (v >> 1));
+            T.m0 += (int64_t)(v & 1u) * 128;
+            if (T.m0 >= g.M) return;
+        } else {
+            const WorkItem wi = work_item(g);
+            split = wi.split;
+            T = tile_from_id<EPI, BM>(g, g.tile_begin + wi.tile);
+        }
     }
     const int k0g = SPLIT ? split * (int)(g.k_chunk / kBK) : 0;                    // first group
     const int nk = SPLIT ? min(a.groups - k0g, (int)(g.k_chunk / kBK)) : a.groups;

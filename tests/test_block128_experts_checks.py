@@ -68,7 +68,9 @@ def test_plans(M, N, K):
     tiles = {4: (256, 256), 5: (128, 256), 6: (p["bm"], 32)}
     bm, bn = tiles[p["kernel"]]
     assert (p["bm"], p["bn"]) == (bm, bn) and (p["kernel"] != 6 or p["bm"] in (16, 32) and p["bm"] >= min(M, 32))
-    assert p["tiles"] == -(-M // bm) * -(-N // bn) and p["workgroups"] == p["tiles"] * p["split_k"]
+    assert p["tiles"] == -(-M // bm) * -(-N // bn)
+    assert p["workgroups"] == (p["tiles"] - p["tail_tiles"]) * p["split_k"]
+    assert p["tail_tiles"] == 0 or (p["kernel"], p["split_k"], p["tail_bm"], p["tail_split"]) == (4, 1, 128, 1)
     chunk = -(--(-K // p["split_k"]) // 128) * 128
     assert 1 <= p["split_k"] and (p["split_k"] - 1) * chunk < K     # no empty slice
     assert p["split_k"] == 1 or p["kernel"] != 6

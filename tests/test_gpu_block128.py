@@ -163,21 +163,25 @@ def test_plans_cover_every_kernel(spg):
     assert plan(16, 1000, 1040)["kernel"] == 6 and plan(17, 516, 272)["bm"] == 32
     assert plan(64, 300, 2064)["split_k"] > 1 and plan(96, 512, 8208)["split_k"] > 1
     assert plan(4096, 34816, 5120, epilogue="swiglu")["kernel"] == 4
-    assert plan(128, 34816, 5120)["kernel"] == 5
+    assert plan(128, 34816, 5120)["kernel"] == 5 and plan(512, 2048, 512)["kernel"] == 5
 
 
-def test_large_tiles(spg):
-    # enough tiles for the 256-row kernel, ragged in M, N and K, checked on
-    # sampled rows and columns
-    M, N, K = 3000, 8200, 400
-    assert spg.gemm_plan(M, N, K, fmt="e4m3_block128")["kernel"] == 4
+@pytest.mark.parametrize("M,N,K,tail", [(3000, 8200, 400, False), (3000, 6400, 1040, True), (2600, 12800, 400, True)])
+def test_large_tiles(spg, M, N, K, tail):
+    # enough tiles for the 256-row kernel, ragged in M, N and K, with and
+    # without a last round of 128-row halves; every row of sampled columns
+    # and every column of sampled rows
+    plan = spg.gemm_plan(M, N, K, fmt="e4m3_block128")
+    assert plan["kernel"] == 4 and (plan["tail_tiles"] > 0) == tail
     qa, sa, qw, sw = operands(spg, M, N, K, 300)
     out = spg.gemm_scaled(qa, sa, qw, sw, fmt="e4m3_block128")
-    rows = np.r_[0:3, 254:258, 1500:1503, 2996:3000]
-    cols = np.r_[0:3, 127:130, 255:258, 4000:4003, 8190:8200]
-    a = values(qa.cpu().numpy(), sa.cpu().numpy(), "row")[rows]
-    w = values(qw.cpu().numpy(), sw.cpu().numpy(), "block")[cols]
-    check(out[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], a @ w.T, np.abs(a) @ np.abs(w).T, "large")
+    rows = np.r_[0:3, 126:130, 254:258, 1500:1503, M - 6:M]
+    cols = np.r_[0:3, 127:130, 255:258, 4000:4003, N - 10:N]
+    a = values(qa.cpu().numpy(), sa.cpu().numpy(), "row")
+    w = values(qw.cpu().numpy(), sw.cpu().numpy(), "block")
+    ar, wc = a[rows], w[cols]
+    check(out[torch.from_numpy(rows).cuda()], ar @ w.T, np.abs(ar) @ np.abs(w).T, "rows")
+    check(out[:, torch.from_numpy(cols).cuda()], a @ wc.T, np.abs(a) @ np.abs(wc).T, "columns")
 
 
 @pytest.mark.parametrize("M,N,K", [(16, 512, 384), (200, 528, 400), (2064, 4112, 272)])
