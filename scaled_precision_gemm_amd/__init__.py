@@ -172,6 +172,48 @@ def _need(cond: bool, msg: str):
         raise ValueError(msg)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _run(fn, what: str, t: torch.Tensor, *args):
+    """Calls the library with t's device current, on that device's current
+    stream (the last argument of every launching entry point)."""
+    if _current_device() == t.get_device():
+        status = fn(*args, _stream(t))
+    else:
+        with torch.cuda.device(t.device):
+            status = fn(*args, _stream(t))
+    if status != 0:
+        raise SpgError(status, what)
+
+
+# The checks of a call depend only on what _sig reads of its tensors (and on
+# its options), so a call that repeats an earlier one's signature reuses what
+# the checks worked out.
+_CALLS: dict = {}
+_CALLS_MAX = 512
+
+
+def _checked(key, check):
+    hit = _CALLS.get(key)
+    if hit is None:
+        hit = check()
+        if len(_CALLS) >= _CALLS_MAX:
+            _CALLS.clear()
+        _CALLS[key] = hit
+    return hit
+
+
+def _sig(t):
+    """What the argument checks read of a tensor: shape, strides, dtype,
+    device and the pointer's alignment (TypeError for a non-tensor)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("arguments must be tensors")
+    return (t.shape, t.stride(), t.dtype, t.device, t.data_ptr() & 15)
+
+
 # ---------------------------------------------------------------------------
 # quantizers
 # ---------------------------------------------------------------------------
@@ -239,13 +281,7 @@ def block128_scale_shape(R: int, K: int, tiling="row") -> tuple:
     return {"row": (gk, R), "column": (gr, K), "block": (gr, gk)}[tiling]
 
 
-def quantize_block128(x: torch.Tensor, tiling="row", out: torch.Tensor | None = None,
-                      scale: torch.Tensor | None = None):
-    """E4M3 with an fp32 scale per 128 elements: x bf16 [R, K] or [B, R, K] ->
-    (codes uint8 like x, scales fp32).  tiling "row": 1 x 128 (activations;
-    scales group-major [ceil(K/128), R]); "column": 128 x 1 (a K-major A, as
-    the weight-gradient product reads it; [ceil(R/128), K]); "block": 128 x
-    128 (weights; [ceil(R/128), ceil(K/128)])."""
+def _check_block128(x, tiling, out, scale):
     _need(isinstance(x, torch.Tensor) and x.dtype == torch.bfloat16 and x.dim() in (2, 3),
           "x must be a 2-D or 3-D bf16 tensor")
     _need(tiling in _TILING, f"unknown tiling {tiling}")
@@ -256,26 +292,37 @@ def quantize_block128(x: torch.Tensor, tiling="row", out: torch.Tensor | None = 
     _need(B >= 1, "x must hold at least one matrix")
     _need(K % 16 == 0, "rows must be a multiple of 16 elements")
     _need(R <= 1 or x.stride(-2) % 8 == 0 and x.stride(-2) >= K, "the row stride must be a multiple of 8, at least K")
-    _need(B == 1 or x.stride(0) % 8 == 0 and x.stride(0) >= (R - 1) * x.stride(-2) + K,
+    _need(R == 0 or B == 1 or x.stride(0) % 8 == 0 and x.stride(0) >= (R - 1) * x.stride(-2) + K,
           "matrices must not overlap, their stride a multiple of 8")
     shape = lead + block128_scale_shape(R, K, tiling)
     for name, t, want, dt in (("out", out, tuple(x.shape), torch.uint8), ("scale", scale, shape, torch.float32)):
         _need(t is None or (isinstance(t, torch.Tensor) and t.device == x.device and t.dtype == dt
                             and tuple(t.shape) == want), f"{name} must be {dt} {want} on {x.device}")
-    if out is not None:
-        _need((out.stride(-1) == 1 or K <= 1) and (R <= 1 or out.stride(-2) % 16 == 0 and out.stride(-2) >= K)
+    ldq, qbs = K, R * K
+    if out is not None and R > 0:
+        _need(out.stride(-1) == 1 and (R == 1 or out.stride(-2) % 16 == 0 and out.stride(-2) >= K)
               and (B == 1 or out.stride(0) % 16 == 0 and out.stride(0) >= (R - 1) * out.stride(-2) + K),
               "out rows must be contiguous, 16-byte aligned and must not overlap")
+        ldq, qbs = out.stride(-2) if R > 1 else K, out.stride(0) if B > 1 else 0
     _need(scale is None or scale.is_contiguous(), "scale must be contiguous")
     _need(x.is_cuda, "x must be a CUDA tensor")
+    return (B, R, K, x.stride(-2) if R > 1 else K, x.stride(0) if B > 1 else 0), (ldq, qbs), shape
+
+
+def quantize_block128(x: torch.Tensor, tiling="row", out: torch.Tensor | None = None,
+                      scale: torch.Tensor | None = None):
+    """E4M3 with an fp32 scale per 128 elements: x bf16 [R, K] or [B, R, K] ->
+    (codes uint8 like x, scales fp32).  tiling "row": 1 x 128 (activations;
+    scales group-major [ceil(K/128), R]); "column": 128 x 1 (a K-major A, as
+    the weight-gradient product reads it; [ceil(R/128), K]); "block": 128 x
+    128 (weights; [ceil(R/128), ceil(K/128)])."""
+    dims, strides, shape = _checked(("quantize", tiling, _sig(x), _sig(out), _sig(scale)),
+                                    lambda: _check_block128(x, tiling, out, scale))
     q = out if out is not None else torch.empty(x.shape, dtype=torch.uint8, device=x.device)
     s = scale if scale is not None else torch.empty(shape, dtype=torch.float32, device=x.device)
-    if R > 0:
-        ldx, ldq = max(x.stride(-2), K) if R > 1 else K, max(q.stride(-2), K) if R > 1 else K
-        with torch.cuda.device(x.device):
-            _check(lib.quantize_block128(_ptr(x), B, R, K, ldx, x.stride(0) if B > 1 else 0, _ptr(q), ldq,
-                                         q.stride(0) if B > 1 else 0, _ptr(s), _TILING[tiling], _stream(x)),
-                   "quantize_block128")
+    if dims[1] > 0:
+        _run(lib.quantize_block128, "quantize_block128", x, x.data_ptr(), *dims, q.data_ptr(), *strides, s.data_ptr(),
+             _TILING[tiling])
     return q, s
 
 
@@ -547,23 +594,13 @@ def gemm_scaled(A, sa, W, sw, epilogue="store", residual=None, fmt="e4m3_row",
         wsp, wsn = workspace.data_ptr(), workspace.numel()
     else:
         wsp, wsn = None, 0
-    _check(lib.gemm_scaled(_ptr(out), A.data_ptr(), _ptr(sa), W.data_ptr(), _ptr(sw), _ptr(residual), epi,
-                           ctypes.byref(d), wsp, wsn, _stream(A)), "gemm_scaled")
+    _run(lib.gemm_scaled, "gemm_scaled", A, _ptr(out), A.data_ptr(), _ptr(sa), W.data_ptr(), _ptr(sw), _ptr(residual),
+         epi, ctypes.byref(d), wsp, wsn)
     return segs if segs is not None else out
 
 
 _GEMM_CACHE: dict = {}
 _GEMM_CACHE_MAX = 256
-
-
-def _sig(t):
-    """What the argument checks read of a tensor: shape, strides, dtype,
-    device and the pointer's alignment (TypeError for a non-tensor)."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError
-    return (t.shape, t.stride(), t.dtype, t.device, t.data_ptr() & 15)
 
 
 def _prepare(A, sa, W, sw, fmt, epilogue, out, residual, tscale_a, tscale_w, scale_layout, bias_scale,
@@ -666,6 +703,7 @@ def _grouped(A, sa, W, sw, offsets, epilogue, rows, out):
         _need(tuple(out.shape) == (R, n_out), f"out must have shape {(R, n_out)}")
     d = GroupedDesc(R, a_rows, N, K, _ld(A), W.stride(1) if N > 1 else K, W.stride(0) if E > 1 else 0,
                     n_out if out is None else _ld(out), E, 0)
+    _need(A.is_cuda, "operands must be CUDA tensors")
     return d, epi, n_out
 
 
@@ -678,14 +716,13 @@ def gemm_grouped(A, sa, W, sw, offsets, epilogue="store", rows=None, out=None):
     [E, N, K], sw fp32 [E, ceil(N/128), ceil(K/128)] ("block"); offsets int32
     [E + 1] and rows int32 [R] as expert_route returns them.  Rows of no
     expert are left as they were (undefined in an output allocated here)."""
-    d, epi, n_out = _grouped(A, sa, W, sw, offsets, epilogue, rows, out)
-    _need(A.is_cuda, "operands must be CUDA tensors")
+    d, epi, n_out = _checked(("grouped", epilogue, _sig(A), _sig(sa), _sig(W), _sig(sw), _sig(offsets), _sig(rows),
+                              _sig(out)), lambda: _grouped(A, sa, W, sw, offsets, epilogue, rows, out))
     if out is None:
         out = torch.empty((d.rows, n_out), dtype=torch.bfloat16, device=A.device)
     if d.rows > 0 and n_out > 0:
-        with torch.cuda.device(A.device):
-            _check(lib.gemm_grouped(_ptr(out), _ptr(A), _ptr(sa), _ptr(W), _ptr(sw), _ptr(offsets), _ptr(rows), epi,
-                                    ctypes.byref(d), _stream(A)), "gemm_grouped")
+        _run(lib.gemm_grouped, "gemm_grouped", A, out.data_ptr(), A.data_ptr(), sa.data_ptr(), W.data_ptr(),
+             sw.data_ptr(), offsets.data_ptr(), _ptr(rows), epi, ctypes.byref(d))
     return out
 
 
@@ -716,8 +753,7 @@ def _route_desc(logits, top, score, groups, top_groups, renormalize, scale):
                      int(logits.dtype == torch.bfloat16), scale)
 
 
-def _order_ws(workspace, T, E, dev):
-    n = lib.expert_route_workspace_bytes(T, E)
+def _order_ws(workspace, n, dev):
     if n == 0:
         return None, 0
     if workspace is None:
@@ -740,26 +776,30 @@ def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1
     index; weights are scale p / sum p (renormalize) or scale p.  Logits of
     -inf mask an expert: places that no expert is left for hold expert -1,
     weight 0, slot -1."""
-    d = _route_desc(logits, top, score, groups, top_groups, renormalize, scale)
-    dev = logits.device
-    _need(bias is None or (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32 and bias.device == dev
-                           and tuple(bias.shape) == (d.E,) and bias.is_contiguous()),
-          f"bias must be a contiguous fp32 [{d.E}] tensor on {dev}")
-    _need(logits.is_cuda, "logits must be a CUDA tensor")
-    T = d.T
-    ws, nws = _order_ws(workspace, T, d.E, dev) if order else (None, 0)
+    def check():
+        d = _route_desc(logits, top, score, groups, top_groups, renormalize, scale)
+        _need(bias is None or (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32
+                               and bias.device == logits.device and tuple(bias.shape) == (d.E,)
+                               and bias.is_contiguous()),
+              f"bias must be a contiguous fp32 [{d.E}] tensor on {logits.device}")
+        _need(logits.is_cuda, "logits must be a CUDA tensor")
+        return d, lib.expert_route_workspace_bytes(d.T, d.E)
+
+    d, nws = _checked(("route", _sig(logits), top, score, _sig(bias), groups, top_groups, bool(renormalize), scale), check)
+    dev, T = logits.device, d.T
     weights = torch.empty((T, top), dtype=torch.float32, device=dev)
-    # one allocation for the integers
-    ints = torch.empty((T * top * (3 if order else 1) + (d.E + 1 if order else 0),), dtype=torch.int32, device=dev)
-    n = T * top
-    experts = ints[:n].view(T, top)
-    rows, slots, offsets = (ints[n:2 * n], ints[2 * n:3 * n].view(T, top), ints[3 * n:]) if order else (None,) * 3
-    with torch.cuda.device(dev):
-        # an empty tensor's pointer may be null: rows and slots of no token
-        _check(lib.expert_route(_ptr(logits), _ptr(bias), _ptr(weights), _ptr(experts), _ptr(offsets),
-                                (_ptr(rows) or _ptr(offsets)) if order else None,
-                                (_ptr(slots) or _ptr(offsets)) if order else None,
-                                ctypes.byref(d), _ptr(ws), nws, _stream(logits)), "expert_route")
+    experts = torch.empty((T, top), dtype=torch.int32, device=dev)
+    if not order:
+        _run(lib.expert_route, "expert_route", logits, logits.data_ptr(), _ptr(bias), weights.data_ptr(),
+             experts.data_ptr(), None, None, None, ctypes.byref(d), None, 0)
+        return ExpertRoute(weights, experts, None, None, None)
+    ws, nws = _order_ws(workspace, nws, dev)
+    offsets = torch.empty((d.E + 1,), dtype=torch.int32, device=dev)
+    rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
+    slots = torch.empty((T, top), dtype=torch.int32, device=dev)
+    po = offsets.data_ptr()           # no token: rows and slots are empty and may have no address
+    _run(lib.expert_route, "expert_route", logits, logits.data_ptr(), _ptr(bias), weights.data_ptr(),
+         experts.data_ptr(), po, rows.data_ptr() or po, slots.data_ptr() or po, ctypes.byref(d), _ptr(ws), nws)
     return ExpertRoute(weights, experts, offsets, rows, slots)
 
 
@@ -772,13 +812,12 @@ def expert_sort(experts, n_experts, workspace=None):
     _index("experts", experts, (T, top), dev)
     _need(top >= 1 and n_experts >= 1, "at least one expert")
     _need(experts.is_cuda, "experts must be a CUDA tensor")
-    ws, nws = _order_ws(workspace, T, n_experts, dev)
+    ws, nws = _order_ws(workspace, lib.expert_route_workspace_bytes(T, n_experts), dev)
     offsets = torch.empty((n_experts + 1,), dtype=torch.int32, device=dev)
     rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
     slots = torch.empty((T, top), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.expert_sort(_ptr(experts), T, top, n_experts, _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(ws), nws,
-                               _stream(experts)), "expert_sort")
+    _run(lib.expert_sort, "expert_sort", experts, _ptr(experts), T, top, n_experts, _ptr(offsets), _ptr(rows),
+         _ptr(slots), _ptr(ws), nws)
     return offsets, rows, slots
 
 
@@ -786,18 +825,22 @@ def expert_route_backward(grad_weights, logits, experts, score="softmax", renorm
     """The gradient of the logits ([T, E], their type) from that of
     expert_route's weights (fp32 [T, top]), for the same logits, options and
     the experts it chose."""
-    _need(isinstance(experts, torch.Tensor) and experts.dim() == 2, "experts must be a 2-D int32 tensor")
-    d = _route_desc(logits, experts.shape[1], score, 1, 1, renormalize, scale)
-    dev, T = logits.device, d.T
-    _index("experts", experts, (T, d.top), dev)
-    _need(isinstance(grad_weights, torch.Tensor) and grad_weights.dtype == torch.float32 and grad_weights.device == dev
-          and tuple(grad_weights.shape) == (T, d.top) and grad_weights.is_contiguous(),
-          f"grad_weights must be a contiguous fp32 {(T, d.top)} tensor on {dev}")
-    _need(logits.is_cuda, "logits must be a CUDA tensor")
-    grad = torch.empty((T, d.E), dtype=logits.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.expert_route_backward(_ptr(grad_weights), _ptr(logits), _ptr(experts), _ptr(grad), ctypes.byref(d),
-                                         _stream(logits)), "expert_route_backward")
+    def check():
+        _need(isinstance(experts, torch.Tensor) and experts.dim() == 2, "experts must be a 2-D int32 tensor")
+        d = _route_desc(logits, experts.shape[1], score, 1, 1, renormalize, scale)
+        dev = logits.device
+        _index("experts", experts, (d.T, d.top), dev)
+        _need(isinstance(grad_weights, torch.Tensor) and grad_weights.dtype == torch.float32
+              and grad_weights.device == dev and tuple(grad_weights.shape) == (d.T, d.top)
+              and grad_weights.is_contiguous(), f"grad_weights must be a contiguous fp32 {(d.T, d.top)} tensor on {dev}")
+        _need(logits.is_cuda, "logits must be a CUDA tensor")
+        return d
+
+    d = _checked(("route backward", _sig(grad_weights), _sig(logits), _sig(experts), score, bool(renormalize), scale),
+                 check)
+    grad = torch.empty((d.T, d.E), dtype=logits.dtype, device=logits.device)
+    _run(lib.expert_route_backward, "expert_route_backward", logits, grad_weights.data_ptr(), logits.data_ptr(),
+         experts.data_ptr(), grad.data_ptr(), ctypes.byref(d))
     return grad
 
 
@@ -818,19 +861,21 @@ def expert_combine(y, weights, slots, residual=None, out=None):
     """out[t] = residual[t] + sum_j weights[t, j] y[slots[t, j]] in bf16 [T, H]
     (fp32 sums, one rounding): y bf16 [R, H] the experts' rows, weights and
     slots of expert_route; residual bf16 [T, H], which may be out itself."""
-    dev = _combine_args(y, weights, slots, None)
-    (T, top), (R, H) = slots.shape, y.shape
-    for name, t in (("residual", residual), ("out", out)):
-        if t is not None:
-            _rows_ok(name, t, torch.bfloat16, dev)
-            _need(tuple(t.shape) == (T, H), f"{name} must have shape {(T, H)}")
-    _need(y.is_cuda, "y must be a CUDA tensor")
+    def check():
+        dev = _combine_args(y, weights, slots, None)
+        want = (slots.shape[0], y.shape[1])
+        for name, t in (("residual", residual), ("out", out)):
+            if t is not None:
+                _rows_ok(name, t, torch.bfloat16, dev)
+                _need(tuple(t.shape) == want, f"{name} must have shape {want}")
+        _need(y.is_cuda, "y must be a CUDA tensor")
+        return (_ld(y), 0 if residual is None else _ld(residual), want[1] if out is None else _ld(out)), want
+
+    (ldy, ldr, ldo), want = _checked(("combine", _sig(y), _sig(weights), _sig(slots), _sig(residual), _sig(out)), check)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.expert_combine(_ptr(y), R, _ld(y), _ptr(weights), _ptr(slots), T, top, H, _ptr(residual),
-                                  _ld(residual) if residual is not None else 0, _ptr(out), _ld(out), _stream(y)),
-               "expert_combine")
+        out = torch.empty(want, dtype=torch.bfloat16, device=y.device)
+    _run(lib.expert_combine, "expert_combine", y, y.data_ptr(), y.shape[0], ldy, weights.data_ptr(), slots.data_ptr(),
+         want[0], slots.shape[1], want[1], _ptr(residual), ldr, out.data_ptr(), ldo)
     return out
 
 
@@ -839,22 +884,26 @@ def expert_combine_backward(grad_out, y, weights, slots, grad_y=None):
     grad_out bf16 [T, H] (which is the residual's gradient as it is).  Rows of
     grad_y that no slot names are left as they were (undefined in one
     allocated here); the slots must be distinct, as expert_route's are."""
-    _need(isinstance(grad_out, torch.Tensor) and grad_out.dim() == 2, "grad_out must be a 2-D bf16 tensor")
-    dev = _combine_args(y, weights, slots, grad_out.shape[0])
+    def check():
+        _need(isinstance(grad_out, torch.Tensor) and grad_out.dim() == 2, "grad_out must be a 2-D bf16 tensor")
+        dev = _combine_args(y, weights, slots, grad_out.shape[0])
+        R, H = y.shape
+        _rows_ok("grad_out", grad_out, torch.bfloat16, dev)
+        _need(grad_out.shape[1] == H, f"grad_out must have shape {(slots.shape[0], H)}")
+        if grad_y is not None:
+            _rows_ok("grad_y", grad_y, torch.bfloat16, dev)
+            _need(tuple(grad_y.shape) == (R, H), f"grad_y must have shape {(R, H)}")
+        _need(y.is_cuda, "y must be a CUDA tensor")
+        return _ld(grad_out), _ld(y), H if grad_y is None else _ld(grad_y)
+
+    ldg, ldy, ldgy = _checked(("combine backward", _sig(grad_out), _sig(y), _sig(weights), _sig(slots), _sig(grad_y)),
+                              check)
     (T, top), (R, H) = slots.shape, y.shape
-    _rows_ok("grad_out", grad_out, torch.bfloat16, dev)
-    _need(grad_out.shape[1] == H, f"grad_out must have shape {(T, H)}")
-    if grad_y is not None:
-        _rows_ok("grad_y", grad_y, torch.bfloat16, dev)
-        _need(tuple(grad_y.shape) == (R, H), f"grad_y must have shape {(R, H)}")
-    _need(y.is_cuda, "y must be a CUDA tensor")
     if grad_y is None:
-        grad_y = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    grad_weights = torch.empty((T, top), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib.expert_combine_backward(_ptr(grad_out), _ld(grad_out), _ptr(y), R, _ld(y), _ptr(weights),
-                                           _ptr(slots), T, top, H, _ptr(grad_y), _ld(grad_y), _ptr(grad_weights),
-                                           _stream(y)), "expert_combine_backward")
+        grad_y = torch.empty((R, H), dtype=torch.bfloat16, device=y.device)
+    grad_weights = torch.empty((T, top), dtype=torch.float32, device=y.device)
+    _run(lib.expert_combine_backward, "expert_combine_backward", y, grad_out.data_ptr(), ldg, y.data_ptr(), R, ldy,
+         weights.data_ptr(), slots.data_ptr(), T, top, H, grad_y.data_ptr(), ldgy, grad_weights.data_ptr())
     return grad_y, grad_weights
 
 
