@@ -430,12 +430,13 @@ int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
  *             [T, top], the row of each (token, place), -1 where there is no
  *             expert.  They are gemm_grouped's offsets and row_index and
  *             expert_combine's slots.
- *   ws      : device workspace of at least expert_route_workspace_bytes(T, E)
- *             (any contents; not used without row order; 0 for up to 64
- *             tokens, whose routing is one launch)
+ *   ws      : device workspace of at least expert_order_workspace_bytes(T,
+ *             top, E) (any contents; 0 up to 16384 entries T * top; not used
+ *             without row order)
  * 1 <= E <= 1024, 1 <= top <= min(E, 32), 1 <= groups <= 64 dividing E,
  * 1 <= top_groups <= groups, T * top < 2^31; beyond: SPG_EUNSUPPORTED for
  * E, top and groups too large, else SPG_EINVAL.  scale is any finite number.
+ * Two launches with row order, one without.
  */
 enum {
     SPG_SCORE_SOFTMAX = 0,
@@ -448,7 +449,7 @@ typedef struct spg_route_desc {
     float scale;
 } spg_route_desc;
 
-size_t expert_route_workspace_bytes(int64_t T, int32_t E);
+size_t expert_order_workspace_bytes(int64_t T, int32_t top, int32_t E);
 int expert_route(const void *logits, const float *bias, float *weights, int32_t *experts, int32_t *offsets,
                  int32_t *rows, int32_t *slots, const spg_route_desc *d, void *ws, size_t ws_bytes, void *stream);
 

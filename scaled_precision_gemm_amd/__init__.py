@@ -108,7 +108,7 @@ SIGNATURES = {
     "quantize_block128": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P, ctypes.c_int, _P]),
     "gemm_grouped": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.POINTER(GroupedDesc), _P]),
     "spg_grouped_tile_rows": (ctypes.c_int, [ctypes.POINTER(GroupedDesc), ctypes.c_int]),
-    "expert_route_workspace_bytes": (_SZ, [_I64, _I32]),
+    "expert_order_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "expert_route": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P, _SZ, _P]),
     "expert_sort": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "expert_route_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P]),
@@ -733,11 +733,21 @@ def grouped_tile_rows(rows: int, experts: int, N: int, K: int, epilogue="store")
     return lib.spg_grouped_tile_rows(ctypes.byref(d), epi)
 
 
-def expert_workspace(T: int, E: int, device="cuda"):
-    """A device workspace for the row order of T tokens over E experts, or
-    None when it needs none."""
-    n = lib.expert_route_workspace_bytes(T, E)
+def expert_workspace(T: int, top: int, E: int, device="cuda"):
+    """A device workspace for the row order of T tokens with `top` of E
+    experts each, or None when it needs none."""
+    n = lib.expert_order_workspace_bytes(T, top, E)
     return torch.empty((n,), dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def _order_ws(workspace, n, dev):
+    if n == 0:
+        return None
+    if workspace is None:
+        return torch.empty((n,), dtype=torch.uint8, device=dev)
+    _need(isinstance(workspace, torch.Tensor) and workspace.device == dev and workspace.is_contiguous()
+          and workspace.numel() * workspace.element_size() >= n, f"the workspace must hold {n} bytes on {dev}")
+    return workspace
 
 
 def _route_desc(logits, top, score, groups, top_groups, renormalize, scale):
@@ -751,16 +761,6 @@ def _route_desc(logits, top, score, groups, top_groups, renormalize, scale):
     _need(math.isfinite(scale), "scale must be finite")
     return RouteDesc(T, _ld(logits), E, top, groups, top_groups, _SCORE[score], int(bool(renormalize)),
                      int(logits.dtype == torch.bfloat16), scale)
-
-
-def _order_ws(workspace, n, dev):
-    if n == 0:
-        return None, 0
-    if workspace is None:
-        workspace = torch.empty((n,), dtype=torch.uint8, device=dev)
-    _need(isinstance(workspace, torch.Tensor) and workspace.device == dev and workspace.is_contiguous()
-          and workspace.numel() * workspace.element_size() >= n, f"the workspace must hold {n} bytes on {dev}")
-    return workspace, n
 
 
 def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1, renormalize=True, scale=1.0,
@@ -783,7 +783,7 @@ def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1
                                and bias.is_contiguous()),
               f"bias must be a contiguous fp32 [{d.E}] tensor on {logits.device}")
         _need(logits.is_cuda, "logits must be a CUDA tensor")
-        return d, lib.expert_route_workspace_bytes(d.T, d.E)
+        return d, lib.expert_order_workspace_bytes(d.T, d.top, d.E)
 
     d, nws = _checked(("route", _sig(logits), top, score, _sig(bias), groups, top_groups, bool(renormalize), scale), check)
     dev, T = logits.device, d.T
@@ -793,7 +793,7 @@ def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1
         _run(lib.expert_route, "expert_route", logits, logits.data_ptr(), _ptr(bias), weights.data_ptr(),
              experts.data_ptr(), None, None, None, ctypes.byref(d), None, 0)
         return ExpertRoute(weights, experts, None, None, None)
-    ws, nws = _order_ws(workspace, nws, dev)
+    ws = _order_ws(workspace, nws, dev)
     offsets = torch.empty((d.E + 1,), dtype=torch.int32, device=dev)
     rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
     slots = torch.empty((T, top), dtype=torch.int32, device=dev)
@@ -812,7 +812,8 @@ def expert_sort(experts, n_experts, workspace=None):
     _index("experts", experts, (T, top), dev)
     _need(top >= 1 and n_experts >= 1, "at least one expert")
     _need(experts.is_cuda, "experts must be a CUDA tensor")
-    ws, nws = _order_ws(workspace, lib.expert_route_workspace_bytes(T, n_experts), dev)
+    nws = lib.expert_order_workspace_bytes(T, top, n_experts)
+    ws = _order_ws(workspace, nws, dev)
     offsets = torch.empty((n_experts + 1,), dtype=torch.int32, device=dev)
     rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
     slots = torch.empty((T, top), dtype=torch.int32, device=dev)

@@ -189,10 +189,11 @@ int validate_route(const spg_route_desc *d)
     return SPG_OK;
 }
 
-// The counts of every chunk; none for what one workgroup orders.
-size_t route_ws(int64_t T, int32_t E)
+// The counts of every chunk of tokens.
+size_t order_ws(int64_t T, int32_t top, int32_t E)
 {
-    return T <= kRouteOneLaunch ? 0 : (size_t)cdiv(T, route_chunk(T)) * (size_t)E * sizeof(int32_t);
+    const int32_t chunk = route_chunk(T, top);
+    return chunk == 0 ? 0 : (size_t)cdiv(T, chunk) * (size_t)E * sizeof(int32_t);
 }
 
 RouteArgs route_args(const spg_route_desc *d)
@@ -209,8 +210,6 @@ RouteArgs route_args(const spg_route_desc *d)
     a.bf16 = d->logits_bf16 != 0;
     a.renorm = d->renormalize != 0;
     a.scale = d->scale;
-    a.chunk = (int32_t)route_chunk(d->T);
-    a.chunks = (int32_t)cdiv(d->T, a.chunk);
     a.div_top = make_fastdiv((uint32_t)d->top);
     a.div_group = make_fastdiv((uint32_t)(d->E / d->groups));
     return a;
@@ -218,10 +217,10 @@ RouteArgs route_args(const spg_route_desc *d)
 
 }  // namespace
 
-SPG_EXPORT size_t expert_route_workspace_bytes(int64_t T, int32_t E)
+SPG_EXPORT size_t expert_order_workspace_bytes(int64_t T, int32_t top, int32_t E)
 {
-    if (T <= 0 || E < 1 || E > kRouteMaxExperts || T >= kMaxGrid) return 0;
-    return route_ws(T, E);
+    if (T <= 0 || top < 1 || E < 1 || E > kRouteMaxExperts || T >= kMaxGrid / top) return 0;
+    return order_ws(T, top, E);
 }
 
 SPG_EXPORT int expert_route(const void *logits, const float *bias, float *weights, int32_t *experts, int32_t *offsets,
@@ -240,6 +239,7 @@ SPG_EXPORT int expert_route(const void *logits, const float *bias, float *weight
         !aligned4(slots))
         return SPG_EINVAL;
     RouteArgs a = route_args(d);
+    a.vec = aligned16(logits) && d->ld % (d->logits_bf16 ? 8 : 4) == 0;
     a.logits = logits;
     a.bias = bias;
     a.weights = weights;
@@ -247,12 +247,14 @@ SPG_EXPORT int expert_route(const void *logits, const float *bias, float *weight
     a.offsets = offsets;
     a.rows = rows;
     a.slots = slots;
+    if (order && order_ws(d->T, d->top, d->E) > 0) {
+        if (!ws || ws_bytes < order_ws(d->T, d->top, d->E) || !aligned4(ws)) return SPG_EWORKSPACE;
+        a.hist = (int32_t *)ws;
+        a.chunk = route_chunk(d->T, d->top);
+        a.chunks = (int32_t)cdiv(d->T, a.chunk);
+    }
     // no token: the row order is that of no rows
     if (d->T == 0 && !order) return SPG_OK;
-    if (order && route_ws(d->T, d->E) > 0) {
-        if (!ws || ws_bytes < route_ws(d->T, d->E) || !aligned4(ws)) return SPG_EWORKSPACE;
-        a.hist = (int32_t *)ws;
-    }
     return launch_expert_route(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 
@@ -264,7 +266,8 @@ SPG_EXPORT int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32
     if (T >= kMaxGrid / top) return SPG_EUNSUPPORTED;
     if (!offsets || (T > 0 && (!experts || !rows || !slots))) return SPG_EINVAL;
     if (!aligned4(experts) || !aligned4(offsets) || !aligned4(rows) || !aligned4(slots)) return SPG_EINVAL;
-    if (route_ws(T, E) > 0 && (!ws || ws_bytes < route_ws(T, E) || !aligned4(ws))) return SPG_EWORKSPACE;
+    const size_t need = order_ws(T, top, E);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned4(ws))) return SPG_EWORKSPACE;
     spg_route_desc d;
     memset(&d, 0, sizeof(d));
     d.T = T;
@@ -276,7 +279,11 @@ SPG_EXPORT int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32
     a.offsets = offsets;
     a.rows = rows;
     a.slots = slots;
-    a.hist = (int32_t *)ws;
+    if (need > 0) {
+        a.hist = (int32_t *)ws;
+        a.chunk = route_chunk(T, top);
+        a.chunks = (int32_t)cdiv(T, a.chunk);
+    }
     return launch_expert_sort(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 

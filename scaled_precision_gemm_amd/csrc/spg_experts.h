@@ -16,22 +16,23 @@ struct RouteArgs {
     int32_t *offsets;           // [E + 1], or null: no row order
     int32_t *rows;              // [T * top]
     int32_t *slots;             // [T, top]
-    int32_t *hist;              // workspace [chunks, E]
+    int32_t *hist;              // workspace: counts [chunks, E], or null: none
+    int32_t chunk, chunks;      // tokens of a chunk, chunks
     int64_t T;
     int32_t E, top, groups, top_groups;
     int32_t score, bf16;        // SPG_SCORE_*; logits (and grad_logits) bf16, else fp32
     int32_t renorm;
+    int32_t vec;                // rows of logits 16-byte aligned
     float scale;
-    int32_t chunk;              // tokens per histogram row
-    int32_t chunks;
     FastDiv div_top, div_group; // by top and by E / groups
 };
 
 constexpr int kRouteMaxExperts = 1024, kRouteMaxTop = 32, kRouteMaxGroups = 64;
-constexpr int64_t kRouteOneLaunch = 64;        // tokens routed and ordered by one workgroup
-
-// Chunk length (tokens) of the histogram rows for T tokens.
-int64_t route_chunk(int64_t T);
+// Up to this many entries (tokens x places) every workgroup of the row order
+// counts them all itself; beyond, the route launch leaves counts per chunk.
+constexpr int64_t kRouteSelfCount = 16384;
+// Tokens of a chunk; 0: no counts.
+int32_t route_chunk(int64_t T, int32_t top);
 
 hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s);
 hipError_t launch_expert_sort(const RouteArgs &a, hipStream_t s);

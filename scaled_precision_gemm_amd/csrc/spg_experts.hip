@@ -14,12 +14,15 @@
 // slots that no expert is left for get expert -1 and weight 0.  A NaN logit
 // is not chosen either and makes its token's weights NaN.
 //
-// A team of 16 lanes (64 where E > 256 or top > 16) works on one token; lane
-// l holds the EPL consecutive experts l EPL .., so of equal values the lowest
-// lane has the lowest index.  Each of the `top` rounds takes the team's
-// maximum - of the keys' high words through DPP row operations, then of the
-// low words where more than one lane holds the maximum - and the winner drops
-// its expert.  Four tokens share a wave's rounds.
+// A team of 64 or 16 lanes works on one token; lane l holds the EPL
+// consecutive experts l EPL ...  Each of the `top` rounds takes the team's
+// maximum through DPP row operations - of 32-bit keys where the logits are
+// compared, of the high words of 64-bit keys and, where several experts share
+// it, their low words - and drops the lowest expert that holds it.  No LDS and
+// no divergent code in the rounds: 8 rounds over 256 experts are about 350
+// instructions with 64 lanes (4 keys each) and 800 for four tokens at once
+// with 16 (16 keys each).  Few tokens are bound by one wave's latency and take
+// 64 lanes; many by issue and take 16.
 #include "spg_experts.h"
 #include "spg_gemm_common.h"
 
@@ -39,7 +42,12 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v)
 // the four exchanges that make a value uniform over a row of 16 lanes: with
 // every combine symmetric, all lanes end with the same bits
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+// lane 15 of a row into the next row; lane 31 into rows 2 and 3
+constexpr int kBcast15 = 0x142, kBcast31 = 0x143;
 
+// The maximum over the team, in every lane (all lanes active: row operations
+// read their neighbours).  64 lanes: each row's maximum travels through rows
+// 1, 2, 3 to lane 63.
 template <int TEAM>
 __device__ __forceinline__ uint32_t team_max(uint32_t v)
 {
@@ -48,8 +56,9 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v)
     v = max(v, dpp<kHalfMirror>(v));
     v = max(v, dpp<kMirror>(v));
     if (TEAM == 64) {
-        v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-        v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+        v = max(v, dpp<kBcast15>(v));
+        v = max(v, dpp<kBcast31>(v));
+        v = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
     }
     return v;
 }
@@ -119,40 +128,135 @@ __device__ __forceinline__ float load_logit(const RouteArgs &a, int64_t t, int e
     return ((const float *)a.logits)[t * a.ld + e];
 }
 
-// LDS of one token while it is routed: its choices (groups only), its group
-// scores, then the chosen experts and their scores.
-template <int TEAM>
-struct TokenLds {
-    double score[kRouteMaxGroups];
-    double p[TEAM == 16 ? 16 : kRouteMaxTop];
-    int32_t e[TEAM == 16 ? 16 : kRouteMaxTop];
-    uint64_t kept;
-};
-
-// Routes the token of this team (live: it exists); `c` is room for E doubles
-// when GROUPS.  On return lanes j < top hold weight and expert of choice j.
-// Every lane of the workgroup calls it (it holds barriers).
-template <int TEAM, int EPL, bool BF16, bool PLAIN>
-__device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool live, TokenLds<TEAM> &L, double *c,
-                                            float &w_out, int32_t &e_out)
+// The EPL logits from expert e0 on (-inf past the last expert): 16 bytes a
+// load where rows are 16-byte aligned (a.vec) and the lane's all exist.
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, int64_t t, bool live, int e0, float (&l)[EPL])
 {
-#pragma clang fp contract(off)
-    const int tl = threadIdx.x & (TEAM - 1);
-    using Key = typename std::conditional<PLAIN, uint32_t, uint64_t>::type;
-    float l[EPL];
-    Key key[EPL];
-    float mx = -INFINITY;
-    bool nan = false;
+    constexpr int kPer = BF16 ? 8 : 4;
+    if (EPL % kPer == 0 && a.vec && live && e0 + EPL <= a.E) {
+#pragma unroll
+        for (int v = 0; v < EPL / kPer; ++v) {
+            const uint4 q = BF16 ? *reinterpret_cast<const uint4 *>((const uint16_t *)a.logits + t * a.ld + e0 + v * kPer)
+                                 : *reinterpret_cast<const uint4 *>((const float *)a.logits + t * a.ld + e0 + v * kPer);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (BF16) {
+                    l[(v * kPer + 2 * i) % EPL] = bf16_lo(w[i]);
+                    l[(v * kPer + 2 * i + 1) % EPL] = bf16_hi(w[i]);
+                } else {
+                    l[(v * kPer + i) % EPL] = __uint_as_float(w[i]);
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = live && e0 + i < a.E ? load_logit<BF16>(a, t, e0 + i) : -INFINITY;
+}
+
+// Orders this wave's LDS accesses before and after (teams never span waves).
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The two largest of (a1 >= a2) and (b1 >= b2).
+__device__ __forceinline__ void merge2(double &a1, double &a2, double b1, double b2)
+{
+    const double lo = a1 < b1 ? a1 : b1, hi2 = a2 < b2 ? b2 : a2;
+    a1 = a1 < b1 ? b1 : a1;
+    a2 = lo < hi2 ? hi2 : lo;
+}
+
+// Which of this lane's experts' groups stay: bit i for expert tl EPL + i.
+// c: its choices (-inf where never chosen).  scores: LDS of the token, one
+// double per group; all: LDS of the token, one per expert.
+template <int TEAM, int EPL>
+__device__ __forceinline__ uint32_t kept_experts(const RouteArgs &a, const double (&c)[EPL], volatile double *scores,
+                                                 volatile double *all)
+{
+    const int tl = threadIdx.x & (TEAM - 1), size = a.E / a.groups;
+    const double none = -(double)INFINITY;
+    auto rank = [&](int g, double v) {                    // groups before g
+        int better = 0;
+        for (int h = 0; h < a.groups; ++h) {
+            const double o = scores[h];
+            better += (o > v || (o == v && h < g)) ? 1 : 0;
+        }
+        return better;
+    };
+    const int lanes = size / EPL;
+    if (size % EPL == 0 && (lanes & (lanes - 1)) == 0 && lanes <= TEAM) {
+        // a group is a power of two of whole lanes: two largest in the lane,
+        // then over the group's lanes
+        double m1 = none, m2 = none;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) merge2(m1, m2, c[i], none);
+        auto step = [&](auto ctrl) { merge2(m1, m2, dpp64<decltype(ctrl)::value>(m1), dpp64<decltype(ctrl)::value>(m2)); };
+        if (lanes > 1) step(std::integral_constant<int, kXor1>{});
+        if (lanes > 2) step(std::integral_constant<int, kXor2>{});
+        if (lanes > 4) step(std::integral_constant<int, kHalfMirror>{});
+        if (lanes > 8) step(std::integral_constant<int, kMirror>{});
+        if (lanes > 16) merge2(m1, m2, __shfl_xor(m1, 16, 64), __shfl_xor(m2, 16, 64));
+        if (lanes > 32) merge2(m1, m2, __shfl_xor(m1, 32, 64), __shfl_xor(m2, 32, 64));
+        const int g = tl / lanes;
+        const double v = m2 > none ? m1 + m2 : m1;
+        if (tl % lanes == 0 && g < a.groups) scores[g] = v;
+        wave_sync();
+        return g < a.groups && v > none && rank(g, v) < a.top_groups ? ~0u : 0u;
+    }
+    // groups that cut across lanes: the choices through LDS
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (tl * EPL + i < a.E) all[tl * EPL + i] = c[i];
+    wave_sync();
+    for (int g = tl; g < a.groups; g += TEAM) {
+        double m1 = none, m2 = none;
+        for (int i = 0; i < size; ++i) merge2(m1, m2, all[g * size + i], none);
+        scores[g] = m2 > none ? m1 + m2 : m1;
+    }
+    wave_sync();
+    uint32_t keep = 0;
+    int last = -1;
+    bool in = false;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = tl * EPL + i;
-        l[i] = live && e < a.E ? load_logit<BF16>(a, t, e) : -INFINITY;
+        if (e >= a.E) continue;
+        const int g = (int)fdiv_q((uint32_t)e, a.div_group);
+        if (g != last) {
+            const double v = scores[g];
+            in = v > none && rank(g, v) < a.top_groups;
+            last = g;
+        }
+        keep |= in ? 1u << i : 0u;
+    }
+    return keep;
+}
+
+// Routes token t (live: it exists) with this team; lanes j < top return weight
+// and expert of place j.  scores, all: the team's LDS (GROUPS only).
+template <int TEAM, int EPL, bool BF16, bool PLAIN>
+__device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool live, volatile double *scores,
+                                            volatile double *all, float &w_out, int32_t &e_out)
+{
+#pragma clang fp contract(off)
+    const int tl = threadIdx.x & (TEAM - 1);
+    float l[EPL];
+    float mx = -INFINITY;
+    bool nan = false;
+    load_logits<EPL, BF16>(a, t, live, tl * EPL, l);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
         nan = nan || l[i] != l[i];
         mx = l[i] > mx ? l[i] : mx;
     }
     nan = team_ballot<TEAM>(nan) != 0;
-    // the largest logit (fp32 order through the keys) and the softmax sum
-    {
+    {   // the largest logit, through the keys
         const uint32_t k = team_max<TEAM>(key32(mx));
         mx = k == 0u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
     }
@@ -161,13 +265,15 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool 
     // counts as the only size that matters (1 for it, 0 for the others)
     auto raw = [&](float v) -> double {
         if (!(v > -INFINITY)) return 0.0;
-        if (soft) return v == mx ? 1.0 : exp((double)v - (double)mx);
-        return 1.0 / (1.0 + exp(-(double)v));
+        const double x = soft ? (v == mx ? 0.0 : (double)v - (double)mx) : -(double)v;
+        const double y = exp(x);
+        return soft ? y : 1.0 / (1.0 + y);
     };
     double z = 1.0;
+    uint32_t hi[EPL], lo[PLAIN ? 1 : EPL];
     if (PLAIN) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = key32(l[i]);
+        for (int i = 0; i < EPL; ++i) hi[i] = key32(l[i]);
         if (soft && !a.renorm) {
             double part = 0.0;
 #pragma unroll
@@ -175,106 +281,65 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool 
             z = team_sum<TEAM>(part);
         }
     } else {
-        double p[EPL], part = 0.0;
+        double c[EPL], part = 0.0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            p[i] = raw(l[i]);
-            part += p[i];
+            c[i] = raw(l[i]);
+            part += c[i];
         }
         if (soft) z = team_sum<TEAM>(part);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = tl * EPL + i;
-            double v = soft ? p[i] / z : p[i];
-            if (a.bias && e < a.E) v = v + (double)a.bias[e];
-            if (!(l[i] > -INFINITY)) v = -(double)INFINITY;
-            key[i] = (Key)key64(v);
-            if (a.groups > 1 && e < a.E) c[e] = v;
+            if (soft) c[i] = c[i] / z;
+            if (a.bias && e < a.E) c[i] = c[i] + (double)a.bias[e];
+            if (!(l[i] > -INFINITY && c[i] > -(double)INFINITY)) c[i] = -(double)INFINITY;
         }
-        if (a.groups > 1) {
-            __syncthreads();
-            const int size = a.E / a.groups;
-            for (int gI = tl; gI < a.groups; gI += TEAM) {
-                double m1 = -(double)INFINITY, m2 = m1;
-                for (int i = 0; i < size; ++i) {
-                    const double v = c[gI * size + i];
-                    if (v > m1) {
-                        m2 = m1;
-                        m1 = v;
-                    } else if (v > m2) {
-                        m2 = v;
-                    }
-                }
-                L.score[gI] = m2 > -(double)INFINITY ? m1 + m2 : m1;
-            }
-            if (tl == 0) L.kept = 0;
-            __syncthreads();
-            for (int gI = tl; gI < a.groups; gI += TEAM) {
-                const double v = L.score[gI];
-                int better = 0;
-                for (int h = 0; h < a.groups; ++h) {
-                    const double o = L.score[h];
-                    better += (o > v || (o == v && h < gI)) ? 1 : 0;
-                }
-                if (better < a.top_groups && v > -(double)INFINITY)
-                    atomicOr((unsigned long long *)&L.kept, 1ull << gI);
-            }
-            __syncthreads();
-            const uint64_t kept = L.kept;
+        const uint32_t keep = a.groups > 1 ? kept_experts<TEAM, EPL>(a, c, scores, all) : ~0u;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const uint32_t gI = fdiv_q((uint32_t)(tl * EPL + i), a.div_group);
-                if (gI >= 64u || !((kept >> gI) & 1ull)) key[i] = 0;
-            }
+        for (int i = 0; i < EPL; ++i) {
+            const uint64_t k = (keep >> i) & 1u ? key64(c[i]) : 0ull;
+            hi[i] = (uint32_t)(k >> 32);
+            lo[PLAIN ? 0 : i] = (uint32_t)k;
         }
     }
-    // the rounds
+    // the rounds; a key of 0 (its high word is 0 for nothing else) is never chosen
     int32_t my_e = -1;
     for (int j = 0; j < a.top; ++j) {
-        Key best = key[0];
-        int bi = 0;
+        uint32_t m = hi[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bi = i;
+        for (int i = 1; i < EPL; ++i) m = max(m, hi[i]);
+        m = team_max<TEAM>(m);
+        uint32_t mlo = 0;
+        bool ties = false;
+        if (!PLAIN) {
+            int same = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) same += hi[i] == m ? 1 : 0;
+            const uint64_t who = team_ballot<TEAM>(same > 0);
+            // several experts with this high word in any team of the wave
+            ties = __any(m != 0u && ((who & (who - 1)) != 0 || same > 1)) != 0;
+            if (ties) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) mlo = max(mlo, hi[i] == m ? lo[i] : 0u);
+                mlo = team_max<TEAM>(mlo);
             }
-        bool cand;
-        if (PLAIN) {
-            const uint32_t m = team_max<TEAM>((uint32_t)best);   // in every lane: row operations read all 16
-            cand = best != 0 && best == m;
-        } else {
-            const uint32_t hi = (uint32_t)((uint64_t)best >> 32);
-            const uint32_t mh = team_max<TEAM>(hi);
-            cand = best != 0 && hi == mh;
-            const uint32_t lo = cand ? (uint32_t)best : 0u;
-            const uint32_t ml = team_max<TEAM>(lo);
-            cand = cand && lo == ml;
         }
-        const uint64_t who = team_ballot<TEAM>(cand);
-        const int winner = who ? __builtin_ctzll(who) : -1;
-        if (tl == winner) {
-            L.e[j] = tl * EPL + bi;
+        // the lowest expert that holds the maximum, as the largest ~e
+        uint32_t ne = 0;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (i == bi) {
-                    key[i] = 0;
-                    L.p[j] = raw(l[i]);
-                }
-        } else if (winner < 0 && tl == 0) {
-            L.e[j] = -1;
-            L.p[j] = 0.0;
-        }
+        for (int i = EPL - 1; i >= 0; --i)
+            ne = hi[i] == m && (PLAIN || !ties || lo[PLAIN ? 0 : i] == mlo) ? ~(uint32_t)(tl * EPL + i) : ne;
+        ne = team_max<TEAM>(m != 0u ? ne : 0u);
+        const int32_t e = ne ? (int32_t)~ne : -1;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) hi[i] = tl * EPL + i == e ? 0u : hi[i];
+        my_e = tl == j ? e : my_e;
     }
-    __syncthreads();
-    double pj = 0.0;
-    if (tl < a.top) {
-        pj = L.p[tl];
-        my_e = L.e[tl];
-    }
-    if (soft && !a.renorm) pj = z > 0.0 ? pj / z : 0.0;
-    const double total = a.renorm ? team_sum<TEAM>(pj) : 1.0;
-    double w = total > 0.0 ? (double)a.scale * (pj / total) : 0.0;
+    double p = live && my_e >= 0 ? raw(load_logit<BF16>(a, t, my_e)) : 0.0;
+    if (soft && !a.renorm) p = z > 0.0 ? p / z : 0.0;
+    const double total = a.renorm ? team_sum<TEAM>(p) : 1.0;
+    double w = total > 0.0 ? (double)a.scale * (p / total) : 0.0;
     if (nan) w = __longlong_as_double(0x7FF8000000000000ll);
     w_out = (float)w;
     e_out = my_e;
@@ -293,41 +358,114 @@ __device__ __forceinline__ uint64_t match_expert(int32_t e, bool valid, int bits
     return m;
 }
 
-constexpr int kSortThreads = 1024, kOneThreads = 512;
+constexpr int kOrderThreads = 1024, kOrderWaves = kOrderThreads / 64;
+constexpr int kRouteThreads = 512;
 
-// Ranks entries [n0, n1) of `experts` (flat, token-major) into the row order:
-// base[e] (LDS) is the position of the first of them for expert e.  Each wave
-// takes a contiguous run of entries, counted first (cnt[wave][e]) so that the
-// order is that of the entries.  Entries with no expert get slot -1.
-template <int NT>
-__device__ __forceinline__ void sort_entries(const RouteArgs &a, const int32_t *experts, int64_t n0, int64_t n1,
-                                             int32_t *base, int32_t *cnt)
+// The row order of the n = T top entries of a.experts (flat, token-major), of
+// which workgroup `part` of `parts` places its own: rows of an expert are
+// ordered by entry.  The entries of an expert before and after the part come
+// from the counts of chunks of a.chunk tokens (a.hist, written by the launch
+// before), or, for few entries, every workgroup counts all of them in LDS
+// itself: n / 1024 additions a thread, which collide where experts repeat.
+// Measured behind the route launch (us): 8192 entries 7.2 counted here, 8.2
+// from chunk counts; 65536 entries 21.7 and 8.2.
+__global__ __launch_bounds__(kOrderThreads) void order_kernel(const RouteArgs a)
 {
-    constexpr int kSortWaves = NT / 64;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int E = a.E;
+    extern __shared__ int32_t cnt[];                      // [kOrderWaves][E]
+    __shared__ int32_t before[kRouteMaxExperts], after[kRouteMaxExperts];
+    __shared__ int32_t wsum[kOrderWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E;
     const int bits = 32 - __builtin_clz((unsigned)E);
-    const int64_t n = n1 - n0, per = ((n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-    const int64_t w0 = n0 + min(n, wave * per), w1 = n0 + min(n, (wave + 1) * per);
-    for (int i = tid; i < kSortWaves * E; i += NT) cnt[i] = 0;
+    const int32_t *experts = a.experts;
+    const int part = blockIdx.x, parts = gridDim.x;
+    const int64_t n = a.T * a.top;
+    int64_t n0, n1;
+    int c0 = 0, c1 = 0;                                   // this part's chunks
+    if (a.hist) {
+        const int per = (a.chunks + parts - 1) / parts;
+        c0 = min(a.chunks, part * per);
+        c1 = min(a.chunks, c0 + per);
+        n0 = min(n, (int64_t)c0 * a.chunk * a.top);
+        n1 = min(n, (int64_t)c1 * a.chunk * a.top);
+    } else {
+        const int64_t step = (n + parts - 1) / parts;
+        n0 = min(n, part * step);
+        n1 = min(n, n0 + step);
+    }
+    const int64_t per = ((n1 - n0 + kOrderWaves - 1) / kOrderWaves + 63) / 64 * 64;
+    const int64_t w0 = min(n1, n0 + wave * per), w1 = min(n1, w0 + per);
+    for (int i = tid; i < kOrderWaves * E; i += kOrderThreads) cnt[i] = 0;
+    for (int e = tid; e < E; e += kOrderThreads) before[e] = after[e] = 0;
     __syncthreads();
     int32_t *mine = cnt + wave * E;
     for (int64_t i = w0 + lane; i < w1; i += 64) {
         const int32_t e = experts[i];
         if ((uint32_t)e < (uint32_t)E) atomicAdd(&mine[e], 1);
     }
-    __syncthreads();
-    for (int e = tid; e < E; e += NT) {
-        int32_t at = base[e];
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int32_t c = cnt[w * E + e];
-            cnt[w * E + e] = at;
-            at += c;
+    if (a.hist) {
+        // threads q, q + E', q + 2 E' ... (E' = E rounded up to a power of
+        // two) share expert q's chunks
+        const int e2 = 1 << (E > 1 ? 32 - __builtin_clz((unsigned)(E - 1)) : 0);
+        const int e = tid & (e2 - 1), first = tid / e2, step = kOrderThreads / e2;
+        if (e < E) {
+            int32_t b = 0, f = 0;
+#pragma unroll 8
+            for (int c = first; c < a.chunks; c += step) {
+                const int32_t v = a.hist[(int64_t)c * E + e];
+                b += c < c0 ? v : 0;
+                f += c >= c1 ? v : 0;
+            }
+            if (b) atomicAdd(&before[e], b);
+            if (f) atomicAdd(&after[e], f);
+        }
+    } else {
+        for (int64_t i = tid; i < n0; i += kOrderThreads) {
+            const int32_t e = experts[i];
+            if ((uint32_t)e < (uint32_t)E) atomicAdd(&before[e], 1);
+        }
+        for (int64_t i = n1 + tid; i < n; i += kOrderThreads) {
+            const int32_t e = experts[i];
+            if ((uint32_t)e < (uint32_t)E) atomicAdd(&after[e], 1);
         }
     }
     __syncthreads();
-    // the next position of each expert, read and written by lanes of one wave
-    volatile int32_t *next = mine;
+    // rows of experts below e: a scan over the experts (one per thread)
+    int32_t own = 0, all = 0;
+    if (tid < E) {
+#pragma unroll
+        for (int w = 0; w < kOrderWaves; ++w) own += cnt[w * E + tid];
+        all = before[tid] + own + after[tid];
+    }
+    int32_t sum = all;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int32_t o = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += o;
+    }
+    if (lane == 63) wsum[wave] = sum;
+    __syncthreads();
+    int32_t at = sum - all, total = 0;
+#pragma unroll
+    for (int w = 0; w < kOrderWaves; ++w) {
+        at += w < wave ? wsum[w] : 0;
+        total += wsum[w];
+    }
+    if (tid < E) {
+        if (part == 0) a.offsets[tid] = at;
+        int32_t pos = at + before[tid];
+#pragma unroll
+        for (int w = 0; w < kOrderWaves; ++w) {           // where each wave's first entry goes
+            const int32_t c = cnt[w * E + tid];
+            cnt[w * E + tid] = pos;
+            pos += c;
+        }
+    }
+    if (part == 0) {
+        if (tid == 0) a.offsets[E] = total;
+        for (int64_t i = total + tid; i < n; i += kOrderThreads) a.rows[i] = -1;
+    }
+    __syncthreads();
+    volatile int32_t *next = mine;                        // read and written by lanes of this wave
     for (int64_t i0 = w0; i0 < w1; i0 += 64) {
         const int64_t i = i0 + lane;
         const int32_t e = i < w1 ? experts[i] : -1;
@@ -335,190 +473,61 @@ __device__ __forceinline__ void sort_entries(const RouteArgs &a, const int32_t *
         const uint64_t same = match_expert(e, valid, bits);
         int32_t pos = -1;
         if (valid) {
-            const uint64_t below = same & ((1ull << lane) - 1);
-            pos = next[e] + __popcll(below);
+            pos = next[e] + __popcll(same & ((1ull << lane) - 1));
             a.rows[pos] = (int32_t)fdiv_q((uint32_t)i, a.div_top);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (valid && (same >> lane) == 1ull) next[e] = pos + 1;      // the last lane of its expert
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (i < w1) a.slots[i] = pos;
     }
 }
 
-// start[e] = rows of experts below e, for the totals in start; returns
-// (in every thread) the sum.
-template <int NT>
-__device__ __forceinline__ int32_t exclusive_scan(int32_t *start, int E, int32_t *wsum)
-{
-    constexpr int kWaves = NT / 64, kPer = kRouteMaxExperts / NT;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int32_t v[kPer], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        v[i] = tid * kPer + i < E ? start[tid * kPer + i] : 0;
-        mine += v[i];
-    }
-    int32_t s = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int32_t o = __shfl_up(s, off, 64);
-        if (lane >= off) s += o;
-    }
-    if (lane == 63) wsum[wave] = s;
-    __syncthreads();
-    int32_t at = s - mine, all = 0;
-    for (int w = 0; w < kWaves; ++w) {
-        at += w < wave ? wsum[w] : 0;
-        all += wsum[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (tid * kPer + i < E) start[tid * kPer + i] = at;
-        at += v[i];
-    }
-    __syncthreads();
-    return all;
-}
-
-// Tokens in order, one team each; a workgroup takes `chunk` tokens and counts
-// its experts for the row order.
+// One team per token; a workgroup takes a chunk of a.chunk tokens (with
+// a.hist it counts its experts), else as many as it has teams.
 template <int TEAM, int EPL, bool BF16, bool PLAIN>
-__global__ __launch_bounds__(kThreads) void route_kernel(const RouteArgs a)
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
 {
-    constexpr int TOK = kThreads / TEAM;
-    __shared__ TokenLds<TEAM> lds_t[TOK];
-    extern __shared__ double lds_c[];
+    constexpr int TOK = kRouteThreads / TEAM;
+    extern __shared__ double lds_dyn[];                   // groups: scores [TOK][groups], choices [TOK][E]
     __shared__ int32_t lds_h[kRouteMaxExperts];
-    const int tid = threadIdx.x, tl = tid & (TEAM - 1), team = tid / TEAM;
+    const int tid = threadIdx.x, team = tid / TEAM, tl = tid & (TEAM - 1);
     const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    const bool count = a.offsets != nullptr;
-    if (count) {
-        for (int e = tid; e < a.E; e += kThreads) lds_h[e] = 0;
+    if (a.hist) {
+        for (int e = tid; e < a.E; e += kRouteThreads) lds_h[e] = 0;
         __syncthreads();
     }
     for (int64_t tb = t0; tb < t1; tb += TOK) {
         const int64_t t = tb + team;
-        const bool live = t < t1;
         float w;
         int32_t e;
-        route_token<TEAM, EPL, BF16, PLAIN>(a, t, live, lds_t[team], lds_c + (int64_t)team * a.E, w, e);
-        if (live && tl < a.top) {
+        route_token<TEAM, EPL, BF16, PLAIN>(a, t, t < t1, lds_dyn + team * a.groups,
+                                            lds_dyn + TOK * a.groups + (int64_t)team * a.E, w, e);
+        if (t < t1 && tl < a.top) {
             a.weights[t * a.top + tl] = w;
             a.experts[t * a.top + tl] = e;
-            if (count && e >= 0) atomicAdd(&lds_h[e], 1);
+            if (a.hist && e >= 0) atomicAdd(&lds_h[e], 1);
         }
-        __syncthreads();
     }
-    if (count)
-        for (int e = tid; e < a.E; e += kThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = lds_h[e];
+    if (a.hist) {
+        __syncthreads();
+        for (int e = tid; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = lds_h[e];
+    }
 }
 
-// The same for at most kRouteOneLaunch tokens in one workgroup, the row order
-// included: a decode step's routing is one launch.
-template <int TEAM, int EPL, bool BF16, bool PLAIN>
-__global__ __launch_bounds__(kOneThreads) void route_one_kernel(const RouteArgs a)
-{
-    constexpr int TOK = kOneThreads / TEAM;
-    __shared__ TokenLds<TEAM> lds_t[TOK];
-    __shared__ int32_t lds_e[kRouteOneLaunch * kRouteMaxTop];
-    __shared__ int32_t lds_start[kRouteMaxExperts];
-    __shared__ int32_t lds_wsum[kOneThreads / 64];
-    extern __shared__ double lds_dyn[];
-    const int tid = threadIdx.x, tl = tid & (TEAM - 1), team = tid / TEAM;
-    for (int e = tid; e < a.E; e += kOneThreads) lds_start[e] = 0;
-    __syncthreads();
-    for (int64_t tb = 0; tb < a.T; tb += TOK) {
-        const int64_t t = tb + team;
-        const bool live = t < a.T;
-        float w;
-        int32_t e;
-        route_token<TEAM, EPL, BF16, PLAIN>(a, t, live, lds_t[team], lds_dyn + (int64_t)team * a.E, w, e);
-        if (live && tl < a.top) {
-            a.weights[t * a.top + tl] = w;
-            a.experts[t * a.top + tl] = e;
-            lds_e[t * a.top + tl] = e;
-            if (e >= 0) atomicAdd(&lds_start[e], 1);
-        }
-        __syncthreads();
-    }
-    if (a.offsets == nullptr) return;
-    const int32_t all = exclusive_scan<kOneThreads>(lds_start, a.E, lds_wsum);
-    for (int e = tid; e < a.E; e += kOneThreads) a.offsets[e] = lds_start[e];
-    if (tid == 0) a.offsets[a.E] = all;
-    const int64_t n = a.T * a.top;
-    for (int64_t i = all + tid; i < n; i += kOneThreads) a.rows[i] = -1;
-    sort_entries<kOneThreads>(a, lds_e, 0, n, lds_start, (int32_t *)lds_dyn);
-}
-
-// Experts of one chunk of tokens counted (the row order of given experts).
-__global__ __launch_bounds__(kThreads) void count_kernel(const RouteArgs a)
+// The experts of each chunk of tokens counted (for experts chosen elsewhere).
+__global__ __launch_bounds__(kRouteThreads) void count_kernel(const RouteArgs a)
 {
     __shared__ int32_t lds_h[kRouteMaxExperts];
-    for (int e = threadIdx.x; e < a.E; e += kThreads) lds_h[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) lds_h[e] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    for (int64_t i = t0 * a.top + threadIdx.x; i < t1 * a.top; i += kThreads) {
+    for (int64_t i = t0 * a.top + threadIdx.x; i < t1 * a.top; i += kRouteThreads) {
         const int32_t e = a.experts[i];
         if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&lds_h[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = lds_h[e];
-}
-
-// The row order of at most kRouteOneLaunch tokens' experts, in one workgroup.
-__global__ __launch_bounds__(kOneThreads) void sort_one_kernel(const RouteArgs a)
-{
-    __shared__ int32_t lds_start[kRouteMaxExperts];
-    __shared__ int32_t lds_wsum[kOneThreads / 64];
-    extern __shared__ double lds_dyn[];
-    const int tid = threadIdx.x;
-    const int64_t n = a.T * a.top;
-    for (int e = tid; e < a.E; e += kOneThreads) lds_start[e] = 0;
-    __syncthreads();
-    for (int64_t i = tid; i < n; i += kOneThreads) {
-        const int32_t e = a.experts[i];
-        if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&lds_start[e], 1);
-    }
-    __syncthreads();
-    const int32_t all = exclusive_scan<kOneThreads>(lds_start, a.E, lds_wsum);
-    for (int e = tid; e < a.E; e += kOneThreads) a.offsets[e] = lds_start[e];
-    if (tid == 0) a.offsets[a.E] = all;
-    for (int64_t i = all + tid; i < n; i += kOneThreads) a.rows[i] = -1;
-    sort_entries<kOneThreads>(a, a.experts, 0, n, lds_start, (int32_t *)lds_dyn);
-}
-
-// Row order from the chunks' counts: every workgroup sums the counts of the
-// chunks before its own (and of all, for the experts' starts) and ranks its
-// own chunk's entries.
-__global__ __launch_bounds__(kSortThreads) void order_kernel(const RouteArgs a)
-{
-    extern __shared__ double lds_dyn[];
-    __shared__ int32_t lds_start[kRouteMaxExperts];
-    __shared__ int32_t lds_wsum[kSortThreads / 64];
-    const int tid = threadIdx.x;
-    int32_t before = 0, total = 0;
-    if (tid < a.E)
-#pragma unroll 8
-        for (int c = 0; c < a.chunks; ++c) {
-            const int32_t v = a.hist[(int64_t)c * a.E + tid];
-            before += c < (int)blockIdx.x ? v : 0;
-            total += v;
-        }
-    if (tid < a.E) lds_start[tid] = total;
-    __syncthreads();
-    const int32_t all = exclusive_scan<kSortThreads>(lds_start, a.E, lds_wsum);
-    const int64_t n = a.T * a.top;
-    if (blockIdx.x == 0) {
-        if (tid < a.E) a.offsets[tid] = lds_start[tid];
-        if (tid == 0) a.offsets[a.E] = all;
-        for (int64_t i = all + tid; i < n; i += kSortThreads) a.rows[i] = -1;
-    }
-    __syncthreads();
-    if (tid < a.E) lds_start[tid] += before;
-    __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * a.chunk, t1 = min(a.T, t0 + a.chunk);
-    sort_entries<kSortThreads>(a, a.experts, t0 * a.top, t1 * a.top, lds_start, (int32_t *)lds_dyn);
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = lds_h[e];
 }
 
 // ---- gradient of the logits --------------------------------------------------
@@ -579,19 +588,40 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
             mine = g * p * n;
         }
     }
-    for (int i0 = 0; i0 < a.E; i0 += 64) {
-        const int i = i0 + lane;
-        float v = dense && i < a.E ? -ex(load_logit<BF16>(a, t, i)) * rz * common : 0.0f;
+    // four columns per lane, every choice compared with each
+    const bool vec = a.E % 4 == 0 && ((uintptr_t)a.grad_logits & (BF16 ? 7u : 15u)) == 0;
+    for (int i0 = 0; i0 < a.E; i0 += 256) {
+        const int i = i0 + 4 * lane;
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            v[c] = dense && i + c < a.E ? -ex(load_logit<BF16>(a, t, i + c)) * rz * common : 0.0f;
         for (int j = 0; j < a.top; ++j) {
-            const int32_t ej = __shfl(e, j, 64);
-            const float mj = __shfl(mine, j, 64);
-            if (ej == i) v += mj;
+            const int32_t ej = __builtin_amdgcn_readlane(e, j) - i;
+            const float mj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), j));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] += ej == c ? mj : 0.0f;
         }
-        if (i < a.E) {
-            if (BF16)
-                ((uint16_t *)a.grad_logits)[t * a.E + i] = (uint16_t)f32_to_bf16(v);
-            else
-                ((float *)a.grad_logits)[t * a.E + i] = v;
+        if (i >= a.E) continue;
+        const int64_t at = t * a.E + i;
+        if (BF16) {
+            uint16_t *o = (uint16_t *)a.grad_logits + at;
+            if (vec) {
+                *reinterpret_cast<uint2 *>(o) = make_uint2(gemm::pack_bf16x2(v[0], v[1]), gemm::pack_bf16x2(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (i + c < a.E) o[c] = (uint16_t)f32_to_bf16(v[c]);
+            }
+        } else {
+            float *o = (float *)a.grad_logits + at;
+            if (vec) {
+                *reinterpret_cast<v4f *>(o) = v4f{v[0], v[1], v[2], v[3]};
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (i + c < a.E) o[c] = v[c];
+            }
         }
     }
 }
@@ -748,32 +778,49 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(const Combin
     }
 }
 
-template <int TEAM, int EPL, bool BF16, bool PLAIN>
-hipError_t launch_route(const RouteArgs &a, hipStream_t s)
+hipError_t launch_order(const RouteArgs &a, hipStream_t s)
 {
-    if (a.T <= kRouteOneLaunch) {
-        const size_t choices = a.groups > 1 ? (size_t)(kOneThreads / TEAM) * a.E * sizeof(double) : 0;
-        const size_t counts = a.offsets ? (size_t)(kOneThreads / 64) * a.E * sizeof(int32_t) : 0;
-        route_one_kernel<TEAM, EPL, BF16, PLAIN>
-            <<<1, kOneThreads, choices > counts ? choices : counts, s>>>(a);
-        return hipGetLastError();
-    }
-    const size_t choices = a.groups > 1 ? (size_t)(kThreads / TEAM) * a.E * sizeof(double) : 0;
-    route_kernel<TEAM, EPL, BF16, PLAIN><<<(unsigned)a.chunks, kThreads, choices, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.offsets == nullptr) return e;
-    order_kernel<<<(unsigned)a.chunks, kSortThreads, (size_t)(kSortThreads / 64) * a.E * sizeof(int32_t), s>>>(a);
+    // parts of at least 1024 entries (one step of every wave), at most 64,
+    // and with chunk counts at most one per chunk
+    int64_t parts = (a.T * a.top + 1023) / 1024;
+    parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
+    if (a.hist && parts > a.chunks) parts = a.chunks;
+    order_kernel<<<(unsigned)parts, kOrderThreads, (size_t)kOrderWaves * a.E * sizeof(int32_t), s>>>(a);
     return hipGetLastError();
 }
+
+template <int TEAM, int EPL, bool BF16, bool PLAIN>
+hipError_t launch_route(const RouteArgs &in, hipStream_t s)
+{
+    constexpr int TOK = kRouteThreads / TEAM;
+    RouteArgs a = in;
+    if (a.hist == nullptr) {
+        a.chunk = TOK;
+        a.chunks = (int32_t)((a.T + TOK - 1) / TOK);
+    }
+    if (a.T > 0) {
+        const size_t choices = a.groups > 1 ? (size_t)TOK * (a.groups + a.E) * sizeof(double) : 0;
+        route_kernel<TEAM, EPL, BF16, PLAIN><<<(unsigned)a.chunks, kRouteThreads, choices, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return a.offsets != nullptr ? launch_order(a, s) : hipSuccess;
+}
+
+// 64 lanes a token up to kRouteWide tokens (four waves a SIMD), and where 16
+// lanes could not hold the experts or the places.
+constexpr int64_t kRouteWide = 4096;
 
 template <bool BF16, bool PLAIN>
 hipError_t launch_route_size(const RouteArgs &a, hipStream_t s)
 {
-    if (a.top <= 16) {
+    if (a.T > kRouteWide && a.top <= 16) {
         if (a.E <= 64) return launch_route<16, 4, BF16, PLAIN>(a, s);
         if (a.E <= 128) return launch_route<16, 8, BF16, PLAIN>(a, s);
         if (a.E <= 256) return launch_route<16, 16, BF16, PLAIN>(a, s);
     }
+    if (a.E <= 64) return launch_route<64, 1, BF16, PLAIN>(a, s);
+    if (a.E <= 128) return launch_route<64, 2, BF16, PLAIN>(a, s);
     if (a.E <= 256) return launch_route<64, 4, BF16, PLAIN>(a, s);
     if (a.E <= 512) return launch_route<64, 8, BF16, PLAIN>(a, s);
     return launch_route<64, 16, BF16, PLAIN>(a, s);
@@ -783,12 +830,14 @@ bool aligned16(const void *p, int64_t ld) { return ((uintptr_t)p & 15) == 0 && (
 
 }  // namespace
 
-// At most 256 chunks, so the sums over the chunks' counts stay short, and at
-// least 64 tokens each.
-int64_t route_chunk(int64_t T)
+// Chunks of the row order's counts: whole rounds of a route workgroup's teams
+// (32 tokens of 16 lanes, 8 of 64), at most 256 chunks, since every part of
+// the row order sums them all.
+int32_t route_chunk(int64_t T, int32_t top)
 {
-    const int64_t c = (T + 255) / 256;
-    return c < 64 ? 64 : c;
+    if (T * top <= kRouteSelfCount) return 0;
+    const int64_t unit = T > kRouteWide ? 32 : 8, c = (T + 255) / 256;
+    return (int32_t)((c + unit - 1) / unit * unit);
 }
 
 hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s)
@@ -800,15 +849,12 @@ hipError_t launch_expert_route(const RouteArgs &a, hipStream_t s)
 
 hipError_t launch_expert_sort(const RouteArgs &a, hipStream_t s)
 {
-    if (a.T <= kRouteOneLaunch) {
-        sort_one_kernel<<<1, kOneThreads, (size_t)(kOneThreads / 64) * a.E * sizeof(int32_t), s>>>(a);
-        return hipGetLastError();
+    if (a.hist) {
+        count_kernel<<<(unsigned)a.chunks, kRouteThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    count_kernel<<<(unsigned)a.chunks, kThreads, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    order_kernel<<<(unsigned)a.chunks, kSortThreads, (size_t)(kSortThreads / 64) * a.E * sizeof(int32_t), s>>>(a);
-    return hipGetLastError();
+    return launch_order(a, s);
 }
 
 hipError_t launch_expert_route_backward(const RouteArgs &a, hipStream_t s)

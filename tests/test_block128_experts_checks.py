@@ -127,24 +127,27 @@ def route(d, logits=FAKE, bias=None, w=FAR, x=FAR, off=FAR, rows=FAR, slots=FAR,
     (dict(top=33), {}, EUNSUP), (dict(E=128, ld=128, groups=128), {}, EUNSUP), (dict(T=2 ** 28), {}, EUNSUP),
     ({}, dict(logits=None), EINVAL), ({}, dict(w=None), EINVAL), ({}, dict(x=None), EINVAL), ({}, dict(off=None), EINVAL),
     ({}, dict(rows=None), EINVAL), ({}, dict(slots=None), EINVAL), ({}, dict(logits=MIS4), EINVAL),
-    ({}, dict(bias=MIS4), EINVAL), ({}, dict(ws=None), EWS), ({}, dict(nws=2 * 64 * 4 - 1), EWS), ({}, dict(ws=MIS4), EWS),
+    ({}, dict(bias=MIS4), EINVAL), ({}, dict(slots=MIS4), EINVAL), (dict(T=2100), dict(ws=None), EWS),
+    (dict(T=2100), dict(nws=132 * 64 * 4 - 1), EWS), (dict(T=2100), dict(ws=MIS4), EWS),
     (dict(T=0), dict(off=None, rows=None, slots=None), 0),
 ])
 def test_route_refusals(kw, call, want):
     assert route(route_desc(**kw), **call) == want
 
 
-def test_route_workspace():
-    n = spg.lib.expert_route_workspace_bytes
-    assert n(64, 256) == 0 and n(65, 256) == 2 * 256 * 4 and n(0, 8) == 0 and n(100, 0) == 0 and n(100, 1025) == 0
-    assert n(10 ** 6, 1024) == 256 * 1024 * 4
+def test_order_workspace():
+    n = spg.lib.expert_order_workspace_bytes
+    assert n(2048, 8, 256) == 0 and n(0, 8, 8) == 0 and n(3000, 8, 0) == 0 and n(3000, 8, 1025) == 0 and n(3000, 0, 8) == 0
+    assert n(2049, 8, 256) == 129 * 256 * 4                    # chunks of 16 tokens
+    assert n(8192, 8, 128) == 256 * 128 * 4                    # of 32
+    assert n(10 ** 6, 8, 1024) == 255 * 1024 * 4               # of 3936: at most 256 chunks
 
 
 def test_sort_and_backward_refusals():
     sort = lambda x=FAKE, T=100, top=4, E=64, off=FAR, rows=FAR, slots=FAR, ws=FAR, nws=1 << 20: spg.lib.expert_sort(  # noqa: E731
         x, T, top, E, off, rows, slots, ws, nws, None)
     assert [sort(T=-1), sort(top=0), sort(E=0), sort(x=None), sort(off=None), sort(rows=None), sort(slots=None),
-            sort(x=MIS4), sort(E=1025), sort(T=2 ** 30), sort(ws=None), sort(nws=8)] == \
+            sort(x=MIS4), sort(E=1025), sort(T=2 ** 30), sort(T=5000, ws=None), sort(T=5000, nws=8)] == \
         [EINVAL] * 8 + [EUNSUP] * 2 + [EWS] * 2
     back = lambda d, g=FAR, l=FAKE, x=FAR, o=P(0x8000000): spg.lib.expert_route_backward(g, l, x, o, ctypes.byref(d), None)  # noqa: E731,E741
     assert [back(route_desc(top=33)), back(route_desc(top=65)), back(route_desc(), g=None), back(route_desc(), l=None),

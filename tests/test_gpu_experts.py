@@ -213,19 +213,22 @@ def check_order(experts, E, offsets, rows, slots):
 def check_route(spg, x, top, **how):
     """x: fp32 values [T, E], exact in bf16 too; both logit types."""
     bias = how.get("bias")
-    W, X, _ = route_ref(x, top, how.get("score", "softmax"), bias, how.get("groups", 1), how.get("top_groups", 1),
+    # of many tokens, the first and the last ones
+    some = np.arange(len(x)) if len(x) <= 300 else np.r_[0:60, len(x) - 60:len(x)]
+    W, X, _ = route_ref(x[some], top, how.get("score", "softmax"), bias, how.get("groups", 1), how.get("top_groups", 1),
                         how.get("renormalize", True), how.get("scale", 1.0))
     if bias is not None:
         how = dict(how, bias=torch.from_numpy(bias).cuda())
     for dt in (torch.float32, torch.bfloat16):
         r = spg.expert_route(torch.from_numpy(x).cuda().to(dt), top, **how)
-        got = r.experts.cpu().numpy()
+        ids = r.experts.cpu().numpy()
+        got = ids[some]
         assert np.array_equal(got, X), f"experts differ at {np.argwhere(got != X)[:5].tolist()}"
-        w = r.weights.cpu().numpy()
+        w = r.weights.cpu().numpy()[some]
         assert np.array_equal(np.isnan(w), np.isnan(W))
         # fp64 scores (a few 2^-52) and one rounding to fp32, half a step 2^-24
         np.testing.assert_allclose(w, W, rtol=1.01 * 2.0 ** -24, atol=2.0 ** -140)
-        check_order(got, x.shape[1], r.offsets, r.rows, r.slots)
+        check_order(ids, x.shape[1], r.offsets, r.rows, r.slots)
 
 
 def logits(T, E, seed, std=1.5):
@@ -235,17 +238,18 @@ def logits(T, E, seed, std=1.5):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,top", [(1, 1), (2, 2), (7, 3), (60, 4), (64, 8), (65, 6), (128, 8), (160, 16), (256, 17),
                                    (257, 8), (512, 10), (1000, 32), (1024, 2)])
-@pytest.mark.parametrize("T", [3, 130])
+@pytest.mark.parametrize("T", [3, 130, 4100])
 def test_route_sizes(spg, score, E, top, T):
     check_route(spg, logits(T, E, E), top, score=score)
     check_route(spg, logits(T, E, E + 1), top, score=score, renormalize=False, scale=2.5,
                 bias=(0.3 * np.random.default_rng(E).standard_normal(E)).astype(np.float32))
 
 
-@pytest.mark.parametrize("T", [0, 1, 16, 63, 64, 65, 1000, 16500])
+@pytest.mark.parametrize("T", [0, 1, 16, 129, 1000, 2048, 2049, 4500, 16500])
 def test_route_token_counts(spg, T):
-    # one launch up to 64 tokens; counted in chunks beyond, and chunks longer
-    # than 64 tokens from 16385 on
+    # 64 lanes a token up to 4096 and 16 beyond; the row order counted by
+    # itself up to 16384 entries (2048 tokens), from counts of chunks
+    # beyond, of more than 32 tokens past 8192
     x = logits(T, 64, T)
     if T > 2000:
         r = spg.expert_route(torch.from_numpy(x).cuda(), 8)
@@ -260,14 +264,14 @@ def test_route_token_counts(spg, T):
 @pytest.mark.parametrize("E,groups,top_groups,top", [(256, 8, 4, 8), (160, 8, 3, 6), (60, 4, 1, 4), (64, 64, 9, 9),
                                                      (512, 16, 5, 20), (96, 3, 3, 8), (8, 2, 1, 4)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("T", [5, 70, 4200])
 def test_route_groups(spg, E, groups, top_groups, top, score, T):
     bias = (0.2 * np.random.default_rng(E).standard_normal(E)).astype(np.float32)
     for b in (None, bias):
         check_route(spg, logits(T, E, groups), top, score=score, groups=groups, top_groups=top_groups, bias=b, scale=2.5)
 
 
-@pytest.mark.parametrize("T", [40, 200])
+@pytest.mark.parametrize("T", [10, 200, 4200])
 def test_route_ties_go_to_the_lowest_index(spg, T):
     x = np.random.default_rng(5).integers(-1, 2, (T, 96)).astype(np.float32)
     x[0] = 0
@@ -279,7 +283,7 @@ def test_route_ties_go_to_the_lowest_index(spg, T):
         check_route(spg, x, 12, score=score, bias=np.zeros(96, np.float32))
 
 
-@pytest.mark.parametrize("T", [12, 100])
+@pytest.mark.parametrize("T", [12, 100, 4200])
 def test_route_masks(spg, T):
     # masked experts, rows with fewer experts left than places, rows with
     # none, values of the type's lowest, infinite logits, NaN
@@ -309,10 +313,17 @@ def test_route_strided_logits_and_no_order(spg):
     W, X, _ = route_ref(x, 6)
     r = spg.expert_route(wide[:, 33:161], 6, order=False)
     assert np.array_equal(r.experts.cpu().numpy(), X) and r.offsets is None and r.rows is None and r.slots is None
-    ws = spg.expert_workspace(90, 128)
-    r2 = spg.expert_route(wide[:, 33:161], 6, workspace=ws)
+    assert spg.expert_workspace(90, 6, 128) is None
+    r2 = spg.expert_route(wide[:, 33:161], 6)
     assert torch.equal(r2.weights, r.weights)
     check_order(X, 128, r2.offsets, r2.rows, r2.slots)
+    x = torch.from_numpy(logits(3000, 128, 4)).cuda()      # a given workspace, whatever it holds
+    ws = spg.expert_workspace(3000, 6, 128)
+    ws.fill_(0xA5)
+    r, r2 = spg.expert_route(x, 6), spg.expert_route(x, 6, workspace=ws)
+    for a, b in zip(r, r2):
+        assert torch.equal(a, b)
+    check_order(r.experts.cpu().numpy(), 128, r.offsets, r.rows, r.slots)
 
 
 @pytest.mark.parametrize("T,top,E", [(1, 1, 1), (7, 3, 5), (64, 8, 256), (65, 8, 256), (3000, 5, 1000), (17000, 2, 33)])
