@@ -293,8 +293,11 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(P[m & 3][e], fy[m % Y_], c[e]);
         asm volatile("" : "+v"(c));
     };
+    // a strip past the tile's last row only copies and waits with the others:
+    // a tile of at most BM / 2 rows has one wave per SIMD at work
+    const bool busy = wm * G::kStrip < (int)a_rows;
     int slot = 0;
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = 0; kt < (busy ? nk : 0); ++kt) {
         const int next = slot + 1 == G::kDepth ? 0 : slot + 1;
         const StageCopy c = plan(kt + G::kDepth);
 #pragma unroll
@@ -327,10 +330,18 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         }
         slot = next;
     }
-    if (nk > 0) {
+    if (nk > 0 && busy) {
         add(kM - 3);
         add(kM - 2);
         add(kM - 1);
+    }
+    for (int kt = 0; kt < (busy ? 0 : nk); ++kt) {
+        const StageCopy c = plan(kt + G::kDepth);
+        wait_vmem<(G::kDepth - 2) * G::kCopies>();
+        block_barrier();
+#pragma unroll
+        for (int idx = 0; idx < G::kCopies; ++idx) issue_one(c, slot, idx);
+        slot = slot + 1 == G::kDepth ? 0 : slot + 1;
     }
     wait_vmem<0>();
     wait_lds();
