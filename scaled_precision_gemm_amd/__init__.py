@@ -727,7 +727,7 @@ def gemm_grouped(A, sa, W, sw, offsets, epilogue="store", rows=None, out=None):
 
 
 def grouped_tile_rows(rows: int, experts: int, N: int, K: int, epilogue="store") -> int:
-    """Rows of the tiles gemm_grouped takes (16, 32, 128 or 256)."""
+    """Rows of the tiles gemm_grouped takes (16, 128 or 256)."""
     epi = _EPI.get(epilogue, epilogue)
     d = GroupedDesc(rows, rows, N, K, K, K, N * K, N // 2 if epi == EPI_SWIGLU else N, experts, 0)
     return lib.spg_grouped_tile_rows(ctypes.byref(d), epi)

@@ -59,14 +59,19 @@ namespace {
 
 int64_t grouped_nout(const spg_grouped_desc *d, int epi) { return epi == SPG_EPI_SWIGLU ? d->N / 2 : d->N; }
 
-// Tile rows from the mean rows of an expert; tiles of 16 and 32 rows stream
-// the weights (decode), the larger ones feed the matrix cores.
+// Tile rows from the mean rows of an expert.  Tiles of 16 rows stream the
+// weights with many small workgroups (decode): up to 4 rows, or up to 8 where
+// 128-row tiles would leave compute units idle.  Measured (us, cold weights;
+// 16-, 128-, 256-row tiles): 64 experts of 2048 x 2048 with 2 rows 41, 46, 58,
+// 4 rows 49, 49, 60, 8 rows 57, 52, 62, 128 rows -, 84, 94, 192 rows -, 108,
+// 100; 128 experts of 1536 x 2048 with 4 rows 70, 71, 86, 192 rows -, 155, 160,
+// 256 rows -, 185, 173; 8 experts of 4096 x 4096 with 8 rows 22, 25, 34, 12
+// rows 28, 28, 43.  (32-row tiles were not the fastest of any of these.)
 int tile_rows(const spg_grouped_desc *d)
 {
     const double mean = (double)d->rows / d->experts;
-    if (mean <= 12) return 16;
-    if (mean <= 28) return 32;
-    return mean <= 160 ? 128 : 256;
+    if (mean <= (d->experts * cdiv(d->N, 256) < 256 ? 8 : 4)) return 16;
+    return mean <= 176 ? 128 : 256;
 }
 
 // Upper bound of the row tiles: every expert adds at most one partial tile,
@@ -79,7 +84,7 @@ int64_t most_tiles(const spg_grouped_desc *d, int bm)
 
 int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
 {
-    return bm <= 32 ? cdiv(grouped_nout(d, epi), narrow_cols(epi))
+    return bm == 16 ? cdiv(grouped_nout(d, epi), narrow_cols(epi))
                     : (epi == SPG_EPI_SWIGLU ? cdiv(d->N / 2, 128) : cdiv(d->N, 256));
 }
 
@@ -166,7 +171,7 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
     g.tiles_n = grouped_columns(d, epilogue, bm);
     g.div_per = make_fastdiv((uint32_t)g.tiles_n);
     const int64_t workgroups = most_tiles(d, bm) * g.tiles_n;
-    const hipError_t e = bm <= 32 ? launch_gemm_block_narrow(a, bm, workgroups, (hipStream_t)stream)
+    const hipError_t e = bm == 16 ? launch_gemm_block_narrow(a, bm, workgroups, (hipStream_t)stream)
                                   : launch_gemm_block_tiles(a, bm, workgroups, (hipStream_t)stream);
     return e == hipSuccess ? SPG_OK : SPG_EHIP;
 }

@@ -27,7 +27,7 @@ struct BlockArgs {
 
 // Tiles of 256 or 128 token rows x 256 weight rows.
 hipError_t launch_gemm_block_tiles(const BlockArgs &a, int bm, int64_t workgroups, hipStream_t s);
-// 16- or 32-row tiles x narrow_cols() output columns.
+// 16- or 32-row tiles (experts: 16) x narrow_cols() output columns.
 hipError_t launch_gemm_block_narrow(const BlockArgs &a, int bm, int64_t workgroups, hipStream_t s);
 // Sum of the K slices' partial tiles and the epilogue.
 hipError_t launch_gemm_block_reduce(const BlockArgs &a, int bm, hipStream_t s);

@@ -50,9 +50,9 @@ struct Geometry {
     // longer than two of them
     static constexpr int kAhead = 2;
     static constexpr int kLds = kDepth * kSlot;
-    // after the main loop: a staging region of kY 4 KiB passes per wave, a
-    // row of ones (the scales that the shared epilogue applies) and biases
-    static constexpr int kRegion = kY * 4096, kOnes = kWaves * kRegion, kBias = kOnes + 1024;
+    // after the main loop: a staging region of kY 4 KiB passes per wave and
+    // the biases
+    static constexpr int kRegion = kY * 4096, kBias = kWaves * kRegion;
     static_assert(kBias + kWaves * 512 <= kLds, "the epilogue's LDS fits in the slots");
     static_assert(kSlot % 256 == 0, "a slot starts on LDS bank 0");
 };
@@ -346,10 +346,6 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
     wait_vmem<0>();
     wait_lds();
     block_barrier();                                        // the slots become the epilogue's
-    float *const lds_one = reinterpret_cast<float *>(&lds[G::kOnes]);
-    if (tid < 256) lds_one[tid] = 1.0f;
-    wait_lds();
-    block_barrier();
 
     // Lane l of a 16 x 16 result holds token l % 16 and weight rows 4 (l / 16)
     // + e as taken; exchanging the odd 16-lane rows of token block 2 y with
@@ -388,8 +384,8 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         GemmArgs ge = g;
         ge.M = m_end;
         if (EXPERTS) ge.stride_o = 0;
-        epilogue<EPI, Y_ / 2, true, true, SO>(ge, T, acc, lds_one, lds_one, reinterpret_cast<float *>(&lds[G::kBias]),
-                                              &lds[wave * G::kRegion], wave);
+        epilogue<EPI, Y_ / 2, true, true, SO, true>(ge, T, acc, nullptr, nullptr,
+                                                    reinterpret_cast<float *>(&lds[G::kBias]), &lds[wave * G::kRegion], wave);
     }
     clock_mark(g.clocks, 1);
 }

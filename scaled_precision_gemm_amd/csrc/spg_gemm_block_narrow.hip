@@ -263,11 +263,15 @@ template <int EPI, bool EXPERTS>
 hipError_t launch_epi(const BlockArgs &a, int bm, int64_t workgroups, hipStream_t s)
 {
     constexpr int RB = narrow_cols(EPI) / 16;
-    if (bm == 16)
+    if (bm == 16) {
         gemm_block_narrow_kernel<EPI, 1, RB, EXPERTS><<<dim3((unsigned)workgroups), kNarrowThreads, 0, s>>>(a);
-    else
-        gemm_block_narrow_kernel<EPI, 2, RB, EXPERTS><<<dim3((unsigned)workgroups), kNarrowThreads, 0, s>>>(a);
-    return hipGetLastError();
+        return hipGetLastError();
+    }
+    if constexpr (!EXPERTS) {                            // experts take 16 or at least 128 rows
+        gemm_block_narrow_kernel<EPI, 2, RB, false><<<dim3((unsigned)workgroups), kNarrowThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace

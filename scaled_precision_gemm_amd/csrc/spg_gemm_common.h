@@ -466,8 +466,9 @@ constexpr int kEpiRegionBytes = 4 * 4096;   // per workgroup
 // hold acc[x][0..1] and cover token rows wm * 64 .. wm * 64 + 63).
 // GIVEN: wave_in is the caller's wave index; otherwise it is derived here.
 // SPLITOUT: the output is column segments (g.nseg > 0), addressed per pass.
+// UNIT: the accumulators carry their scales already (lds_sa, lds_sw unused).
 template <int EPI, bool FULL, int MI = 4, bool GIVEN = false, bool BIAS = false, bool STAGED = false,
-          bool SPLITOUT = false>
+          bool SPLITOUT = false, bool UNIT = false>
 __device__ __forceinline__ void epilogue_impl(const GemmArgs &g, const Tile &T, const Acc &acc, const float *lds_sa,
                                               const float *lds_sw, float *lds_bias, uint8_t *region_base,
                                               int wave_in)
@@ -546,9 +547,11 @@ __device__ __forceinline__ void epilogue_impl(const GemmArgs &g, const Tile &T, 
     constexpr int NX = SW ? 2 : 4;
     float sa_r[MI];
     v4f sw_r[BIAS ? 1 : NX][4], swu_r[SW ? 2 : 1][4];
+    if (!UNIT) {
 #pragma unroll
-    for (int y = 0; y < MI; ++y) sa_r[y] = lds_sa[wm * (MI * 32) + y * 32 + l32];
-    if (!BIAS) {
+        for (int y = 0; y < MI; ++y) sa_r[y] = lds_sa[wm * (MI * 32) + y * 32 + l32];
+    }
+    if (!BIAS && !UNIT) {
 #pragma unroll
         for (int x = 0; x < NX; ++x)
 #pragma unroll
@@ -564,7 +567,7 @@ __device__ __forceinline__ void epilogue_impl(const GemmArgs &g, const Tile &T, 
         const int64_t row0 = T.m0 + wm * (MI * 32) + y * 32;
         const int rows_valid = FULL ? 32 : (int)min((int64_t)32, g.M - row0);
         if (rows_valid <= 0) break;                                 // uniform per wave
-        const float sa = sa_r[y];
+        const float sa = UNIT ? 1.0f : sa_r[y];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             uint8_t *const region = region_base + (STAGED ? (y * NP + p) * 4096 : 0);
@@ -620,9 +623,10 @@ __device__ __forceinline__ void epilogue_impl(const GemmArgs &g, const Tile &T, 
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int wl = wtile_row0<EPI>(wn, x) + q * 8 + khalf * 4;
-                    const v4f sw = BIAS ? *reinterpret_cast<const v4f *>(lds_sw + wl) : sw_r[BIAS ? 0 : x][q];
+                    const v4f sw = UNIT ? v4f{1.0f, 1.0f, 1.0f, 1.0f}
+                                   : BIAS ? *reinterpret_cast<const v4f *>(lds_sw + wl) : sw_r[BIAS ? 0 : x][q];
                     const v4f bias = BIAS ? *reinterpret_cast<const v4f *>(bias_w + (wl - wn * 128)) : v4f{};
-                    const v4f swu = SW ? swu_r[x & 1][q] : v4f{};
+                    const v4f swu = UNIT ? sw : SW ? swu_r[x & 1][q] : v4f{};
                     uint2 *dst = reinterpret_cast<uint2 *>(region + l32 * 128 + phys(l32, xx * 4 + q) * 16 + khalf * 8);
                     float v[4];
 #pragma unroll
@@ -689,7 +693,7 @@ __device__ __forceinline__ void epilogue_impl(const GemmArgs &g, const Tile &T, 
 // apart for it, so the split-output code is not part of the kernels that
 // write one output (inside a persistent kernel it cost those 4.5%: more
 // scalar spills and twice the code).
-template <int EPI, int MI = 4, bool GIVEN = false, bool STAGE = false, bool SO = false>
+template <int EPI, int MI = 4, bool GIVEN = false, bool STAGE = false, bool SO = false, bool UNIT = false>
 __device__ __forceinline__ void epilogue(const GemmArgs &g, const Tile &T, const Acc &acc, const float *lds_sa,
                                          const float *lds_sw, float *lds_bias, uint8_t *region, int wave_in = 0)
 {
@@ -701,10 +705,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const Tile &T, const
     if constexpr (SO) {
         // split outputs: one instantiation per bias form, with bounds checks
         if (EPI == SPG_EPI_ADD && brow)
-            epilogue_impl<EPI, false, MI, GIVEN, EPI == SPG_EPI_ADD, false, true>(g, T, acc, lds_sa, lds_sw, lds_bias,
-                                                                               region, wave_in);
+            epilogue_impl<EPI, false, MI, GIVEN, EPI == SPG_EPI_ADD, false, true, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias,
+                                                                                     region, wave_in);
         else
-            epilogue_impl<EPI, false, MI, GIVEN, false, false, true>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+            epilogue_impl<EPI, false, MI, GIVEN, false, false, true, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region,
+                                                                         wave_in);
         return;
     }
     const bool full = T.m0 + wm * (MI * 32) + MI * 32 <= g.M && T.c0 + (SW ? wn * 64 + 64 : wn * 128 + 128) <= o.nvalid &&
@@ -713,23 +718,23 @@ __device__ __forceinline__ void epilogue(const GemmArgs &g, const Tile &T, const
     if constexpr (EPI == SPG_EPI_ADD) {
         if (brow) {
             if (full)
-                epilogue_impl<EPI, true, MI, GIVEN, true>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+                epilogue_impl<EPI, true, MI, GIVEN, true, false, false, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
             else
-                epilogue_impl<EPI, false, MI, GIVEN, true>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+                epilogue_impl<EPI, false, MI, GIVEN, true, false, false, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
             return;
         }
         if constexpr (STAGE) {
             // offsets inside the quadrant stay below 2^31 bytes
             if (full && g.ldr < (INT64_C(1) << 23) / MI) {
-                epilogue_impl<EPI, true, MI, GIVEN, false, true>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+                epilogue_impl<EPI, true, MI, GIVEN, false, true, false, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
                 return;
             }
         }
     }
     if (full)
-        epilogue_impl<EPI, true, MI, GIVEN>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+        epilogue_impl<EPI, true, MI, GIVEN, false, false, false, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
     else
-        epilogue_impl<EPI, false, MI, GIVEN>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
+        epilogue_impl<EPI, false, MI, GIVEN, false, false, false, UNIT>(g, T, acc, lds_sa, lds_sw, lds_bias, region, wave_in);
 }
 
 }  // namespace gemm

@@ -88,7 +88,7 @@ def run_grouped(spg, counts, N, K, epi, gather, tail=0, head=0, seed=0, tokens=N
 # expert with everything, tiles that end inside, each tile height
 COUNTS = {
     "one_token": [0, 1, 0], "singles": [1] * 9, "decode": [3, 0, 16, 17, 1, 0, 0, 12], "all_in_one": [0, 0, 40, 0],
-    "tile32": [20, 33, 5, 40], "tile128": [129, 0, 127, 1, 255, 64], "tile256": [300, 0, 511, 1, 256],
+    "tile128_small": [20, 33, 5, 40], "tile128": [129, 0, 127, 1, 255, 64], "tile256": [300, 0, 511, 1, 256],
 }
 
 
@@ -102,7 +102,7 @@ def test_grouped_parity(spg, counts, gather, epi):
 @pytest.mark.parametrize("N,K", [(1, 16), (33, 128), (129, 144), (640, 1552)])
 @pytest.mark.parametrize("rows", [2, 25, 100, 300])
 def test_grouped_odd_sizes(spg, N, K, rows):
-    assert spg.grouped_tile_rows(3 * rows, 3, N, K) == {2: 16, 25: 32, 100: 128, 300: 256}[rows]
+    assert spg.grouped_tile_rows(3 * rows, 3, N, K) == {2: 16, 25: 128, 100: 128, 300: 256}[rows]
     run_grouped(spg, [rows, rows - 1, rows + 1], N, K, "store", True, seed=N)
 
 
@@ -110,6 +110,16 @@ def test_grouped_odd_sizes(spg, N, K, rows):
 def test_grouped_many_experts(spg, E):
     rng = np.random.default_rng(E)
     run_grouped(spg, rng.integers(0, 6, E), 256, 144, "swiglu", True, seed=E)
+
+
+@pytest.mark.parametrize("E,rows,N,K,epi", [(65, 40, 2048, 400, "swiglu"), (40, 500, 1100, 528, "store"),
+                                            (512, 12, 300, 400, "store"), (70, 20, 1100, 256, "store")])
+def test_grouped_more_tiles_than_compute_units(spg, E, rows, N, K, epi):
+    # several rounds of tiles, experts in runs of 64 and not, empty ones in a row
+    rng = np.random.default_rng(E)
+    counts = rng.integers(0, 2 * rows + 1, E)
+    counts[E // 3:E // 3 + 3] = 0
+    run_grouped(spg, counts, N, K, epi, True, seed=E, tokens=200)
 
 
 def test_grouped_offsets_and_indices_out_of_range(spg):
