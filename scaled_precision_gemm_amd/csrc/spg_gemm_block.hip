@@ -48,7 +48,7 @@ struct Geometry {
     static constexpr int kCopies = kCopyA + kCopyW + 2;     // and the two scale lines
     // weight blocks read ahead: one block is kY MFMAs, and an LDS read takes
     // longer than two of them
-    static constexpr int kAhead = 2;
+    static constexpr int kAhead = kY == 4 ? 2 : 4;
     static constexpr int kLds = kDepth * kSlot;
     // after the main loop: a staging region of kY 4 KiB passes per wave and
     // the biases
