@@ -318,8 +318,8 @@ def quantize_block128(x: torch.Tensor, tiling="row", out: torch.Tensor | None = 
     128 (weights; [ceil(R/128), ceil(K/128)])."""
     dims, strides, shape = _checked(("quantize", tiling, _sig(x), _sig(out), _sig(scale)),
                                     lambda: _check_block128(x, tiling, out, scale))
-    q = out if out is not None else torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    s = scale if scale is not None else torch.empty(shape, dtype=torch.float32, device=x.device)
+    q = out if out is not None else x.new_empty(x.shape, dtype=torch.uint8)
+    s = scale if scale is not None else x.new_empty(shape, dtype=torch.float32)
     if dims[1] > 0:
         _run(lib.quantize_block128, "quantize_block128", x, x.data_ptr(), *dims, q.data_ptr(), *strides, s.data_ptr(),
              _TILING[tiling])
@@ -719,7 +719,7 @@ def gemm_grouped(A, sa, W, sw, offsets, epilogue="store", rows=None, out=None):
     d, epi, n_out = _checked(("grouped", epilogue, _sig(A), _sig(sa), _sig(W), _sig(sw), _sig(offsets), _sig(rows),
                               _sig(out)), lambda: _grouped(A, sa, W, sw, offsets, epilogue, rows, out))
     if out is None:
-        out = torch.empty((d.rows, n_out), dtype=torch.bfloat16, device=A.device)
+        out = A.new_empty((d.rows, n_out), dtype=torch.bfloat16)
     if d.rows > 0 and n_out > 0:
         _run(lib.gemm_grouped, "gemm_grouped", A, out.data_ptr(), A.data_ptr(), sa.data_ptr(), W.data_ptr(),
              sw.data_ptr(), offsets.data_ptr(), _ptr(rows), epi, ctypes.byref(d))
@@ -740,13 +740,13 @@ def expert_workspace(T: int, top: int, E: int, device="cuda"):
     return torch.empty((n,), dtype=torch.uint8, device=device) if n > 0 else None
 
 
-def _order_ws(workspace, n, dev):
+def _order_ws(workspace, n, like):
     if n == 0:
         return None
     if workspace is None:
-        return torch.empty((n,), dtype=torch.uint8, device=dev)
-    _need(isinstance(workspace, torch.Tensor) and workspace.device == dev and workspace.is_contiguous()
-          and workspace.numel() * workspace.element_size() >= n, f"the workspace must hold {n} bytes on {dev}")
+        return like.new_empty((n,), dtype=torch.uint8)
+    _need(isinstance(workspace, torch.Tensor) and workspace.device == like.device and workspace.is_contiguous()
+          and workspace.numel() * workspace.element_size() >= n, f"the workspace must hold {n} bytes on {like.device}")
     return workspace
 
 
@@ -786,17 +786,17 @@ def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1
         return d, lib.expert_order_workspace_bytes(d.T, d.top, d.E)
 
     d, nws = _checked(("route", _sig(logits), top, score, _sig(bias), groups, top_groups, bool(renormalize), scale), check)
-    dev, T = logits.device, d.T
-    weights = torch.empty((T, top), dtype=torch.float32, device=dev)
-    experts = torch.empty((T, top), dtype=torch.int32, device=dev)
+    T = d.T
+    weights = logits.new_empty((T, top), dtype=torch.float32)
+    experts = logits.new_empty((T, top), dtype=torch.int32)
     if not order:
         _run(lib.expert_route, "expert_route", logits, logits.data_ptr(), _ptr(bias), weights.data_ptr(),
              experts.data_ptr(), None, None, None, ctypes.byref(d), None, 0)
         return ExpertRoute(weights, experts, None, None, None)
-    ws = _order_ws(workspace, nws, dev)
-    offsets = torch.empty((d.E + 1,), dtype=torch.int32, device=dev)
-    rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
-    slots = torch.empty((T, top), dtype=torch.int32, device=dev)
+    ws = _order_ws(workspace, nws, logits)
+    offsets = experts.new_empty((d.E + 1,))
+    rows = experts.new_empty((T * top,))
+    slots = experts.new_empty((T, top))
     po = offsets.data_ptr()           # no token: rows and slots are empty and may have no address
     _run(lib.expert_route, "expert_route", logits, logits.data_ptr(), _ptr(bias), weights.data_ptr(),
          experts.data_ptr(), po, rows.data_ptr() or po, slots.data_ptr() or po, ctypes.byref(d), _ptr(ws), nws)
@@ -813,10 +813,10 @@ def expert_sort(experts, n_experts, workspace=None):
     _need(top >= 1 and n_experts >= 1, "at least one expert")
     _need(experts.is_cuda, "experts must be a CUDA tensor")
     nws = lib.expert_order_workspace_bytes(T, top, n_experts)
-    ws = _order_ws(workspace, nws, dev)
-    offsets = torch.empty((n_experts + 1,), dtype=torch.int32, device=dev)
-    rows = torch.empty((T * top,), dtype=torch.int32, device=dev)
-    slots = torch.empty((T, top), dtype=torch.int32, device=dev)
+    ws = _order_ws(workspace, nws, experts)
+    offsets = experts.new_empty((n_experts + 1,))
+    rows = experts.new_empty((T * top,))
+    slots = experts.new_empty((T, top))
     _run(lib.expert_sort, "expert_sort", experts, _ptr(experts), T, top, n_experts, _ptr(offsets), _ptr(rows),
          _ptr(slots), _ptr(ws), nws)
     return offsets, rows, slots
@@ -839,7 +839,7 @@ def expert_route_backward(grad_weights, logits, experts, score="softmax", renorm
 
     d = _checked(("route backward", _sig(grad_weights), _sig(logits), _sig(experts), score, bool(renormalize), scale),
                  check)
-    grad = torch.empty((d.T, d.E), dtype=logits.dtype, device=logits.device)
+    grad = logits.new_empty((d.T, d.E))
     _run(lib.expert_route_backward, "expert_route_backward", logits, grad_weights.data_ptr(), logits.data_ptr(),
          experts.data_ptr(), grad.data_ptr(), ctypes.byref(d))
     return grad
@@ -874,7 +874,7 @@ def expert_combine(y, weights, slots, residual=None, out=None):
 
     (ldy, ldr, ldo), want = _checked(("combine", _sig(y), _sig(weights), _sig(slots), _sig(residual), _sig(out)), check)
     if out is None:
-        out = torch.empty(want, dtype=torch.bfloat16, device=y.device)
+        out = y.new_empty(want)
     _run(lib.expert_combine, "expert_combine", y, y.data_ptr(), y.shape[0], ldy, weights.data_ptr(), slots.data_ptr(),
          want[0], slots.shape[1], want[1], _ptr(residual), ldr, out.data_ptr(), ldo)
     return out
@@ -901,8 +901,8 @@ def expert_combine_backward(grad_out, y, weights, slots, grad_y=None):
                               check)
     (T, top), (R, H) = slots.shape, y.shape
     if grad_y is None:
-        grad_y = torch.empty((R, H), dtype=torch.bfloat16, device=y.device)
-    grad_weights = torch.empty((T, top), dtype=torch.float32, device=y.device)
+        grad_y = y.new_empty((R, H))
+    grad_weights = weights.new_empty((T, top))
     _run(lib.expert_combine_backward, "expert_combine_backward", y, grad_out.data_ptr(), ldg, y.data_ptr(), R, ldy,
          weights.data_ptr(), slots.data_ptr(), T, top, H, grad_y.data_ptr(), ldgy, grad_weights.data_ptr())
     return grad_y, grad_weights
