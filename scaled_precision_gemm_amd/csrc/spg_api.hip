@@ -379,15 +379,23 @@ void make_plan(const spg_gemm_desc *d, int epi, int units, spg_plan *p, bool ali
 constexpr size_t kWsAlign = 256;
 size_t align_ws(size_t b) { return (b + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
+// Row stride of the transposed copies.  Block-scaled: whole 128-byte lines, so
+// that the product's row segments are lines (4096 x 2048 over 4000 tokens: 44
+// us with rows of 4000 bytes, 39 with 4096).
+int64_t transposed_ld(const spg_gemm_desc *d)
+{
+    return d->format == SPG_FMT_E4M3_BLOCK128 ? (d->K + 127) / 128 * 128 : d->K;
+}
+
 // Workspace bytes of the transposed copies of K-major operands (A first,
 // then W, each 256-byte aligned); `a_bytes` gets the A part.
 size_t transpose_bytes(const spg_gemm_desc *d, size_t *a_bytes)
 {
     size_t a = 0, w = 0;
     if (d->layout & SPG_LAYOUT_A_KMAJOR)
-        a = align_ws((size_t)(d->stride_a ? d->batch : 1) * (size_t)d->M * (size_t)d->K);
+        a = align_ws((size_t)(d->stride_a ? d->batch : 1) * (size_t)d->M * (size_t)transposed_ld(d));
     if (d->layout & SPG_LAYOUT_W_KMAJOR)
-        w = align_ws((size_t)(d->stride_w ? d->batch : 1) * (size_t)d->N * (size_t)d->K);
+        w = align_ws((size_t)(d->stride_w ? d->batch : 1) * (size_t)d->N * (size_t)transposed_ld(d));
     if (a_bytes) *a_bytes = a;
     return a + w;
 }
@@ -611,21 +619,23 @@ SPG_EXPORT int gemm_scaled(void *out, const void *A, const void *sa, const void 
     int64_t lda = d->lda, ldw = d->ldw, stride_a = d->stride_a, stride_w = d->stride_w;
     if (d->layout & SPG_LAYOUT_A_KMAJOR) {
         uint8_t *at = (uint8_t *)ws;
-        if (launch_transpose_u8(A_nt, d->K, d->M, d->lda, d->stride_a, d->stride_a ? d->batch : 1, at, s) !=
+        if (launch_transpose_u8(A_nt, d->K, d->M, d->lda, d->stride_a, d->stride_a ? d->batch : 1, at,
+                                transposed_ld(d), s) !=
             hipSuccess)
             return SPG_EHIP;
         A_nt = at;
-        lda = d->K;
-        stride_a = d->stride_a ? d->M * d->K : 0;
+        lda = transposed_ld(d);
+        stride_a = d->stride_a ? d->M * lda : 0;
     }
     if (d->layout & SPG_LAYOUT_W_KMAJOR) {
         uint8_t *wt = (uint8_t *)ws + t_a;
-        if (launch_transpose_u8(W_nt, d->K, d->N, d->ldw, d->stride_w, d->stride_w ? d->batch : 1, wt, s) !=
+        if (launch_transpose_u8(W_nt, d->K, d->N, d->ldw, d->stride_w, d->stride_w ? d->batch : 1, wt,
+                                transposed_ld(d), s) !=
             hipSuccess)
             return SPG_EHIP;
         W_nt = wt;
-        ldw = d->K;
-        stride_w = d->stride_w ? d->N * d->K : 0;
+        ldw = transposed_ld(d);
+        stride_w = d->stride_w ? d->N * ldw : 0;
     }
 
     GemmArgs g;
