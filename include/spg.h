@@ -379,8 +379,8 @@ int gemm_scaled(void *out, const void *A, const void *sa, const void *W, const v
  *               The call cannot check device data: offsets are clamped to
  *               that range and a decreasing pair is an empty expert, so
  *               nothing outside the operands is read or written; where
- *               ranges overlap after that, those rows hold either expert's
- *               values
+ *               ranges overlap after that, what the output rows hold is
+ *               undefined
  *   row_index : device int32 [rows] or NULL; the row of A that output row r
  *               is made from (an index outside [0, a_rows) stands for a row
  *               of zeros); the same row may serve any number of output rows

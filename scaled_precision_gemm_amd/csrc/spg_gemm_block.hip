@@ -77,17 +77,12 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
     int64_t m_end = g.M;
     int split = 0;
     if (EXPERTS) {
-        const int32_t mt = total_tiles<BM>(a);
-        const int64_t n = (int64_t)mt * g.tiles_n;
-        if ((int64_t)blockIdx.x >= n) return;
-        const uint32_t v = (uint32_t)xcd_remap(blockIdx.x, n);
-        const uint32_t m = fdiv(v, g.div_per);            // div_per: by tiles_n
-        const ExpertTile t = find_tile<BM>(a, (int32_t)m);
+        const ExpertTile t = expert_tile<BM>(a);
         if (t.expert < 0) return;
-        T.global = v;
+        T.global = t.id;
         T.b = t.expert;
         T.m0 = t.m0;
-        T.tn = v - m * (uint32_t)g.tiles_n;
+        T.tn = t.column;
         T.n0 = T.tn * (SW ? 128 : 256);
         T.c0 = T.n0;
         m_end = t.end;

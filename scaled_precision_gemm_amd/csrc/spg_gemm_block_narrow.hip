@@ -50,17 +50,12 @@ __global__ __launch_bounds__(kNarrowThreads) void gemm_block_narrow_kernel(const
     // ---- the tile: token rows m0 .. m_end - 1 (at most 16 TB), columns j0 ..
     int64_t b, m0 = 0, m_end = g.M, j0;
     if (EXPERTS) {
-        const int32_t mt = total_tiles<16 * TB>(a);
-        const int64_t n = (int64_t)mt * g.tiles_n;
-        if ((int64_t)blockIdx.x >= n) return;
-        const uint32_t v = (uint32_t)xcd_remap(blockIdx.x, n);
-        const uint32_t m = fdiv(v, g.div_per);           // by tiles_n
-        const ExpertTile t = find_tile<16 * TB>(a, (int32_t)m);
+        const ExpertTile t = expert_tile<16 * TB>(a);
         if (t.expert < 0) return;
         b = t.expert;
         m0 = t.m0;
         m_end = t.end;
-        j0 = (int64_t)(v - m * (uint32_t)g.tiles_n) * kCols;
+        j0 = (int64_t)t.column * kCols;
     } else {
         b = (int64_t)blockIdx.x / g.tiles_n;
         j0 = ((int64_t)blockIdx.x - b * g.tiles_n) * kCols;

@@ -208,6 +208,22 @@ def test_weight_gradient(spg, M, N, T):
     check(out, a.T @ b, np.abs(a).T @ np.abs(b), "dW")
 
 
+@pytest.mark.parametrize("M,share", [(16, None), (160, None), (160, "w")])
+def test_batched_k_major(spg, M, share):
+    # both gradients of a batch of products: stored operands with batch
+    # strides, scales as stored
+    N, T, nb = 272, 400, 3
+    dy = bf16_normal((nb, T, M), 0.01, 1)
+    x = bf16_normal((T, N), 1.0, 2) if share == "w" else bf16_normal((nb, T, N), 1.0, 2)
+    qy, sy = spg.quantize_block128(dev(dy), "column")
+    qx, sx = spg.quantize_block128(dev(x), "block")
+    dw = spg.gemm_scaled(qy, sy, qx, sx, fmt="e4m3_block128", a_kmajor=True, w_kmajor=True)
+    for b in range(nb):
+        a = values(qy[b].cpu().numpy(), sy[b].cpu().numpy(), "column")
+        w = values((qx if share else qx[b]).cpu().numpy(), (sx if share else sx[b]).cpu().numpy(), "block")
+        check(dw[b], a.T @ w, np.abs(a).T @ np.abs(w), f"dW {b}")
+
+
 @pytest.mark.parametrize("M", [8, 150])
 @pytest.mark.parametrize("share", ["none", "a", "w"])
 def test_batch(spg, M, share):

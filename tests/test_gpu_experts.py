@@ -141,6 +141,24 @@ def test_grouped_offsets_and_indices_out_of_range(spg):
     assert bool((out[[3, 20, 40]] == 0).all())
 
 
+@pytest.mark.parametrize("E", [3, 130])
+@pytest.mark.parametrize("R", [60, 2000])
+def test_grouped_overlapping_offsets_stay_inside(spg, E, R):
+    # more tiles than the grid has workgroups: nothing outside the output rows
+    # is touched, and every row holds one expert's values or what it held
+    N, K = 256, 384
+    qa, sa = spg.quantize_block128(dev(bf16_normal((R, K), 1.0, 1)), "row")
+    qw, sw = spg.quantize_block128(dev(bf16_normal((1, N, K), 0.02, 2)), "block")
+    frame = torch.full((R + 600, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    offsets = i32([0 if e % 2 == 0 else R for e in range(E + 1)])
+    spg.gemm_grouped(qa, sa, qw.expand(E, N, K), sw.repeat(E, 1, 1), offsets, out=frame[300:300 + R])
+    assert bool((frame[:300] == 3.0).all()) and bool((frame[300 + R:] == 3.0).all())
+    a, w = row_values(qa, sa), block_values(qw[0], sw[0])
+    got = frame[300:300 + R]
+    ok, _ = oracle.within_tolerance(host(got), a @ w.T, np.abs(a) @ np.abs(w).T)
+    assert bool((torch.from_numpy(ok).cuda() | (got == 3.0)).all()) and ok.any()
+
+
 def test_grouped_no_rows_and_strides(spg):
     u8, f32 = dict(dtype=torch.uint8, device="cuda"), dict(dtype=torch.float32, device="cuda")
     out = spg.gemm_grouped(torch.zeros((0, 256), **u8), torch.zeros((2, 0), **f32), torch.zeros((3, 64, 256), **u8),
