@@ -202,16 +202,19 @@ bool narrow_route(const spg_gemm_desc *d, int64_t nout, bool aligned_scales = tr
 // Block-scaled FP8 (kernels 4 - 6): decode width as for the other formats,
 // else the cheapest of 256- and 128-row tiles with K in s slices, priced in
 // microseconds on MI355X as
-//   rounds (stages S + 5) + [s > 1] (7 + partial tiles written and read at 5 TB/s)
-// with S = 1.5 us a stage of 256-row tiles and 0.92 of 128-row tiles, 5 us a
-// tile's fill and epilogue, 7 us the reduction's launch and latency.  Measured
-// against the model (us): 1024 x 5120 x 17408 in 256-row tiles s = 1, 2, 3, 4:
-// 179, 116, 100, 133 (209, 129, 106, 140), 128-row tiles s = 1, 3: 131, 119
-// (130, 126); 512 x 5120 x 17408 128-row s = 1, 2, 3, 4: 122, 75, 62, 85; 128 x
-// 5120 x 17408 s = 4, 8, 12: 42, 31, 32; 512 x 2048 x 2048 s = 1, 2, 4: 19, 21,
-// 21; 1024 x 7168 x 5120 128- and 256-row: 44 and 59; 2048 x 7168 x 5120 90 and
-// 68.  A last round of 256-row tiles that fills at most half of the units runs
-// as 128-row halves in a second launch (kernel's tail), when that is cheaper.
+//   rounds (stages S + 5) + [s > 1] (5 + s / 4 + partial tiles written and read at 4 TB/s)
+// with S = 1.1 + 0.45 f us a stage of 256-row tiles and 0.6 + 0.32 f of 128-row
+// tiles where a share f of the compute units is at work, 5 us a tile's fill and
+// epilogue, the rest the reduction's launch and reads.  Measured against the
+// model (us): 1024 x 5120 x 17408 in 256-row tiles s = 1, 2, 3: 160, 106, 95
+// (173, 124, 112), 128-row tiles s = 1: 103 (114); 512 x 5120 x 17408 128-row s
+// = 1, 2, 3, 4: 98, 65, 57, 76 (100, 76, 68, 109); 64 x 5120 x 17408 s = 4, 8, 12:
+// 29, 24, 27 (37, 31, 32); 300 x 8192 x 8192 s = 1, 2: 49, 39 (51, 50); 512 x 2048
+// x 2048 s = 1, 2: 16, 20 (15, 20); 1024 x 7168 x 5120 128- and 256-row: 39 and 53
+// (40, 57); 2048 x 7168 x 5120 76 and 65 (84, 65).  A last round of 256-row
+// tiles that fills at most half of the units runs as 128-row halves in a second
+// launch (kernel's tail), when that is cheaper (4096 x 5120 x 6144: 121 us,
+// model 123).
 void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
 {
     const int64_t nout = n_out_of(d, epi);
@@ -230,7 +233,11 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
     p->kernel = 4;
     p->bm = (int32_t)kTile;
     const int64_t tiles_n = epi == SPG_EPI_SWIGLU ? cdiv(nout, kTile / 2) : cdiv(d->N, kTile);
-    constexpr double kStage[2] = {1.5, 0.92}, kTileCost = 5.0, kReduce = 7.0, kHalfLaunch = 2.0;
+    constexpr double kTileCost = 5.0, kReduce = 5.0, kReduceSlice = 0.25, kHalfLaunch = 2.0;
+    auto stage = [units](bool half, int64_t workgroups) {
+        const double f = workgroups < units ? (double)workgroups / units : 1.0;
+        return half ? 0.6 + 0.32 * f : 1.1 + 0.45 * f;
+    };
     double best = INFINITY;
     for (int half = 0; half < 2; ++half) {
         const int64_t bm = half ? 128 : 256, tiles = d->batch * cdiv(d->M, bm) * tiles_n;
@@ -240,14 +247,16 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
             const int64_t stages = cdiv(cdiv(d->K, s), 128);
             // slices of at least 4 stages, none empty, at most two rounds
             if (s > 1 && (d->K == 0 || stages < 4 || (int64_t)(s - 1) * stages * 128 >= d->K || tiles * s > 2 * units)) continue;
-            const double tile = (double)stages * kStage[half] + kTileCost;
+            const double tile = (double)stages * stage(half, tiles * s) + kTileCost;
             double cost = (double)cdiv(tiles * s, units) * tile;
             if (s > 1)
-                cost += kReduce + 2.0 * (double)(tiles * s) * (double)(d->M < bm ? d->M : bm) * kTile * 4.0 / 5e6;
+                cost += kReduce + kReduceSlice * s +
+                        2.0 * (double)(tiles * s) * (double)(d->M < bm ? d->M : bm) * kTile * 4.0 / 4e6;
             int64_t tail = 0;
             const int64_t rem = tiles % units;
             if (!half && s == 1 && tiles > units && rem > 0 && 2 * rem <= units) {
-                const double t = (double)(tiles / units) * tile + (double)stages * kStage[1] + kTileCost + kHalfLaunch;
+                const double t = (double)(tiles / units) * tile + (double)stages * stage(true, 2 * rem) + kTileCost +
+                                 kHalfLaunch;
                 if (t < cost) {
                     cost = t;
                     tail = rem;

@@ -59,19 +59,29 @@ namespace {
 
 int64_t grouped_nout(const spg_grouped_desc *d, int epi) { return epi == SPG_EPI_SWIGLU ? d->N / 2 : d->N; }
 
+int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
+{
+    return bm == 16 ? cdiv(grouped_nout(d, epi), narrow_cols(epi))
+                    : (epi == SPG_EPI_SWIGLU ? cdiv(d->N / 2, 128) : cdiv(d->N, 256));
+}
+
 // Tile rows from the mean rows of an expert.  Tiles of 16 rows stream the
 // weights with many small workgroups (decode): up to 4 rows, or up to 8 where
-// 128-row tiles would leave compute units idle.  Measured (us, cold weights;
-// 16-, 128-, 256-row tiles): 64 experts of 2048 x 2048 with 2 rows 41, 46, 58,
-// 4 rows 49, 49, 60, 8 rows 57, 52, 62, 128 rows -, 84, 94, 192 rows -, 108,
-// 100; 128 experts of 1536 x 2048 with 4 rows 70, 71, 86, 192 rows -, 155, 160,
-// 256 rows -, 185, 173; 8 experts of 4096 x 4096 with 8 rows 22, 25, 34, 12
-// rows 28, 28, 43.  (32-row tiles were not the fastest of any of these.)
-int tile_rows(const spg_grouped_desc *d)
+// 128-row tiles would leave compute units idle.  256-row tiles read a weight
+// panel half as often: above 112 rows, where they still give every compute
+// unit one.  Measured (us, cold weights; 16-, 128-, 256-row tiles): 64 experts
+// of 2048 x 2048 with 2 rows 43, 46, 56, 4 rows 49, 51, 59, 8 rows 53, 52, 60,
+// 96 rows -, 59, 72, 128 rows -, 74, 71, 176 rows -, 85, 76; 128 experts of 1536
+// x 2048 with 4 rows 81, 77, 89, 96 rows -, 88, 100, 128 rows -, 113, 105, 192
+// rows -, 138, 120; 8 experts of 4096 x 4096 with 8 rows 27, 37, 51, and 256-row
+// tiles not for every unit: 192 rows -, 41, 61, 256 rows -, 44, 61, but 512 rows
+// -, 78, 69.  (32-row tiles were not the fastest of any of these.)
+int tile_rows(const spg_grouped_desc *d, int epi)
 {
     const double mean = (double)d->rows / d->experts;
     if (mean <= (d->experts * cdiv(d->N, 256) < 256 ? 8 : 4)) return 16;
-    return mean <= 176 ? 128 : 256;
+    if (mean <= 112) return 128;
+    return d->experts * cdiv((int64_t)mean, 256) * grouped_columns(d, epi, 256) < 256 ? 128 : 256;
 }
 
 // Upper bound of the row tiles: every expert adds at most one partial tile,
@@ -80,12 +90,6 @@ int64_t most_tiles(const spg_grouped_desc *d, int bm)
 {
     const int64_t most = d->rows / bm + d->experts;
     return most < d->rows ? most : d->rows;
-}
-
-int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
-{
-    return bm == 16 ? cdiv(grouped_nout(d, epi), narrow_cols(epi))
-                    : (epi == SPG_EPI_SWIGLU ? cdiv(d->N / 2, 128) : cdiv(d->N, 256));
 }
 
 int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
@@ -108,7 +112,7 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
         cdiv(d->N, 128) * cdiv(d->K, 128) >= kMaxWords)
         return SPG_EUNSUPPORTED;
     if (indexed && d->a_rows * d->lda >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
-    const int bm = tile_rows(d);
+    const int bm = tile_rows(d, epi);
     if (most_tiles(d, bm) * grouped_columns(d, epi, bm) >= kMaxGrid) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
@@ -117,7 +121,7 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
 
 SPG_EXPORT int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue)
 {
-    return validate_grouped(d, epilogue, false) == SPG_OK ? tile_rows(d) : 0;
+    return validate_grouped(d, epilogue, false) == SPG_OK ? tile_rows(d, epilogue) : 0;
 }
 
 SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const float *sw,
@@ -167,7 +171,7 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
     a.offsets = offsets;
     a.row_index = row_index;
     a.experts = d->experts;
-    const int bm = tile_rows(d);
+    const int bm = tile_rows(d, epilogue);
     g.tiles_n = grouped_columns(d, epilogue, bm);
     g.div_per = make_fastdiv((uint32_t)g.tiles_n);
     const int64_t workgroups = most_tiles(d, bm) * g.tiles_n;

@@ -46,8 +46,10 @@ struct Geometry {
     static constexpr int kCopyA = BM / kWaves / 8;          // copy instructions of a wave per stage: A
     static constexpr int kCopyW = 256 / kWaves / 8;         // W
     static constexpr int kCopies = kCopyA + kCopyW + 2;     // and the two scale lines
-    // weight blocks read ahead: one block is kY MFMAs, and an LDS read takes
-    // longer than two of them
+    // weight blocks read ahead: one block is kY MFMAs, and two of kY == 2 are
+    // less than an LDS read takes (128-row tiles: 41.9 us a call with two
+    // blocks ahead, 39.9 with four, 128 x 34816 x 5120 SWIGLU); four of kY == 4
+    // would need 32 more registers than there are
     static constexpr int kAhead = kY == 4 ? 2 : 4;
     static constexpr int kLds = kDepth * kSlot;
     // after the main loop: a staging region of kY 4 KiB passes per wave and
@@ -177,11 +179,11 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
     auto plan = [&](int kt) -> StageCopy {
         StageCopy c;
         c.live = kt < nk;
-        const int64_t k0 = c.live ? (int64_t)(k0g + kt) * kBK : 0;
-        c.in_e = c.live && k0 + (int64_t)c_even * 16 < g.K;
-        c.in_o = c.live && k0 + (int64_t)c_odd * 16 < g.K;
-        c.soff = (uint32_t)k0;
         const int64_t kg = c.live ? k0g + kt : 0;
+        const uint32_t left = c.live ? (uint32_t)min(g.K - kg * kBK, (int64_t)kBK) : 0;   // bytes of the group
+        c.in_e = c_even * 16 < left;
+        c.in_o = c_odd * 16 < left;
+        c.soff = (uint32_t)kg * kBK;
         c.sw_off = (uint32_t)kg * (uint32_t)a.sw_gs * 4u;
         c.rs_sa = make_rsrc(sa_tile + kg * a.a_rows, sa_bytes);
         return c;
@@ -238,14 +240,28 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
     //                   registers and this wave's copies of the next stage
     //                   have landed -> barrier: the slot is free, the next
     //                   stage is published
-    //   from there on : the copies of stage kt + DEPTH into the freed slot,
-    //                   spread over the MFMAs left; the next stage's first
-    //                   weight blocks; its token block Y once the last MFMA
-    //                   has taken this stage's; its scales
+    //   from there on : the copies of stage kt + DEPTH into the freed slot, one
+    //                   every kSpread / kCopies MFMAs and on into the next stage
+    //                   (the copy path takes 64 bytes a cycle: the waves' 64 or
+    //                   48 KiB issued in the MFMAs left of the stage, eight
+    //                   each, held them up.  Over 8 | 12 | 16 | 20 | 28 MFMAs,
+    //                   us: 4096 x 34816 x 5120 SWIGLU 618 | 605 | 597 | 605 |
+    //                   612, later copies landing too late for the barrier;
+    //                   128-row tiles, 128 x 34816 x 5120 SWIGLU, 8 | 10 | 12 |
+    //                   14 | 16: 40.3 | 39.5 | 36.5 | 35.4 | 35.8);
+    //                   the next stage's first weight blocks; its token block Y
+    //                   once the last MFMA has taken this stage's; its scales
     // Empty assembly statements pin the order (the compiler otherwise gathers
     // MFMAs and multiply-adds into runs that wait for each other); hazards and
     // waits are still the compiler's.
     constexpr int Y_ = G::kY, kM = 8 * Y_, kBar = (8 - G::kAhead) * Y_, kBufs = 2 * G::kAhead;
+    constexpr int kSpread = 16;
+    constexpr auto copy_at = [](int idx) { return kBar + idx * kSpread / G::kCopies; };   // >= kM: in the next stage
+    // copies issued in the stage itself
+    constexpr int kNow = kM - kBar >= kSpread ? G::kCopies : ((kM - kBar) * G::kCopies + kSpread - 1) / kSpread;
+    static_assert(copy_at(kNow - 1) < kM && (kNow == G::kCopies || copy_at(kNow) >= kM) &&
+                      copy_at(G::kCopies - 1) - kM < kBar,
+                  "all copies of a stage are out before the next barrier");
     v8i fa[Y_], fw[kBufs];
     v4f P[4];
     float sv[Y_], fy[Y_], sw_lo, sw_hi;                    // token scales, factors, weight scales (SWIGLU: gate, up)
@@ -271,9 +287,10 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         for (int i = 0; i < G::kDepth; ++i) {
             const StageCopy c = plan(i);
 #pragma unroll
-            for (int idx = 0; idx < G::kCopies; ++idx) issue_one(c, i, idx);
+            for (int idx = 0; idx < G::kCopies; ++idx)
+                if (i < G::kDepth - 1 || idx < kNow) issue_one(c, i, idx);
         }
-        wait_vmem<(G::kDepth - 1) * G::kCopies>();
+        wait_vmem<(G::kDepth - 2) * G::kCopies + kNow>();
         wait_lds();
         block_barrier();
 #pragma unroll
@@ -291,7 +308,8 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
     // a strip past the tile's last row only copies and waits with the others:
     // a tile of at most BM / 2 rows has one wave per SIMD at work
     const bool busy = wm * G::kStrip < (int)a_rows;
-    int slot = 0;
+    int slot = 0, prev = G::kDepth - 1;
+    StageCopy old = plan(G::kDepth - 1);                   // whose last copies, into slot prev, are not out yet
     for (int kt = 0; kt < (busy ? nk : 0); ++kt) {
         const int next = slot + 1 == G::kDepth ? 0 : slot + 1;
         const StageCopy c = plan(kt + G::kDepth);
@@ -306,12 +324,14 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
             P[m & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[X % kBufs], fa[Y], v4f{0.0f, 0.0f, 0.0f, 0.0f},
                                                                         0, 0, 0, 0, 0, 0);
             asm volatile("" : "+v"(P[m & 3]));
+            __builtin_amdgcn_sched_barrier(0);
             if (Y == 0 && X + G::kAhead < 8) read_w(slot, X + G::kAhead);
             if (Y == 0 && X + G::kAhead >= 8) read_w(next, X + G::kAhead - 8);
             if (X == 7) read_a(next, Y);
 #pragma unroll
             for (int idx = 0; idx < G::kCopies; ++idx)
-                if (m >= kBar && idx * (kM - kBar) / G::kCopies == m - kBar) issue_one(c, slot, idx);
+                if (copy_at(idx) == m) issue_one(c, slot, idx);
+                else if (copy_at(idx) - kM == m) issue_one(old, prev, idx);
             add((m + kM - 3) % kM);                        // MFMA m - 3
             // the factors change once the last product that takes the old
             // ones is added: here for the weight rows' first half and, gate
@@ -323,13 +343,18 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
             if (m == kM - 1) read_s(next);
             __builtin_amdgcn_sched_barrier(0);
         }
+        prev = slot;
         slot = next;
+        old = c;
     }
     if (nk > 0 && busy) {
         add(kM - 3);
         add(kM - 2);
         add(kM - 1);
     }
+    if (nk > 0 && !busy)
+#pragma unroll
+        for (int idx = kNow; idx < G::kCopies; ++idx) issue_one(old, prev, idx);
     for (int kt = 0; kt < (busy ? 0 : nk); ++kt) {
         const StageCopy c = plan(kt + G::kDepth);
         wait_vmem<(G::kDepth - 2) * G::kCopies>();

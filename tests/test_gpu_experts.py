@@ -88,7 +88,7 @@ def run_grouped(spg, counts, N, K, epi, gather, tail=0, head=0, seed=0, tokens=N
 # expert with everything, tiles that end inside, each tile height
 COUNTS = {
     "one_token": [0, 1, 0], "singles": [1] * 9, "decode": [3, 0, 16, 17, 1, 0, 0, 12], "all_in_one": [0, 0, 40, 0],
-    "tile128_small": [20, 33, 5, 40], "tile128": [129, 0, 127, 1, 255, 64], "tile256": [300, 0, 511, 1, 256],
+    "tile128_small": [20, 33, 5, 40], "tile128": [129, 0, 127, 1, 255, 64], "tile128_large": [300, 0, 511, 1, 256],
 }
 
 
@@ -100,10 +100,20 @@ def test_grouped_parity(spg, counts, gather, epi):
 
 
 @pytest.mark.parametrize("N,K", [(1, 16), (33, 128), (129, 144), (640, 1552)])
-@pytest.mark.parametrize("rows", [2, 25, 100, 300])
+@pytest.mark.parametrize("rows", [2, 25, 300])
 def test_grouped_odd_sizes(spg, N, K, rows):
-    assert spg.grouped_tile_rows(3 * rows, 3, N, K) == {2: 16, 25: 128, 100: 128, 300: 256}[rows]
+    assert spg.grouped_tile_rows(3 * rows, 3, N, K) == {2: 16, 25: 128, 300: 128}[rows]
     run_grouped(spg, [rows, rows - 1, rows + 1], N, K, "store", True, seed=N)
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["in_order", "gathered"])
+@pytest.mark.parametrize("E,N,K,epi", [(256, 33, 16, "store"), (130, 300, 144, "store"), (130, 512, 400, "swiglu"),
+                                       (70, 1100, 144, "store"), (90, 768, 272, "swiglu")])
+def test_grouped_256_row_tiles(spg, E, N, K, epi, gather):
+    # experts that end on, before and behind a tile's and its strips' last row
+    counts = np.resize([256, 0, 1, 500, 63, 255, 257, 0, 192, 300, 64], E)
+    assert spg.grouped_tile_rows(int(counts.sum()), E, N, K, epi) == 256
+    run_grouped(spg, counts, N, K, epi, gather, tail=3, head=1, seed=E, tokens=None if not gather else 500)
 
 
 @pytest.mark.parametrize("E", [1, 63, 64, 65, 200])
