@@ -192,7 +192,8 @@ int quantize_block16_noalloc(const void *x, int64_t rows, int64_t K, uint8_t *q,
  *   K % 16 == 0, ldx >= K, ldq >= K, ldx % 8 == 0, ldq % 16 == 0; with batch >
  *   1 bstride >= (rows - 1) * ldx + K and % 8 == 0, qbstride >= (rows - 1) *
  *   ldq + K and % 16 == 0.  rows == 0 is a no-op; rows > 0 with K == 0 is
- *   invalid.  One launch, no workspace; every byte is read once.
+ *   invalid, and so are q and scale where they overlap x or each other.  One
+ *   launch, no workspace; every byte is read once.
  */
 enum {
     SPG_BLOCK_ROW = 0,
@@ -434,9 +435,10 @@ int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
  *             top, E) (any contents; 0 up to 16384 entries T * top; not used
  *             without row order)
  * 1 <= E <= 1024, 1 <= top <= min(E, 32), 1 <= groups <= 64 dividing E,
- * 1 <= top_groups <= groups, T * top < 2^31; beyond: SPG_EUNSUPPORTED for
- * E, top and groups too large, else SPG_EINVAL.  scale is any finite number.
- * Two launches with row order, one without.
+ * 1 <= top_groups <= groups, T < 2^25, T * top < 2^31; beyond:
+ * SPG_EUNSUPPORTED for E, top, groups and T too large, else SPG_EINVAL.  scale
+ * is any finite number.  Outputs and workspace must not overlap each other or
+ * an input (SPG_EINVAL).  Two launches with row order, one without.
  */
 enum {
     SPG_SCORE_SOFTMAX = 0,
@@ -481,14 +483,14 @@ int expert_route_backward(const float *grad_weights, const void *logits, const i
  *              itself (ldr == ldo), any other overlap is SPG_EINVAL
  *   out      : bf16 [T, H], row stride ldo
  * Strides are at least H; 16-byte aligned rows (H % 8 == 0) move as vectors.
- * 1 <= top <= 32.  T == 0 or H == 0 is a no-op.
+ * 1 <= top <= 32, T < 2^23, R < 2^31.  T == 0 or H == 0 is a no-op.
  *
  * expert_combine_backward - its gradients: grad_y[slots[t, j]] = weights[t, j]
  * grad_out[t] (bf16 [R, H], row stride ldgy; rows that no slot names are left
  * as they were; the slots must be distinct, as expert_route's are) and
  * grad_weights[t, j] = <grad_out[t], y[slots[t, j]]> in fp32 (0 without a
- * row).  The residual's gradient is grad_out.  grad_y must not overlap an
- * input.
+ * row).  The residual's gradient is grad_out.  grad_y and grad_weights must
+ * not overlap each other or an input (SPG_EINVAL).
  */
 int expert_combine(const void *y, int64_t R, int64_t ldy, const float *weights, const int32_t *slots, int64_t T,
                    int32_t top, int64_t H, const void *residual, int64_t ldr, void *out, int64_t ldo, void *stream);

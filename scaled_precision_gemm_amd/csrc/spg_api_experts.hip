@@ -16,16 +16,35 @@ bool aligned2(const void *p) { return ((uintptr_t)p & 1u) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kMaxWords = INT64_C(1) << 29;        // floats within a 31-bit byte range
-constexpr int64_t kMaxGrid = INT64_C(1) << 31;
+constexpr int64_t kMaxIndex = INT64_C(1) << 31;        // rows and (token, place) pairs are int32
+constexpr int64_t kMaxGrid = INT64_C(1) << 23;         // workgroups: at most 512 threads each, 2^32 in all
 constexpr int64_t kMaxGridYZ = 65535;
 
 // [a0, a1) and [b0, b1) share a byte.
 bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes)
 {
     const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+    return abytes > 0 && bbytes > 0 && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
 }
 int64_t extent(int64_t rows, int64_t ld, int64_t cols) { return rows > 0 ? (rows - 1) * ld + cols : 0; }
+// Byte extents of n pieces `stride` apart stay far inside 64 bits.
+bool addressable(int64_t n, int64_t stride) { return n <= 1 || stride < (INT64_C(1) << 56) / n; }
+
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+// An output (outs[0 .. n)) shares a byte with another or with an input.
+bool any_overlap(const Range *outs, int n, const Range *ins, int m)
+{
+    for (int i = 0; i < n; ++i) {
+        for (int j = i + 1; j < n; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+        for (int j = 0; j < m; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
+    }
+    return false;
+}
 
 }  // namespace
 
@@ -35,6 +54,8 @@ SPG_EXPORT int quantize_block128(const void *x, int64_t batch, int64_t rows, int
     if (tiling != SPG_BLOCK_ROW && tiling != SPG_BLOCK_COLUMN && tiling != SPG_BLOCK_BLOCK) return SPG_EINVAL;
     if (batch < 1 || rows < 0 || K < 0 || (K % 16)) return SPG_EINVAL;
     if (rows == 0) return SPG_OK;
+    if (!addressable(rows, ldx) || !addressable(rows, ldq) || !addressable(batch, bstride) || !addressable(batch, qbstride))
+        return SPG_EUNSUPPORTED;
     if (K == 0) return SPG_EINVAL;                     // a scale of an empty row is undefined
     if (!x || !q || !scale) return SPG_EINVAL;
     if (ldx < K || ldq < K || (ldx & 7) || (ldq & 15)) return SPG_EINVAL;
@@ -46,6 +67,13 @@ SPG_EXPORT int quantize_block128(const void *x, int64_t batch, int64_t rows, int
     if (tiling == SPG_BLOCK_ROW ? (cdiv(rows, 16) >= kMaxGrid || cdiv(K, 512) > kMaxGridYZ)
                                 : (cdiv(K, 128) >= kMaxGrid || cdiv(rows, 128) > kMaxGridYZ))
         return SPG_EUNSUPPORTED;
+    {
+        const int64_t gr = cdiv(rows, 128), gk = cdiv(K, 128);
+        const int64_t words = tiling == SPG_BLOCK_ROW ? gk * rows : tiling == SPG_BLOCK_COLUMN ? gr * K : gr * gk;
+        const Range outs[] = {{q, (batch - 1) * qbstride + extent(rows, ldq, K)}, {scale, 4 * batch * words}};
+        const Range in = {x, 2 * ((batch - 1) * bstride + extent(rows, ldx, K))};
+        if (any_overlap(outs, 2, &in, 1)) return SPG_EINVAL;
+    }
     const hipError_t e = launch_quantize_block128((const uint16_t *)x, batch, rows, K, ldx, bstride, q, ldq, qbstride,
                                                   scale, tiling, (hipStream_t)stream);
     return e == hipSuccess ? SPG_OK : SPG_EHIP;
@@ -105,6 +133,7 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
     if (d->lda < d->K || d->ldw < d->K || (d->lda & 15) || (d->ldw & 15)) return SPG_EINVAL;
     if (d->lda > (INT64_C(1) << 23) || d->ldw > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
     if (d->stride_w < 0 || (d->stride_w & 15)) return SPG_EINVAL;
+    if (!addressable(d->experts, d->stride_w)) return SPG_EUNSUPPORTED;
     if (d->experts > 1 && d->stride_w != 0 && d->stride_w < extent(d->N, d->ldw, d->K)) return SPG_EINVAL;
     if (d->ldo < grouped_nout(d, epi)) return SPG_EINVAL;
     if (d->ldo >= (INT64_C(1) << 26)) return SPG_EUNSUPPORTED;
@@ -194,7 +223,7 @@ int validate_route(const spg_route_desc *d)
     if (d->score != SPG_SCORE_SOFTMAX && d->score != SPG_SCORE_SIGMOID) return SPG_EINVAL;
     if (!isfinite(d->scale)) return SPG_EINVAL;
     if (d->E > kRouteMaxExperts || d->top > kRouteMaxTop || d->groups > kRouteMaxGroups) return SPG_EUNSUPPORTED;
-    if (d->T >= kMaxGrid / d->top) return SPG_EUNSUPPORTED;
+    if (d->T >= kMaxIndex / d->top || cdiv(d->T, 4) >= kMaxGrid || !addressable(d->T, d->ld)) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
 
@@ -228,7 +257,7 @@ RouteArgs route_args(const spg_route_desc *d)
 
 SPG_EXPORT size_t expert_order_workspace_bytes(int64_t T, int32_t top, int32_t E)
 {
-    if (T <= 0 || top < 1 || E < 1 || E > kRouteMaxExperts || T >= kMaxGrid / top) return 0;
+    if (T <= 0 || top < 1 || E < 1 || E > kRouteMaxExperts || T >= kMaxIndex / top) return 0;
     return order_ws(T, top, E);
 }
 
@@ -262,6 +291,14 @@ SPG_EXPORT int expert_route(const void *logits, const float *bias, float *weight
         a.chunk = route_chunk(d->T, d->top);
         a.chunks = (int32_t)cdiv(d->T, a.chunk);
     }
+    {
+        const int64_t bytes = 4 * d->T * d->top;
+        const Range outs[] = {{weights, bytes}, {experts, bytes}, {offsets, order ? 4 * (int64_t)(d->E + 1) : 0},
+                              {rows, order ? bytes : 0}, {slots, order ? bytes : 0},
+                              {a.hist, a.hist ? (int64_t)order_ws(d->T, d->top, d->E) : 0}};
+        const Range ins[] = {{logits, (d->logits_bf16 ? 2 : 4) * extent(d->T, d->ld, d->E)}, {bias, bias ? 4 * d->E : 0}};
+        if (any_overlap(outs, 6, ins, 2)) return SPG_EINVAL;
+    }
     // no token: the row order is that of no rows
     if (d->T == 0 && !order) return SPG_OK;
     return launch_expert_route(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
@@ -272,11 +309,17 @@ SPG_EXPORT int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32
 {
     if (T < 0 || top < 1 || E < 1) return SPG_EINVAL;
     if (E > kRouteMaxExperts) return SPG_EUNSUPPORTED;
-    if (T >= kMaxGrid / top) return SPG_EUNSUPPORTED;
+    if (T >= kMaxIndex / top) return SPG_EUNSUPPORTED;
     if (!offsets || (T > 0 && (!experts || !rows || !slots))) return SPG_EINVAL;
     if (!aligned4(experts) || !aligned4(offsets) || !aligned4(rows) || !aligned4(slots)) return SPG_EINVAL;
     const size_t need = order_ws(T, top, E);
     if (need > 0 && (!ws || ws_bytes < need || !aligned4(ws))) return SPG_EWORKSPACE;
+    {
+        const int64_t bytes = 4 * T * top;
+        const Range outs[] = {{offsets, 4 * (int64_t)(E + 1)}, {rows, bytes}, {slots, bytes}, {ws, (int64_t)need}};
+        const Range in = {experts, bytes};
+        if (any_overlap(outs, 4, &in, 1)) return SPG_EINVAL;
+    }
     spg_route_desc d;
     memset(&d, 0, sizeof(d));
     d.T = T;
@@ -307,7 +350,10 @@ SPG_EXPORT int expert_route_backward(const float *grad_weights, const void *logi
     if (d->logits_bf16 ? !aligned2(logits) || !aligned2(grad_logits) : !aligned4(logits) || !aligned4(grad_logits))
         return SPG_EINVAL;
     const int64_t size = d->logits_bf16 ? 2 : 4;
-    if (overlap(grad_logits, size * d->T * d->E, logits, size * extent(d->T, d->ld, d->E))) return SPG_EINVAL;
+    const Range out = {grad_logits, size * d->T * d->E};
+    const Range ins[] = {{logits, size * extent(d->T, d->ld, d->E)}, {grad_weights, 4 * d->T * d->top},
+                         {experts, 4 * d->T * d->top}};
+    if (any_overlap(&out, 1, ins, 3)) return SPG_EINVAL;
     RouteArgs a = route_args(d);
     a.logits = logits;
     a.grad = grad_weights;
@@ -326,7 +372,7 @@ int validate_combine(int64_t T, int64_t R, int32_t top, int64_t H)
 {
     if (T < 0 || R < 0 || H < 0 || top < 1) return SPG_EINVAL;
     if (top > kRouteMaxTop) return SPG_EUNSUPPORTED;
-    if (T >= kMaxGrid / top || R >= kMaxGrid || H >= kMaxGridYZ * 256) return SPG_EUNSUPPORTED;
+    if (T >= kMaxIndex / top || T >= kMaxGrid || R >= kMaxIndex || H >= kMaxGridYZ * 256) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
 
@@ -339,6 +385,7 @@ SPG_EXPORT int expert_combine(const void *y, int64_t R, int64_t ldy, const float
     const int v = validate_combine(T, R, top, H);
     if (v != SPG_OK) return v;
     if (ldy < H || ldo < H || (residual && ldr < H)) return SPG_EINVAL;
+    if (!addressable(R, ldy) || !addressable(T, ldo) || (residual && !addressable(T, ldr))) return SPG_EUNSUPPORTED;
     if (T == 0 || H == 0) return SPG_OK;
     if ((R > 0 && !y) || !weights || !slots || !out) return SPG_EINVAL;
     if (!aligned2(y) || !aligned2(residual) || !aligned2(out) || !aligned4(weights) || !aligned4(slots))
@@ -373,19 +420,19 @@ SPG_EXPORT int expert_combine_backward(const void *grad_out, int64_t ldg, const 
     const int v = validate_combine(T, R, top, H);
     if (v != SPG_OK) return v;
     if (ldg < H || ldy < H || ldgy < H) return SPG_EINVAL;
+    if (!addressable(T, ldg) || !addressable(R, ldy) || !addressable(R, ldgy)) return SPG_EUNSUPPORTED;
     if (T == 0) return SPG_OK;
     if (!weights || !slots || !grad_weights) return SPG_EINVAL;
     if (H > 0 && (!grad_out || (R > 0 && (!y || !grad_y)))) return SPG_EINVAL;
     if (!aligned2(grad_out) || !aligned2(y) || !aligned2(grad_y) || !aligned4(weights) || !aligned4(slots) ||
         !aligned4(grad_weights))
         return SPG_EINVAL;
-    const int64_t gbytes = 2 * extent(R, ldgy, H), wbytes = 4 * T * top;
-    if (overlap(grad_y, gbytes, y, 2 * extent(R, ldy, H)) || overlap(grad_y, gbytes, grad_out, 2 * extent(T, ldg, H)) ||
-        overlap(grad_y, gbytes, weights, wbytes) || overlap(grad_y, gbytes, slots, wbytes) ||
-        overlap(grad_y, gbytes, grad_weights, wbytes) || overlap(grad_weights, wbytes, weights, wbytes) ||
-        overlap(grad_weights, wbytes, slots, wbytes) || overlap(grad_weights, wbytes, y, 2 * extent(R, ldy, H)) ||
-        overlap(grad_weights, wbytes, grad_out, 2 * extent(T, ldg, H)))
-        return SPG_EINVAL;
+    {
+        const int64_t wbytes = 4 * T * top;
+        const Range outs[] = {{grad_y, 2 * extent(R, ldgy, H)}, {grad_weights, wbytes}};
+        const Range ins[] = {{y, 2 * extent(R, ldy, H)}, {grad_out, 2 * extent(T, ldg, H)}, {weights, wbytes}, {slots, wbytes}};
+        if (any_overlap(outs, 2, ins, 4)) return SPG_EINVAL;
+    }
     CombineArgs a;
     memset(&a, 0, sizeof(a));
     a.y = (const uint16_t *)y;

@@ -184,6 +184,36 @@ def test_combine_backward_refusals():
     assert back(top=33) == EUNSUP and back(T=0, g=None) == 0
 
 
+def test_outputs_overlap_nothing():
+    at = lambda n: P(0x100000 + n)                             # noqa: E731
+    assert [quant(q=at(0)), quant(q=at(2 * 32 * 256 - 16), scale=FAR), quant(q=FAR, scale=at(16380)),
+            quant(q=FAR, scale=P(FAR.value + 32 * 256 - 4)), quant(tiling=2, q=FAR, scale=P(FAR.value - 4))] == [EINVAL] * 5
+    outs = [P(0x40000000 + (i << 24)) for i in range(6)]       # weights, experts, offsets, rows, slots, workspace
+    d = route_desc(T=3000)
+    for i in range(6):
+        for j in range(i):
+            o = list(outs)
+            o[i] = o[j]
+            assert route(d, FAKE, FAR, *o) == EINVAL, (i, j)
+            if j >= 2:
+                assert spg.lib.expert_sort(FAKE, 3000, 8, 64, *o[2:], 1 << 20, None) == EINVAL
+        assert route(d, outs[i], FAR, *outs) == EINVAL and route(d, FAKE, outs[i], *outs) == EINVAL
+        if i >= 2:
+            assert spg.lib.expert_sort(outs[i], 3000, 8, 64, *outs[2:], 1 << 20, None) == EINVAL
+    for g, l, x in ((FAR, FAR, FAKE), (FAKE, FAR, FAR), (FAR, FAKE, FAR)):   # noqa: E741
+        assert spg.lib.expert_route_backward(g, l, x, FAKE, ctypes.byref(route_desc()), None) == EINVAL
+
+
+def test_strides_past_64_bits():
+    big = 2 ** 62
+    assert quant(ldx=big) == EUNSUP and quant(ldq=big) == EUNSUP
+    assert quant(batch=4, bs=big, qbs=8192) == EUNSUP and quant(batch=4, bs=8192, qbs=big) == EUNSUP
+    assert grouped(grouped_desc(stride_w=big)) == EUNSUP
+    assert route(route_desc(ld=big)) == EUNSUP and route(route_desc(T=2 ** 25, top=1)) == EUNSUP
+    assert combine(ldy=big) == EUNSUP and combine(ldo=big) == EUNSUP and combine(res=FAR, ldr=big) == EUNSUP
+    assert combine(T=2 ** 23, top=1) == EUNSUP and combine(R=2 ** 31) == EUNSUP
+
+
 # ---- Python binding -----------------------------------------------------------
 
 def t(shape, dtype):
