@@ -23,6 +23,10 @@
 // instructions with 64 lanes (4 keys each) and 800 for four tokens at once
 // with 16 (16 keys each).  Few tokens are bound by one wave's latency and take
 // 64 lanes; many by issue and take 16.
+//
+// Measured on the GPU: 16 tokens of 256 experts (8 groups, biased sigmoid) 8.6
+// us and 4.0 us for their row order, both one wave's latency; 8192 tokens of
+// 128 experts (softmax, bf16) 6.0 us, 7.4 and, for the gradient, 6.2.
 #include "spg_experts.h"
 #include "spg_gemm_common.h"
 
@@ -631,7 +635,9 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
 // of j, one rounding.  A stream over the chosen rows: one workgroup per token
 // and 2048 columns, 16 bytes per lane and row, up to eight rows in flight.
 // VEC: every pointer and row stride is 16-byte aligned and H % 8 == 0; else
-// one element per lane.
+// one element per lane.  4096 x 8 rows of 2048: 28.5 us (5.9 TB/s), the
+// gradients 50 us (5.7 TB/s).
+
 // 16 bytes of an expert's row, read once: non-temporal, so that the rows do
 // not push each other through the caches (4096 tokens x 6 rows of 7168: 95 us
 // with ordinary loads and stores of rows and outputs, 77 us; with the residual

