@@ -66,49 +66,18 @@ struct Geometry {
     static_assert(kSlot % 256 == 0, "a slot starts on LDS bank 0");
 };
 
+// One tile: rows T.m0 .. m_end - 1 (at most BM) x 256 weight rows, K slice
+// `split`.
 template <int EPI, int BM, bool EXPERTS, bool SPLIT, bool SO>
-__global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_block_kernel(
-    const BlockArgs a)
+__device__ __forceinline__ void block_tile(const BlockArgs &a, const Tile &T, int64_t m_end, int split, uint8_t *lds)
 {
     using G = Geometry<BM>;
     constexpr bool SW = EPI == SPG_EPI_SWIGLU;
-    __shared__ __attribute__((aligned(2048))) uint8_t lds[G::kLds];
     const GemmArgs &g = a.g;
-    clock_mark(g.clocks, 0);
-
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int ln = lane_id();
-
-    // ---- the tile -----------------------------------------------------------
-    Tile T;
-    int64_t m_end = g.M;
-    int split = 0;
-    if (EXPERTS) {
-        const ExpertTile t = expert_tile<BM>(a);
-        if (t.expert < 0) return;
-        T.global = t.id;
-        T.b = t.expert;
-        T.m0 = t.m0;
-        T.tn = t.column;
-        T.n0 = T.tn * (SW ? 128 : 256);
-        T.c0 = T.n0;
-        m_end = t.end;
-    } else {
-        if (BM == 128 && !SPLIT && !g.rows128) {
-            // the tail of a product in 256-row tiles: half v % 2 of tile
-            // tile_begin + v / 2 (neighbouring halves share their W panel)
-            const uint32_t v = (uint32_t)xcd_remap(blockIdx.x, 2 * g.tile_count);
-            T = tile_from_id<EPI, 256>(g, g.tile_begin + (v >> 1));
-            T.m0 += (int64_t)(v & 1u) * 128;
-            if (T.m0 >= g.M) return;
-        } else {
-            const WorkItem wi = work_item(g);
-            split = wi.split;
-            T = tile_from_id<EPI, BM>(g, g.tile_begin + wi.tile);
-        }
-    }
     const int k0g = SPLIT ? split * (int)(g.k_chunk / kBK) : 0;                    // first group
     const int nk = SPLIT ? min(a.groups - k0g, (int)(g.k_chunk / kBK)) : a.groups;
     const int64_t Nh = g.N / 2;
@@ -414,6 +383,55 @@ __global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves
         epilogue<EPI, Y_ / 2, true, true, SO, true>(ge, T, acc, nullptr, nullptr,
                                                     reinterpret_cast<float *>(&lds[G::kBias]), &lds[wave * G::kRegion], wave);
     }
+}
+
+template <int EPI, int BM, bool EXPERTS, bool SPLIT, bool SO>
+__global__ __launch_bounds__(Geometry<BM>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_block_kernel(
+    const BlockArgs a)
+{
+    constexpr bool SW = EPI == SPG_EPI_SWIGLU;
+    // an expert's last tile of at most 128 rows runs as a 128-row tile, whose
+    // rows spread over all eight waves and whose copies have three slots (64
+    // experts of 2048 x 2048, us: 256 rows 121 as 256-row tiles, 109 so; 512 rows
+    // 176 and 168; 128 rows, where most tiles are whole 128-row ones, 70 and 72)
+    constexpr bool LIGHT = EXPERTS && BM == 256;
+    constexpr int kLds = LIGHT && Geometry<128>::kLds > Geometry<BM>::kLds ? Geometry<128>::kLds : Geometry<BM>::kLds;
+    __shared__ __attribute__((aligned(2048))) uint8_t lds[kLds];
+    const GemmArgs &g = a.g;
+    clock_mark(g.clocks, 0);
+
+    // ---- the tile -----------------------------------------------------------
+    Tile T;
+    int64_t m_end = g.M;
+    int split = 0;
+    if (EXPERTS) {
+        const ExpertTile t = expert_tile<BM>(a);
+        if (t.expert < 0) return;
+        T.global = t.id;
+        T.b = t.expert;
+        T.m0 = t.m0;
+        T.tn = t.column;
+        T.n0 = T.tn * (SW ? 128 : 256);
+        T.c0 = T.n0;
+        m_end = t.end;
+    } else {
+        if (BM == 128 && !SPLIT && !g.rows128) {
+            // the tail of a product in 256-row tiles: half v % 2 of tile
+            // tile_begin + v / 2 (neighbouring halves share their W panel)
+            const uint32_t v = (uint32_t)xcd_remap(blockIdx.x, 2 * g.tile_count);
+            T = tile_from_id<EPI, 256>(g, g.tile_begin + (v >> 1));
+            T.m0 += (int64_t)(v & 1u) * 128;
+            if (T.m0 >= g.M) return;
+        } else {
+            const WorkItem wi = work_item(g);
+            split = wi.split;
+            T = tile_from_id<EPI, BM>(g, g.tile_begin + wi.tile);
+        }
+    }
+    if (LIGHT && m_end - T.m0 <= 128)
+        block_tile<EPI, 128, EXPERTS, SPLIT, SO>(a, T, m_end, split, lds);
+    else
+        block_tile<EPI, BM, EXPERTS, SPLIT, SO>(a, T, m_end, split, lds);
     clock_mark(g.clocks, 1);
 }
 
