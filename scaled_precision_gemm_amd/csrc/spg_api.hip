@@ -202,19 +202,21 @@ bool narrow_route(const spg_gemm_desc *d, int64_t nout, bool aligned_scales = tr
 // Block-scaled FP8 (kernels 4 - 6): decode width as for the other formats,
 // else the cheapest of 256- and 128-row tiles with K in s slices, priced in
 // microseconds on MI355X as
-//   rounds (stages S + 5) + [s > 1] (5 + s / 4 + partial tiles written and read at 4 TB/s)
-// with S = 1.1 + 0.45 f us a stage of 256-row tiles and 0.6 + 0.32 f of 128-row
-// tiles where a share f of the compute units is at work, 5 us a tile's fill and
-// epilogue, the rest the reduction's launch and reads.  Measured against the
-// model (us): 1024 x 5120 x 17408 in 256-row tiles s = 1, 2, 3: 160, 106, 95
-// (173, 124, 112), 128-row tiles s = 1: 103 (114); 512 x 5120 x 17408 128-row s
-// = 1, 2, 3, 4: 98, 65, 57, 76 (100, 76, 68, 109); 64 x 5120 x 17408 s = 4, 8, 12:
-// 29, 24, 27 (37, 31, 32); 300 x 8192 x 8192 s = 1, 2: 49, 39 (51, 50); 512 x 2048
-// x 2048 s = 1, 2: 16, 20 (15, 20); 1024 x 7168 x 5120 128- and 256-row: 39 and 53
-// (40, 57); 2048 x 7168 x 5120 76 and 65 (84, 65).  A last round of 256-row
-// tiles that fills at most half of the units runs as 128-row halves in a second
-// launch (kernel's tail), when that is cheaper (4096 x 5120 x 6144: 121 us,
-// model 123).
+//   rounds (5.5 + stages S) + [s > 1] (4.5 + 0.6 s + partial tiles written and read at 8 TB/s)
+// with S = 1.2 + 0.4 f us a stage of 256-row tiles and 0.7 + 0.25 f of 128-row
+// tiles where a share f of the compute units is at work, 5.5 us a tile's fill
+// and epilogue, the rest the reduction's launch and reads.  Fitted to
+// 238 timings of 31 shapes, weights in the last-level cache and from HBM: the
+// choice is the fastest or within 7 % of it for each.  Measured (HBM; the model):
+// 1024 x 5120 x 17408 in 256-row tiles s = 1, 2, 3: 195, 122, 106 (186, 121, 100),
+// 128-row tiles s = 1: 121 (122); 512 x 5120 x 17408 128-row s = 1, 2, 3, 4: 121,
+// 76, 63, 87 (111, 75, 63, 93); 256 x 7168 x 5120 s = 1, 2, 4, 6: 45, 35, 29, 41 (36,
+// 31, 29, 43); 64 x 5120 x 17408 s = 4, 8, 12: 40, 30, 31 (40, 32, 32); 300 x 8192 x
+// 8192 s = 1, 2: 53, 42 (56, 46); 512 x 2048 x 2048 s = 1, 2: 17, 21 (17, 19).  In the
+// cache: 1024 x 7168 x 5120 128- and 256-row 39 and 53 (42, 60), 2048 x 7168 x
+// 5120 76 and 65 (87, 67).  A last round of 256-row tiles that fills at most half
+// of the units runs as 128-row halves in a second launch (kernel's tail), when
+// that is cheaper (4096 x 5120 x 6144: 121 us, model 129).
 void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
 {
     const int64_t nout = n_out_of(d, epi);
@@ -233,10 +235,10 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
     p->kernel = 4;
     p->bm = (int32_t)kTile;
     const int64_t tiles_n = epi == SPG_EPI_SWIGLU ? cdiv(nout, kTile / 2) : cdiv(d->N, kTile);
-    constexpr double kTileCost = 5.0, kReduce = 5.0, kReduceSlice = 0.25, kHalfLaunch = 2.0;
+    constexpr double kTileCost = 5.5, kReduce = 4.5, kReduceSlice = 0.6, kHalfLaunch = 2.0;
     auto stage = [units](bool half, int64_t workgroups) {
         const double f = workgroups < units ? (double)workgroups / units : 1.0;
-        return half ? 0.6 + 0.32 * f : 1.1 + 0.45 * f;
+        return half ? 0.7 + 0.25 * f : 1.2 + 0.4 * f;
     };
     double best = INFINITY;
     for (int half = 0; half < 2; ++half) {
@@ -251,7 +253,7 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
             double cost = (double)cdiv(tiles * s, units) * tile;
             if (s > 1)
                 cost += kReduce + kReduceSlice * s +
-                        2.0 * (double)(tiles * s) * (double)(d->M < bm ? d->M : bm) * kTile * 4.0 / 4e6;
+                        2.0 * (double)(tiles * s) * (double)(d->M < bm ? d->M : bm) * kTile * 4.0 / 8e6;
             int64_t tail = 0;
             const int64_t rem = tiles % units;
             if (!half && s == 1 && tiles > units && rem > 0 && 2 * rem <= units) {
