@@ -13,7 +13,7 @@
 //
 // Bound by the weight stream: 16 x 8192 x 8192 14.4 us (4.7 TB/s), 16 x 5120 x
 // 17408 ADD 23 us with weights from HBM (3.9 TB/s; 160 workgroups, row-scaled
-// 21.6), 64 experts of 2048 x 2048 with two rows each 39 us (6.0 TB/s).  16
+// 21.6), 128 rows over 64 experts of 2048 x 2048 43 us (5.5 TB/s).  16
 // columns a workgroup where 32 leave compute units idle took longer (16 x 5120
 // x 17408 29.8 us for 24.5: A is copied twice as often), and so did rings of
 // 32 KiB a wave (16 x 8192 x 8192 20.6 us for 14.3).
