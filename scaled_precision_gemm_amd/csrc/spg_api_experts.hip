@@ -96,19 +96,20 @@ int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
 // Tile rows from the mean rows of an expert.  Tiles of 16 rows stream the
 // weights with many small workgroups (decode): up to 4 rows, or up to 8 where
 // 128-row tiles would leave compute units idle.  256-row tiles read a weight
-// panel half as often: above 112 rows, where they still give every compute
-// unit one.  Measured (us, cold weights; 16-, 128-, 256-row tiles): 64 experts
-// of 2048 x 2048 with 2 rows 43, 46, 56, 4 rows 49, 51, 59, 8 rows 53, 52, 60,
-// 96 rows -, 59, 72, 128 rows -, 74, 71, 176 rows -, 85, 76; 128 experts of 1536
-// x 2048 with 4 rows 81, 77, 89, 96 rows -, 88, 100, 128 rows -, 113, 105, 192
-// rows -, 138, 120; 8 experts of 4096 x 4096 with 8 rows 27, 37, 51, and 256-row
-// tiles not for every unit: 192 rows -, 41, 61, 256 rows -, 44, 61, but 512 rows
-// -, 78, 69.  (32-row tiles were not the fastest of any of these.)
+// panel half as often (and run an expert's last rows as a 128-row tile): above
+// 96 rows, where they still give every compute unit one.  Measured (us, cold
+// weights; 16-, 128-, 256-row tiles): 64 experts of 2048 x 2048 with 2 rows 43,
+// 46, 46, 4 rows 49, 51, 51, 8 rows 53, 52, 52, 80 rows -, 58, 62, 96 rows -, 59,
+// 60, 112 rows -, 74, 66, 176 rows -, 80, 74; 128 experts of 1536 x 2048 with 4
+// rows 81, 77, 77, 128 rows -, 111, 105, 192 rows -, 135, 116; 16 experts of 4096 x
+// 2048 with 128 rows -, 44, 36; 8 experts of 4096 x 4096 with 8 rows 27, 37, 37, and
+// 256-row tiles not for every unit: 192 rows -, 41, 60, 256 rows -, 44, 60, but 512
+// rows -, 77, 68.  (32-row tiles were not the fastest of any of these.)
 int tile_rows(const spg_grouped_desc *d, int epi)
 {
     const double mean = (double)d->rows / d->experts;
     if (mean <= (d->experts * cdiv(d->N, 256) < 256 ? 8 : 4)) return 16;
-    if (mean <= 112) return 128;
+    if (mean <= 96) return 128;
     return d->experts * cdiv((int64_t)mean, 256) * grouped_columns(d, epi, 256) < 256 ? 128 : 256;
 }
 

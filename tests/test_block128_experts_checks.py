@@ -104,7 +104,7 @@ def test_grouped_refusals(kw, call, want):
 
 def test_grouped_null_desc_and_tile_rows():
     assert grouped(None) == EINVAL
-    rows = (1, 8 * 8, 8 * 9, 8 * 112, 8 * 113)
+    rows = (1, 8 * 8, 8 * 9, 8 * 96, 8 * 97)
     assert [spg.grouped_tile_rows(n, 8, 512, 256) for n in rows] == [16, 16, 128, 128, 128]
     assert [spg.grouped_tile_rows(16 * n, 128, 512, 256) for n in rows] == [16, 128, 128, 128, 256]
     assert spg.grouped_tile_rows(64 * 5, 64, 2048, 256) == 128
