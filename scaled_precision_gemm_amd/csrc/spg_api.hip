@@ -627,27 +627,24 @@ SPG_EXPORT int gemm_scaled(void *out, const void *A, const void *sa, const void 
     // K-major operands: transposed copies (K contiguous) in the workspace,
     // on the call's stream ahead of the GEMM
     const uint8_t *A_nt = (const uint8_t *)A, *W_nt = (const uint8_t *)W;
+    TransposeJob jobs[2];
+    int njobs = 0;
     int64_t lda = d->lda, ldw = d->ldw, stride_a = d->stride_a, stride_w = d->stride_w;
     if (d->layout & SPG_LAYOUT_A_KMAJOR) {
         uint8_t *at = (uint8_t *)ws;
-        if (launch_transpose_u8(A_nt, d->K, d->M, d->lda, d->stride_a, d->stride_a ? d->batch : 1, at,
-                                transposed_ld(d), s) !=
-            hipSuccess)
-            return SPG_EHIP;
+        jobs[njobs++] = {A_nt, d->K, d->M, d->lda, d->stride_a, d->stride_a ? d->batch : 1, at, transposed_ld(d)};
         A_nt = at;
         lda = transposed_ld(d);
         stride_a = d->stride_a ? d->M * lda : 0;
     }
     if (d->layout & SPG_LAYOUT_W_KMAJOR) {
         uint8_t *wt = (uint8_t *)ws + t_a;
-        if (launch_transpose_u8(W_nt, d->K, d->N, d->ldw, d->stride_w, d->stride_w ? d->batch : 1, wt,
-                                transposed_ld(d), s) !=
-            hipSuccess)
-            return SPG_EHIP;
+        jobs[njobs++] = {W_nt, d->K, d->N, d->ldw, d->stride_w, d->stride_w ? d->batch : 1, wt, transposed_ld(d)};
         W_nt = wt;
         ldw = transposed_ld(d);
         stride_w = d->stride_w ? d->N * ldw : 0;
     }
+    if (njobs > 0 && launch_transpose_u8(jobs, njobs, s) != hipSuccess) return SPG_EHIP;
 
     GemmArgs g;
     memset(&g, 0, sizeof(g));

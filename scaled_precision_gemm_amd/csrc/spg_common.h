@@ -205,9 +205,14 @@ hipError_t launch_gemm_narrow(const GemmArgs &g, hipStream_t s);
 hipError_t launch_splitk_reduce(const GemmArgs &g, int64_t tiles, hipStream_t s);
 // [R, C] codes (row stride ld, batch stride bstride, 16-byte aligned rows)
 // -> [C, R] with row stride ldd (a multiple of 16, at least R), batch entries
-// C * ldd apart.
-hipError_t launch_transpose_u8(const uint8_t *src, int64_t R, int64_t C, int64_t ld, int64_t bstride,
-                               int64_t batch, uint8_t *dst, int64_t ldd, hipStream_t s);
+// C * ldd apart.  One launch for at most two of them.
+struct TransposeJob {
+    const uint8_t *src;
+    int64_t R, C, ld, bstride, batch;
+    uint8_t *dst;
+    int64_t ldd;
+};
+hipError_t launch_transpose_u8(const TransposeJob *jobs, int n, hipStream_t s);
 hipError_t launch_quantize_rowwise(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx,
                                    uint8_t *q, int64_t ldq, float *scale, hipStream_t s);
 hipError_t launch_quantize_tensor(const uint16_t *x, int64_t batch, int64_t rows, int64_t K,
