@@ -20,8 +20,8 @@
 //    straight into LDS (buffer loads to LDS), DEPTH slots, one barrier per
 //    stage (see the schedule below).
 //  * What bounds it: the matrix core at the clock that the card's power
-//    allows.  4096 x 34816 x 5120 SWIGLU: 590 us in a burst, 638 us (2.29
-//    PFLOP/s) sustained; the row-scaled kernel 552.  MFMAs are busy 55 % of the
+//    allows.  4096 x 34816 x 5120 SWIGLU: 590 us in a burst, 617 - 656
+//    us (2.3 PFLOP/s) sustained; the row-scaled kernel 552.  MFMAs are busy 55 % of the
 //    cycles (row-scaled 64 %): the four multiply-adds of a partial product
 //    take the issue slots of 7 % of a 16 x 16 x 128 MFMA's 32 cycles, a tile's
 //    fill and epilogue 6.8 us beside 1.57 us a stage.  4096 x 5120 x 6144 ADD
