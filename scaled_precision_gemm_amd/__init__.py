@@ -755,7 +755,10 @@ def _route_desc(logits, top, score, groups, top_groups, renormalize, scale):
           "logits must be a 2-D fp32 or bf16 tensor")
     _rows_ok("logits", logits, logits.dtype, logits.device)
     T, E = logits.shape
-    _need(score in _SCORE, f"unknown score {score}")
+    _need(isinstance(score, str) and score in _SCORE, f"unknown score {score}")
+    # plain numbers: they are part of the checked signature by value
+    _need(all(isinstance(v, int) for v in (top, groups, top_groups)) and isinstance(scale, (int, float)),
+          "top, groups and top_groups must be ints, scale a number")
     _need(1 <= top <= E, "top must be between 1 and the number of experts")
     _need(1 <= top_groups <= groups and E % groups == 0, "groups must divide the experts, top_groups be 1 .. groups")
     _need(math.isfinite(scale), "scale must be finite")

@@ -298,6 +298,10 @@ def test_route_binding():
     refuses("groups", r, t((5, 64), F32), 8, groups=7)
     refuses("groups", r, t((5, 64), F32), 8, groups=8, top_groups=9)
     refuses("finite", r, t((5, 64), F32), 8, scale=float("inf"))
+    # a tensor's value may change while its place in a signature does not
+    refuses("number", r, t((5, 64), F32), 8, scale=torch.tensor(2.5))
+    refuses("ints", r, t((5, 64), F32), torch.tensor(8))
+    refuses("ints", r, t((5, 64), F32), 8.0)
     refuses("bias", r, t((5, 64), F32), 8, bias=t((64,), BF))
     refuses("bias", r, t((5, 64), F32), 8, bias=t((63,), F32))
     s = spg.expert_sort
@@ -307,6 +311,7 @@ def test_route_binding():
     b = spg.expert_route_backward
     refuses("CUDA", b, t((5, 8), F32), t((5, 64), BF), t((5, 8), I32))
     refuses("grad_weights", b, t((5, 8), BF), t((5, 64), BF), t((5, 8), I32))
+    refuses("number", b, t((5, 8), F32), t((5, 64), BF), t((5, 8), I32), scale=torch.tensor(2.5))
     refuses("grad_weights", b, t((5, 7), F32), t((5, 64), BF), t((5, 8), I32))
     refuses("experts", b, t((5, 8), F32), t((6, 64), BF), t((5, 8), I32))
 
