@@ -375,7 +375,9 @@ int gemm_scaled(void *out, const void *A, const void *sa, const void *W, const v
  *   A         : codes [a_rows, K], row stride lda; with row_index a_rows *
  *               lda < 2^31 (else SPG_EUNSUPPORTED)
  *   W, sw     : codes [experts, N, K], row stride ldw, expert stride
- *               stride_w (bytes); sw [experts, ceil(N/128), ceil(K/128)]
+ *               stride_w (bytes; 0: all experts share one matrix of codes);
+ *               sw [experts, ceil(N/128), ceil(K/128)], one plane per expert
+ *               whatever stride_w is
  *   offsets   : device int32 [experts + 1], not decreasing, within [0, rows].
  *               The call cannot check device data: offsets are clamped to
  *               that range and a decreasing pair is an empty expert, so

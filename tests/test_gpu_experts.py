@@ -191,6 +191,21 @@ def test_grouped_no_rows_and_strides(spg):
     assert bool((big == 3.0).all())
 
 
+@pytest.mark.parametrize("epi", ["store", "swiglu"])
+@pytest.mark.parametrize("counts,bm", [([3, 0, 2, 4], 16), ([60, 0, 70, 33], 128), ([110] * 256, 256)])
+def test_grouped_one_weight_and_scales_of_each_expert(spg, counts, bm, epi):
+    # codes that all experts share (expert stride 0), a scale plane for each
+    E, R, K, N = len(counts), sum(counts), 272, 256
+    assert spg.grouped_tile_rows(R, E, N, K, epi) == bm
+    qa, sa = spg.quantize_block128(dev(bf16_normal((R, K), 1.0, 1)), "row")
+    qw, sw = spg.quantize_block128(dev(bf16_normal((N, K), 0.02, 2)), "block")
+    sw = sw[None] * torch.from_numpy(np.random.default_rng(3).uniform(0.25, 4.0, (E, *sw.shape)).astype(np.float32)).cuda()
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    out = spg.gemm_grouped(qa, sa, qw[None].expand(E, N, K), sw, i32(offsets), epi)
+    for e, (lo, hi, y, S) in grouped_ref(qa, sa, qw[None].expand(E, N, K), sw, offsets, None, epi).items():
+        check(out[lo:hi], y, S, f"expert {e}")
+
+
 # ---- routing -----------------------------------------------------------------------
 
 def route_ref(x, top, score="softmax", bias=None, groups=1, top_groups=1, renorm=True, scale=1.0):
