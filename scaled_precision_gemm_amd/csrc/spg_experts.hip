@@ -538,7 +538,7 @@ __global__ __launch_bounds__(kRouteThreads) void count_kernel(const RouteArgs a)
 // With q_j the chosen scores' shares:
 //   renormalised:  d/dl of scale q_j; softmax over the chosen (the softmax's
 //                  own sum cancels): dl_j = scale q_j (g_j - sum g q)
-//                  sigmoid: dp_j = scale (g_j - sum g q) / sum p, dl = dp p (1 - p)
+//                  sigmoid: dl_j = scale q_j (1 - p_j) (g_j - sum g q)
 //   else softmax:  dl_e = p_e ([e chosen] scale g - sum scale g p)
 //   else sigmoid:  dl_j = scale g_j p_j (1 - p_j)
 // One wave per token: lane j < top works out choice j, then the wave writes
@@ -581,16 +581,18 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
         } else {
             mine = q * (g - dot);
         }
+    } else if (a.renorm) {
+        // the shares in 64 bits, as the forward pass forms them: in 32 the
+        // scores of logits below -88 are 0 and 1 / z overflows, though the
+        // shares are ordinary numbers
+        const double p = e >= 0 ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
+        const double z = team_sum<64>(p), q = z > 0.0 ? p / z : 0.0;
+        const double dot = team_sum<64>((double)g * q);
+        mine = (float)(q / (1.0 + exp((double)l)) * ((double)g - dot));
     } else {
         // 1 - p as the sigmoid of -l: exact where p rounds to 1
         const float p = e >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f, n = e >= 0 ? 1.0f / (1.0f + expf(l)) : 0.0f;
-        if (a.renorm) {
-            const float z = team_sum<64>(p);
-            const float dot = team_sum<64>(g * p);
-            mine = z > 0.0f ? (g - dot / z) / z * (p * n) : 0.0f;
-        } else {
-            mine = g * p * n;
-        }
+        mine = g * p * n;
     }
     // four columns per lane, every choice compared with each
     const bool vec = a.E % 4 == 0 && ((uintptr_t)a.grad_logits & (BF16 ? 7u : 15u)) == 0;

@@ -482,6 +482,28 @@ def test_route_backward_against_differences(spg, score, renorm):
             assert abs((f(t, up) - f(t, dn)) / (2 * h) - float(got[t, e])) < 2.0 ** -18
 
 
+@pytest.mark.parametrize("base", [0.0, -80.0, -87.0, -88.5, -89.0, -110.0, -200.0, -700.0])
+@pytest.mark.parametrize("T,E,top", [(4, 8, 2), (9, 64, 8), (5, 300, 32)])
+def test_route_backward_of_small_sigmoid_scores(spg, base, T, E, top):
+    # every score of a token far below the smallest fp32 number, or around
+    # it: the shares, and so the gradient, are ordinary numbers
+    x = torch.from_numpy(logits(T, E, E, 0.6) + np.float32(base)).bfloat16().float().numpy()
+    x[0, 3:] = -np.inf
+    g = np.random.default_rng(E).standard_normal((T, top)).astype(np.float32)
+    for dt, step in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        lg = torch.from_numpy(x).cuda().to(dt)
+        r = spg.expert_route(lg, top, score="sigmoid", scale=2.5)
+        ids = r.experts.cpu().numpy()
+        got = spg.expert_route_backward(torch.from_numpy(g).cuda(), lg, r.experts, score="sigmoid", scale=2.5)
+        got = got.double().cpu().numpy()
+        assert np.isfinite(got).all()
+        with np.errstate(over="ignore"):
+            d, size = route_grad_ref(np.where(np.isfinite(x), x, -700.0), ids, g, "sigmoid", True, 2.5)
+        # scores, shares and sums in fp64; the incoming gradient times the scale
+        # rounded to fp32 (once in each of the two differences), one rounding out
+        assert (np.abs(got - d) <= 3 * 2.0 ** -24 * size + np.abs(d) * step + 2.0 ** -126).all()
+
+
 def test_route_backward_repeated_and_missing_experts(spg):
     # experts chosen elsewhere: the same one twice gets both parts, -1 none
     x = logits(2, 8, 1)
