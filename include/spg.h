@@ -470,8 +470,7 @@ int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32_t E, int32
  * weights: grad_weights fp32 [T, top], logits and experts of expert_route,
  * the same desc (bias and groups have no gradient: the choice is constant);
  * grad_logits [T, E] contiguous in the logits' type, written whole.  fp32
- * arithmetic (the shares of renormalised sigmoids in 64 bits, as in
- * expert_route), one rounding.  With renormalize a softmax's gradient reaches
+ * arithmetic, one rounding.  With renormalize a softmax's gradient reaches
  * the chosen experts only (the others cancel).
  */
 int expert_route_backward(const float *grad_weights, const void *logits, const int32_t *experts, void *grad_logits,

@@ -582,13 +582,17 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
             mine = q * (g - dot);
         }
     } else if (a.renorm) {
-        // the shares in 64 bits, as the forward pass forms them: in 32 the
-        // scores of logits below -88 are 0 and 1 / z overflows, though the
-        // shares are ordinary numbers
-        const double p = e >= 0 ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
-        const double z = team_sum<64>(p), q = z > 0.0 ? p / z : 0.0;
-        const double dot = team_sum<64>((double)g * q);
-        mine = (float)(q / (1.0 + exp((double)l)) * ((double)g - dot));
+        // p = exp(min(l, 0)) / (1 + exp(-|l|)), taken relative to the largest
+        // chosen score where all are small: in 32 bits p is 0 below logits of
+        // -88 and 1 / sum p overflows, though the shares are ordinary numbers.
+        // (64-bit shares instead: 8192 tokens of 128 experts 6.8 us, 5.9 so.)
+        // Where exp(-l) overflows 64 bits the weights are 0, and so is this.
+        const bool some = mx > -709.7827f;
+        const float t = expf(-fabsf(l));
+        const float u = some && e >= 0 ? expf(fminf(l, 0.0f) - fminf(mx, 0.0f)) / (1.0f + t) : 0.0f;
+        const float z = team_sum<64>(u), q = z > 0.0f ? u / z : 0.0f;
+        const float dot = team_sum<64>(g * q);
+        mine = q * ((l < 0.0f ? 1.0f : t) / (1.0f + t)) * (g - dot);
     } else {
         // 1 - p as the sigmoid of -l: exact where p rounds to 1
         const float p = e >= 0 ? 1.0f / (1.0f + expf(-l)) : 0.0f, n = e >= 0 ? 1.0f / (1.0f + expf(l)) : 0.0f;
