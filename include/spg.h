@@ -471,7 +471,8 @@ int expert_sort(const int32_t *experts, int64_t T, int32_t top, int32_t E, int32
  * the same desc (bias and groups have no gradient: the choice is constant);
  * grad_logits [T, E] contiguous in the logits' type, written whole.  fp32
  * arithmetic, one rounding.  With renormalize a softmax's gradient reaches
- * the chosen experts only (the others cancel).
+ * the chosen experts only (the others cancel).  A token with a NaN logit, whose
+ * weights are NaN, gets a row of NaN.
  */
 int expert_route_backward(const float *grad_weights, const void *logits, const int32_t *experts, void *grad_logits,
                           const spg_route_desc *d, void *stream);

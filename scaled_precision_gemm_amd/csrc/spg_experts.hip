@@ -542,7 +542,8 @@ __global__ __launch_bounds__(kRouteThreads) void count_kernel(const RouteArgs a)
 //   else softmax:  dl_e = p_e ([e chosen] scale g - sum scale g p)
 //   else sigmoid:  dl_j = scale g_j p_j (1 - p_j)
 // One wave per token: lane j < top works out choice j, then the wave writes
-// the dense row.  An expert that stands twice in a row gets both parts.
+// the dense row (NaN where a logit of the token is).  An expert that stands
+// twice in a row gets both parts.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArgs a)
 {
@@ -550,17 +551,24 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
     const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
     if (t >= a.T) return;
     const bool soft = a.score == SPG_SCORE_SOFTMAX;
+    // on their way while the experts and then their logits are
+    const float first = load_logit<BF16>(a, t, min(lane, a.E - 1)), second = load_logit<BF16>(a, t, min(lane + 64, a.E - 1));
     int32_t e = lane < a.top ? a.experts[t * a.top + lane] : -1;
     if ((uint32_t)e >= (uint32_t)a.E) e = -1;
     const float g = e >= 0 ? a.grad[t * a.top + lane] * a.scale : 0.0f;
     const float l = e >= 0 ? load_logit<BF16>(a, t, e) : -INFINITY;
     float mine = 0.0f, common = 0.0f, mx = -INFINITY, rz = 0.0f;
     const bool dense = soft && !a.renorm;
-    if (dense) {
-        for (int i = lane; i < a.E; i += 64) mx = fmaxf(mx, load_logit<BF16>(a, t, i));
-    } else {
-        mx = l;
+    // a NaN logit, chosen or not, makes its token's weights NaN: and so its gradient
+    bool nan = first != first || second != second;
+    if (dense) mx = fmaxf(first, second);
+    for (int i0 = 128; i0 < a.E; i0 += 64) {
+        const float v = load_logit<BF16>(a, t, min(i0 + lane, a.E - 1));
+        nan = nan || v != v;
+        if (dense) mx = fmaxf(mx, v);
     }
+    const float zero = __any(nan) ? __uint_as_float(0x7FC00000u) : 0.0f;
+    if (!dense) mx = l;
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
     auto ex = [&](float v) { return v == mx ? 1.0f : expf(v - mx); };
@@ -605,7 +613,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteArg
         float v[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            v[c] = dense && i + c < a.E ? -ex(load_logit<BF16>(a, t, i + c)) * rz * common : 0.0f;
+            v[c] = dense && i + c < a.E ? -ex(load_logit<BF16>(a, t, i + c)) * rz * common + zero : zero;
         for (int j = 0; j < a.top; ++j) {
             const int32_t ej = __builtin_amdgcn_readlane(e, j) - i;
             const float mj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), j));

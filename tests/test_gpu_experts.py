@@ -506,6 +506,34 @@ def test_route_backward_of_small_sigmoid_scores(spg, base, T, E, top):
         assert (np.abs(got - d) <= (2 * reach + 42) * 2.0 ** -24 * size + np.abs(d) * step + 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_route_backward_of_nan_logits(spg, score, renorm, dt):
+    # a NaN logit makes all weights of its token NaN, and so its gradient;
+    # chosen or not, the only one, with fewer experts than places; other
+    # tokens keep theirs
+    for E, top in ((1, 1), (7, 3), (300, 8)):
+        x = logits(6, E, E)
+        clean = torch.from_numpy(x).cuda().to(dt)
+        x[1, E - 1] = x[4, 0] = np.nan
+        x[5] = np.nan
+        if E > 2:
+            x[2, 1:] = -np.inf
+            x[3] = -np.inf
+            x[4, 2:] = -np.inf
+            clean[2, 1:] = clean[3] = -np.inf
+        lg = torch.from_numpy(x).cuda().to(dt)
+        g = torch.randn(6, top, generator=torch.Generator().manual_seed(E)).cuda()
+        how = dict(score=score, renormalize=renorm, scale=1.7)
+        r = spg.expert_route(lg, top, **how)
+        assert bool(r.weights[[1, 4, 5]].isnan().all()) and not bool(r.weights[[0, 2, 3]].isnan().any())
+        got = spg.expert_route_backward(g, lg, r.experts, **how)
+        assert bool(got[[1, 4, 5]].isnan().all())
+        want = spg.expert_route_backward(g, clean, spg.expert_route(clean, top, **how).experts, **how)
+        assert torch.equal(got[[0, 2, 3]], want[[0, 2, 3]]) and bool(got[[0, 2, 3]].isfinite().all())
+
+
 def test_route_backward_repeated_and_missing_experts(spg):
     # experts chosen elsewhere: the same one twice gets both parts, -1 none
     x = logits(2, 8, 1)
