@@ -417,11 +417,14 @@ int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
  *             ties (experts' and groups') to the lowest index
  *   weights : scale p / (sum of the chosen p) with renormalize, else scale p
  * The bias steers the choice only.  p and c are computed and compared in 64
- * bits (without bias and with one group, the logits are compared).
+ * bits (without bias and with one group, the logits are compared).  The shares
+ * of chosen p that 64 bits cannot hold (a softmax's, far below its largest
+ * logit) are those of exp(l - largest chosen l); weights of sigmoids that are
+ * all 0 in 64 bits (logits below -709.78) are 0.
  * A logit or c of -inf is never chosen: where fewer than `top` experts are
  * left, the remaining places get expert -1 and weight 0, so a token whose
  * logits are all -inf has no expert.  A NaN logit is never chosen and makes
- * its token's weights NaN.
+ * its token's weights NaN; an expert whose bias is NaN is never chosen.
  *   logits  : [T, E], fp32 or (logits_bf16) bf16, row stride ld elements
  *   bias    : fp32 [E] or NULL
  *   weights : fp32 [T, top]

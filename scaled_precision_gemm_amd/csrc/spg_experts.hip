@@ -260,10 +260,11 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool 
         mx = l[i] > mx ? l[i] : mx;
     }
     nan = team_ballot<TEAM>(nan) != 0;
-    {   // the largest logit, through the keys
-        const uint32_t k = team_max<TEAM>(key32(mx));
-        mx = k == 0u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
-    }
+    auto largest = [](float v) {                          // over the team, through the keys
+        const uint32_t k = team_max<TEAM>(key32(v));
+        return k == 0u ? -INFINITY : __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
+    };
+    mx = largest(mx);
     const bool soft = a.score == SPG_SCORE_SOFTMAX;
     // score of a logit before the softmax's division; an infinite maximum
     // counts as the only size that matters (1 for it, 0 for the others)
@@ -340,7 +341,18 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, int64_t t, bool 
         for (int i = 0; i < EPL; ++i) hi[i] = tl * EPL + i == e ? 0u : hi[i];
         my_e = tl == j ? e : my_e;
     }
-    double p = live && my_e >= 0 ? raw(load_logit<BF16>(a, t, my_e)) : 0.0;
+    const bool there = live && my_e >= 0;
+    const float chosen = there ? load_logit<BF16>(a, t, my_e) : -INFINITY;
+    double p = there ? raw(chosen) : 0.0;
+    if (a.renorm && __any(there && p < 0x1p-860)) {
+        // scores (below e^-596) from which 64 bits lose digits or everything -
+        // a bias or a group can choose experts far below the largest logit:
+        // shares relative to the largest chosen one.  Sigmoids that are all 0
+        // in 64 bits stay 0.
+        const float mc = largest(chosen);
+        const bool far = soft ? (double)mc - (double)mx < -600.0 : mc < -600.0f && mc > -709.7827f;
+        if (there && far) p = exp((double)chosen - (double)mc);
+    }
     if (soft && !a.renorm) p = z > 0.0 ? p / z : 0.0;
     const double total = a.renorm ? team_sum<TEAM>(p) : 1.0;
     double w = total > 0.0 ? (double)a.scale * (p / total) : 0.0;

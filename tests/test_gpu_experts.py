@@ -359,6 +359,66 @@ def test_route_masks(spg, T):
             check_route(spg, x, 8, score=score, renormalize=renorm, groups=8, top_groups=2, bias=bias)
 
 
+@pytest.mark.parametrize("T", [6, 300, 4200])
+@pytest.mark.parametrize("gap", [300, 590, 640, 710, 740, 800, 2.0 ** 100])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_chosen_far_below_the_largest_logit(spg, T, gap, groups):
+    # the bias steers to experts whose softmax scores are tiny, or 0 even in 64
+    # bits: their shares are the softmax over the chosen ones all the same
+    E, top = 64, 5
+    x = logits(T, E, 12)
+    x[:, 16:] = (x[:, 16:] - np.float32(gap)).astype(np.float32)
+    x[:, 22] -= 70
+    x = torch.from_numpy(x).bfloat16().float().numpy()
+    bias = np.zeros(E, np.float32)
+    bias[:16] = -4.0
+    bias[20:25] = 8.0
+    X = np.tile(np.arange(20, 25), (T, 1))
+    l = x[:, 20:25].astype(np.float64)   # noqa: E741
+    q = np.exp(l - l.max(1, keepdims=True))
+    q /= q.sum(1, keepdims=True)
+    g = np.random.default_rng(T).standard_normal((T, top)).astype(np.float32)
+    for dt, step in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        lg = torch.from_numpy(x).cuda().to(dt)
+        r = spg.expert_route(lg, top, bias=torch.from_numpy(bias).cuda(), groups=groups, top_groups=1, scale=1.5)
+        ids = r.experts.cpu().numpy()
+        assert np.array_equal(np.sort(ids, 1), X)
+        order = ids - 20
+        # fp64 scores (a few 2^-52) and one rounding to fp32
+        np.testing.assert_allclose(r.weights.cpu().numpy(), 1.5 * np.take_along_axis(q, order, 1), rtol=1.01 * 2.0 ** -24,
+                                   atol=2.0 ** -140)
+        got = spg.expert_route_backward(torch.from_numpy(g).cuda(), lg, r.experts, scale=1.5).double().cpu().numpy()
+        qo, lo = np.take_along_axis(q, order, 1), np.take_along_axis(l, order, 1)
+        want = 1.5 * qo * (g - (g * qo).sum(1, keepdims=True))
+        # the bound of test_route_backward with the chosen logits' reach
+        tol = qo * 3.0 * np.abs(g).max(1, keepdims=True) * (2 * np.ptp(lo, 1)[:, None] + 42) * 2.0 ** -24
+        assert (np.abs(np.take_along_axis(got, ids, 1) - want) <= tol + np.abs(want) * step + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("T", [5, 4200])
+@pytest.mark.parametrize("base", [-596.0, -604.0, -700.0, -708.0, -712.0])
+def test_route_of_small_sigmoid_scores(spg, T, base):
+    # scores at the lower end of 64 bits: ordinary shares down to where exp(-l)
+    # of the largest chosen one overflows (-709.78), weights and gradients of 0 below
+    E, top = 40, 8
+    x = np.full((T, E), -np.inf, np.float32)
+    x[:, 3:23] = np.random.default_rng(1).permuted(np.tile(base - 4.0 * np.arange(20), (T, 1)), axis=1)   # exact in bf16
+    l = base - 4.0 * np.arange(top)   # noqa: E741
+    q = np.exp(l - base) / np.exp(l - base).sum() if base > -709 else np.zeros(top)
+    g = np.random.default_rng(T).standard_normal((T, top)).astype(np.float32)
+    want = 2.5 * q * (g - (g * q).sum(1, keepdims=True))
+    tol = 5.0 * q * np.abs(g).max(1, keepdims=True) * (2 * np.ptp(l) + 42) * 2.0 ** -24 + 2.0 ** -126
+    for dt, step in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        lg = torch.from_numpy(x).cuda().to(dt)
+        r = spg.expert_route(lg, top, score="sigmoid", scale=2.5)
+        ids = r.experts.cpu().numpy()
+        assert np.array_equal(np.take_along_axis(x, ids, 1), np.tile(l, (T, 1)))
+        np.testing.assert_allclose(r.weights.cpu().numpy(), np.tile(2.5 * q, (T, 1)), rtol=1.01 * 2.0 ** -24, atol=2.0 ** -140)
+        got = spg.expert_route_backward(torch.from_numpy(g).cuda(), lg, r.experts, score="sigmoid", scale=2.5)
+        got = np.take_along_axis(got.double().cpu().numpy(), ids, 1)
+        assert (np.abs(got - want) <= tol + np.abs(want) * step).all()
+
+
 def test_route_strided_logits_and_no_order(spg):
     x = logits(90, 128, 3)
     wide = torch.zeros((90, 200), device="cuda")
