@@ -221,6 +221,12 @@ typedef enum {
     SPG_LAYOUT_W_KMAJOR = 2    /* W stored [K, N]: ldw >= N                    */
 } spg_layout;
 
+/* Operands with scales of their own for each batch entry (spg_gemm_desc.scale_batch). */
+enum {
+    SPG_SCALE_BATCH_A = 1,
+    SPG_SCALE_BATCH_W = 2
+};
+
 /*
  * Output split along N (split-N epilogue): the output columns of one product
  * go to up to SPG_MAX_OUT_SPLITS separate matrices, one per column range -
@@ -298,6 +304,10 @@ typedef struct spg_out_split {
  *              >= N; multiples of 16), stride_a / stride_w the stored batch
  *              strides; sa / sw keep their meaning (per output row / column,
  *              or per tensor).
+ *   scale_batch : SPG_SCALE_BATCH_* flags (0 by default), E4M3_BLOCK128 only
+ *              (other formats: SPG_EUNSUPPORTED).  The operand has a scale
+ *              plane for each batch entry although its batch stride is 0 (all
+ *              entries share its codes).
  */
 typedef struct spg_gemm_desc {
     int64_t M, N, K, batch;
@@ -311,7 +321,7 @@ typedef struct spg_gemm_desc {
     const float *bias_scale;
     const spg_out_split *out_split;
     int32_t layout;
-    int32_t reserved2;
+    int32_t scale_batch;
 } spg_gemm_desc;
 
 /* Zero every field, set batch = 1 and the dense strides for M, N, K. */
@@ -331,9 +341,10 @@ void spg_gemm_desc_init(spg_gemm_desc *d, int64_t M, int64_t N, int64_t K, int32
  *              sa [ceil(K/128), M] (row groups of A, or column groups of a
  *              K-major A), sw the 128 x 128 blocks of W as it is stored:
  *              [ceil(N/128), ceil(K/128)], K-major [ceil(K/128),
- *              ceil(N/128)]; batch entries back to back unless that
- *              operand's batch stride is 0.  SWIGLU needs N % 256 == 0: the
- *              up rows start on a block boundary
+ *              ceil(N/128)]; batch entries back to back, one plane for all
+ *              where that operand's batch stride is 0 and d->scale_batch does
+ *              not name it.  SWIGLU needs N % 256 == 0: the up rows start on a
+ *              block boundary
  *   residual : bf16 [M, N] (or one row [N] when ldr == 0; E4M3 codes [N]
  *              when d->bias_scale is set), required for SPG_EPI_ADD, NULL
  *              otherwise; it may be the output itself (residual == out,

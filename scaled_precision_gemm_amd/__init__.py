@@ -48,6 +48,7 @@ class SpgError(RuntimeError):
 
 MAX_OUT_SPLITS = 8
 LAYOUT_NT, LAYOUT_A_KMAJOR, LAYOUT_W_KMAJOR = 0, 1, 2
+SCALE_BATCH_A, SCALE_BATCH_W = 1, 2
 
 
 class OutSplit(ctypes.Structure):
@@ -67,7 +68,7 @@ class GemmDesc(ctypes.Structure):
         ("format", ctypes.c_int32), ("scale_layout", ctypes.c_int32),
         ("tscale_a", ctypes.c_void_p), ("tscale_w", ctypes.c_void_p),
         ("clock_probe", ctypes.c_void_p), ("bias_scale", ctypes.c_void_p),
-        ("out_split", ctypes.POINTER(OutSplit)), ("layout", ctypes.c_int32), ("reserved2", ctypes.c_int32),
+        ("out_split", ctypes.POINTER(OutSplit)), ("layout", ctypes.c_int32), ("scale_batch", ctypes.c_int32),
     ]
 
 
@@ -364,6 +365,10 @@ def make_desc(A: torch.Tensor, W: torch.Tensor, fmt, epilogue, out=None, residua
     d.lda, d.ldw = A3.stride(1), W3.stride(1)
     d.stride_a = A3.stride(0) if A3.shape[0] > 1 else 0
     d.stride_w = W3.stride(0) if W3.shape[0] > 1 else 0
+    if fmt == FMT_E4M3_BLOCK128:
+        # an operand expanded over the batch: one matrix of codes, a scale plane for each entry
+        d.scale_batch = ((SCALE_BATCH_A if A3.shape[0] > 1 and d.stride_a == 0 else 0)
+                         | (SCALE_BATCH_W if W3.shape[0] > 1 and d.stride_w == 0 else 0))
     n_out = N // 2 if epi == EPI_SWIGLU else N
     if out is not None:
         o3 = out if out.dim() == 3 else out.unsqueeze(0)
@@ -514,7 +519,9 @@ def gemm_scaled(A, sa, W, sw, epilogue="store", residual=None, fmt="e4m3_row",
            [ceil(N/128),ceil(K/128)] ([B, ...] each when batched), as
            quantize_block128 wrote them with tiling "row" (a K-major A:
            "column") and "block" (a K-major W keeps the blocks of its stored
-           [K,N]: sw [ceil(K/128),ceil(N/128)]); "swiglu" needs N % 256 == 0
+           [K,N]: sw [ceil(K/128),ceil(N/128)]); "swiglu" needs N % 256 == 0.
+           Entries of an operand that is expanded over the batch have their
+           own scales (in the other formats those of its first entry)
     clock_probe: optional int64 tensor of 4 elements on the same device; the
            main GEMM launch records its clock counters there (see
            spg_gemm_desc.clock_probe): shader clock in GHz =

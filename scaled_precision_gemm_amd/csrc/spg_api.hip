@@ -75,6 +75,8 @@ int validate_desc(const spg_gemm_desc *d, int epi)
             return SPG_EUNSUPPORTED;
     }
     if (d->layout < 0 || d->layout > (SPG_LAYOUT_A_KMAJOR | SPG_LAYOUT_W_KMAJOR)) return SPG_EINVAL;
+    if (d->scale_batch & ~(SPG_SCALE_BATCH_A | SPG_SCALE_BATCH_W)) return SPG_EINVAL;
+    if (d->scale_batch && d->format != SPG_FMT_E4M3_BLOCK128) return SPG_EUNSUPPORTED;
     if ((d->lda & 15) || (d->ldw & 15)) return SPG_EINVAL;
     // a 256-row tile of codes must fit the 31-bit range of a buffer resource
     if (d->lda > (INT64_C(1) << 23) || d->ldw > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
@@ -532,8 +534,10 @@ static int run_block(const spg_gemm_desc *d, const spg_plan &p, const GemmArgs &
     // W's scales lie as W is stored
     a.sw_rs = (int32_t)((d->layout & SPG_LAYOUT_W_KMAJOR) ? 1 : groups);
     a.sw_gs = (int32_t)((d->layout & SPG_LAYOUT_W_KMAJOR) ? blocks : 1);
-    a.g.sa_bstride = groups * d->M;
-    a.g.sw_bstride = blocks * groups;
+    // one plane for all entries where the codes are one matrix, unless the
+    // caller has one for each
+    a.g.sa_bstride = d->stride_a || (d->scale_batch & SPG_SCALE_BATCH_A) ? groups * d->M : 0;
+    a.g.sw_bstride = d->stride_w || (d->scale_batch & SPG_SCALE_BATCH_W) ? blocks * groups : 0;
     a.g.clocks = d->clock_probe;
     if (p.kernel == 6) {
         a.g.tiles_m = 1;

@@ -9,8 +9,10 @@ namespace spg {
 
 // GemmArgs first: it starts the kernel-argument segment (see out_at).
 // Scale planes: sa [groups, a_rows] (group-major; batch entries
-// g.sa_bstride floats apart), sw with the block of W row n and K group k at
-// (n / 128) * sw_rs + k * sw_gs (batch entries / experts g.sw_bstride apart).
+// g.sa_bstride floats apart; experts: 0), sw with the block of W row n and K
+// group k at (n / 128) * sw_rs + k * sw_gs (batch entries / experts
+// g.sw_bstride apart).  A stride of 0 is one plane for all, whatever the
+// codes' strides are.
 struct BlockArgs {
     GemmArgs g;
     int64_t a_rows;           // rows of A and of its scale plane

@@ -120,9 +120,8 @@ __device__ __forceinline__ void block_tile(const BlockArgs &a, const Tile &T, in
     vw[1] = (uint32_t)(w_in + (int)rib) * (uint32_t)g.ldw + c_odd * 16u;
     // scales: lane l the token scale of the wave's row l, lanes 0 .. 3 the
     // weight scales of its four 32-row blocks
-    const float *sa = (const float *)g.sa + ((!EXPERTS && g.stride_a) ? T.b * g.sa_bstride : 0);
-    // (every expert has scales of its own, also where all share their codes)
-    const float *sw = (const float *)g.sw + (EXPERTS || g.stride_w ? T.b * g.sw_bstride : 0);
+    const float *sa = (const float *)g.sa + T.b * g.sa_bstride;
+    const float *sw = (const float *)g.sw + T.b * g.sw_bstride;
     uint32_t vsa, vsw = kOOB;
     {
         const uint32_t r = (uint32_t)(wm * G::kStrip + ln);

@@ -114,9 +114,9 @@ __global__ __launch_bounds__(kNarrowThreads) void gemm_block_narrow_kernel(const
         }
     // scales of a chunk: lane l the token scale of tile row l, lane nb the
     // weight scale of block nb
-    const float *sa = (const float *)g.sa + ((!EXPERTS && g.stride_a) ? b * g.sa_bstride : 0) + (gather ? 0 : m0);
+    const float *sa = (const float *)g.sa + b * g.sa_bstride + (gather ? 0 : m0);
     const uint32_t sa_bytes = (uint32_t)((gather ? a.a_rows : a_rows) * 4);
-    const v4i rsw = make_rsrc((const float *)g.sw + (EXPERTS || g.stride_w ? b * g.sw_bstride : 0), (uint32_t)a.sw_words * 4u);
+    const v4i rsw = make_rsrc((const float *)g.sw + b * g.sw_bstride, (uint32_t)a.sw_words * 4u);
     uint32_t vsa, vsw = kOOB;
     {
         bool ok;

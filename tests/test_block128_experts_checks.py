@@ -60,6 +60,18 @@ def test_gemm_refusals():
     assert gemm(d) == EUNSUP                                   # row stride
 
 
+def test_scales_of_each_entry_flags():
+    d = desc(64, 64, 256)
+    plan = spg.Plan()
+    check = lambda: spg.lib.spg_gemm_plan(ctypes.byref(d), 0, 256, ctypes.byref(plan))  # noqa: E731
+    for flags, want in ((0, 0), (1, 0), (2, 0), (3, 0), (4, EINVAL), (-1, EINVAL)):
+        d.scale_batch = flags
+        assert check() == want
+    spg.lib.spg_gemm_desc_init(ctypes.byref(d), 64, 64, 256, spg.FMT_E4M3_ROW)
+    d.scale_batch = 1
+    assert check() == EUNSUP
+
+
 @pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 128, 129, 1000, 4096, 100000])
 @pytest.mark.parametrize("N", [16, 512, 5120, 34816])
 @pytest.mark.parametrize("K", [16, 1024, 5120, 17408])

@@ -242,6 +242,35 @@ def test_batch(spg, M, share):
         check(out[b], y, S, f"batch {b}")
 
 
+@pytest.mark.parametrize("M,K", [(8, 400), (150, 400), (40, 8208)])
+@pytest.mark.parametrize("share", ["a", "w", "both"])
+@pytest.mark.parametrize("kmajor", [False, True])
+def test_one_matrix_and_scales_of_each_entry(spg, M, K, share, kmajor):
+    # an operand expanded over the batch (batch stride 0) with a scale plane
+    # for each entry: 16-row, 128-row and K-split kernels
+    N, nb = 272, 3
+    rng = np.random.default_rng(M)
+
+    def operand(rows, std, tiling, seed, shared):
+        x = bf16_normal((rows, K) if shared else (nb, rows, K), std, seed)
+        q, s = spg.quantize_block128(dev(x), tiling)
+        if shared:
+            f = rng.uniform(0.25, 4.0, (nb, *s.shape)).astype(np.float32)
+            q, s = q[None].expand(nb, *q.shape), s[None] * torch.from_numpy(f).cuda()
+        return q, s
+    qa, sa = operand(M, 1.0, "row", 31, share != "w")
+    qw, sw = operand(N, 0.02, "block", 32, share != "a")
+    w, s = qw, sw
+    if kmajor:                               # the same values with W stored [K, N]
+        w = qw[0].t().contiguous()[None].expand(nb, K, N) if share != "a" else qw.transpose(1, 2).contiguous()
+        s = sw.transpose(1, 2).contiguous()
+    out = spg.gemm_scaled(qa, sa, w, s, fmt="e4m3_block128", w_kmajor=kmajor)
+    for b in range(nb):
+        D, S = sums(qa[b], sa[b], qw[b], sw[b])
+        y, S, _ = oracle.epilogue("store", D, S, 1.0, 1.0)
+        check(out[b], y, S, f"batch {b}")
+
+
 @pytest.mark.parametrize("M", [9, 64, 300])
 def test_bias_rows_splits_and_strides(spg, M):
     N, K = 520, 2064
