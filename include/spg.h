@@ -415,7 +415,8 @@ int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const
                  const int32_t *row_index, int epilogue, const spg_grouped_desc *d, void *stream);
 
 /* Rows of the tiles gemm_grouped takes for `d` (16, 128 or 256), chosen
- * from rows / experts and the number of tiles; 0 for an invalid call.  Host query. */
+ * from rows / experts and the number of tiles; 0 for an invalid call (a_rows is
+ * not looked at: the rows may be gathered).  Host query. */
 int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
 
 /*

@@ -121,7 +121,9 @@ int64_t most_tiles(const spg_grouped_desc *d, int bm)
     return most < d->rows ? most : d->rows;
 }
 
-int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
+// Checks that do not depend on whether rows are gathered (a_rows is then free,
+// but addressed with 31-bit offsets).
+int validate_grouped(const spg_grouped_desc *d, int epi)
 {
     if (!d) return SPG_EINVAL;
     if (epi != SPG_EPI_STORE && epi != SPG_EPI_ADD && epi != SPG_EPI_SWIGLU) return SPG_EINVAL;
@@ -130,7 +132,6 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
     if (d->experts < 1) return SPG_EINVAL;
     if (d->experts > 65536) return SPG_EUNSUPPORTED;
     if (epi == SPG_EPI_SWIGLU && (d->N % 256)) return SPG_EINVAL;
-    if (!indexed && d->a_rows < d->rows) return SPG_EINVAL;
     if (d->lda < d->K || d->ldw < d->K || (d->lda & 15) || (d->ldw & 15)) return SPG_EINVAL;
     if (d->lda > (INT64_C(1) << 23) || d->ldw > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
     if (d->stride_w < 0 || (d->stride_w & 15)) return SPG_EINVAL;
@@ -141,7 +142,6 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
     if (d->rows >= kMaxWords || d->a_rows >= kMaxWords || d->N >= kMaxWords || d->K >= kMaxWords ||
         cdiv(d->N, 128) * cdiv(d->K, 128) >= kMaxWords)
         return SPG_EUNSUPPORTED;
-    if (indexed && d->a_rows * d->lda >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
     const int bm = tile_rows(d, epi);
     if (most_tiles(d, bm) * grouped_columns(d, epi, bm) >= kMaxGrid) return SPG_EUNSUPPORTED;
     return SPG_OK;
@@ -151,15 +151,17 @@ int validate_grouped(const spg_grouped_desc *d, int epi, bool indexed)
 
 SPG_EXPORT int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue)
 {
-    return validate_grouped(d, epilogue, false) == SPG_OK ? tile_rows(d, epilogue) : 0;
+    return validate_grouped(d, epilogue) == SPG_OK ? tile_rows(d, epilogue) : 0;
 }
 
 SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const float *sw,
                             const int32_t *offsets, const int32_t *row_index, int epilogue, const spg_grouped_desc *d,
                             void *stream)
 {
-    const int v = validate_grouped(d, epilogue, row_index != nullptr);
+    const int v = validate_grouped(d, epilogue);
     if (v != SPG_OK) return v;
+    if (!row_index && d->a_rows < d->rows) return SPG_EINVAL;
+    if (row_index && d->a_rows * d->lda >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
     const int64_t nout = grouped_nout(d, epilogue);
     if (d->rows == 0 || nout == 0) return SPG_OK;
     if (!out || !A || !sa || !W || !sw || !offsets) return SPG_EINVAL;

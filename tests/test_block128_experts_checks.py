@@ -123,6 +123,15 @@ def test_grouped_null_desc_and_tile_rows():
     assert spg.grouped_tile_rows(8, 8, 500, 24) == 0
 
 
+@pytest.mark.parametrize("a_rows", [0, 4096, 32768, 2 ** 28])
+def test_tile_rows_of_gathered_rows(a_rows):
+    # the first product of an experts' layer: more output rows than rows of A
+    d = grouped_desc(rows=32768, a_rows=a_rows, N=2048, K=2048, lda=2048, ldw=2048, stride_w=2048 * 2048, ldo=2048,
+                     experts=64)
+    assert spg.lib.spg_grouped_tile_rows(ctypes.byref(d), 0) == 256
+    assert spg.grouped_tile_rows(32768, 64, 2048, 2048) == 256
+
+
 def route_desc(**kw):
     d = dict(T=100, ld=64, E=64, top=8, groups=1, top_groups=1, score=0, renormalize=1, logits_bf16=0, scale=1.0)
     d.update(kw)
