@@ -58,13 +58,9 @@ int validate_desc(const spg_gemm_desc *d, int epi)
         const int64_t need_w = (d->layout & SPG_LAYOUT_W_KMAJOR) ? d->N : d->K;
         if (d->lda < need_a || d->ldw < need_w) return SPG_EINVAL;
         if (d->scale_layout != SPG_SCALES_ROW_MAJOR) return SPG_EINVAL;   // NVFP4 only
-        if (d->layout != SPG_LAYOUT_NT) {
-            // the transposed copies are read with row stride K; the
-            // transpose runs one 64 x 64 block per workgroup
-            if (d->K > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
-            const int64_t blocks = cdiv(d->K, 64) * (cdiv(d->M, 64) + cdiv(d->N, 64)) * d->batch;
-            if (blocks >= (INT64_C(1) << 31)) return SPG_EUNSUPPORTED;
-        }
+        // the transposed copies' row stride is K, rounded up to 128 for block
+        // scales (transposed_ld), and has the limit of lda and ldw
+        if (d->layout != SPG_LAYOUT_NT && d->K > (INT64_C(1) << 23)) return SPG_EUNSUPPORTED;
     }
     if (d->format == SPG_FMT_E4M3_BLOCK128) {
         // the up rows' scale blocks start where the up rows do
@@ -94,6 +90,13 @@ int validate_desc(const spg_gemm_desc *d, int epi)
     }
     // the epilogue addresses a 32-row block with 32-bit byte offsets
     if (d->ldo >= (INT64_C(1) << 26) || (epi == SPG_EPI_ADD && d->ldr >= (INT64_C(1) << 26)))
+        return SPG_EUNSUPPORTED;
+    // the transpose runs one block of kTransposeEdge squared per workgroup
+    auto blocks = [&](int64_t rows, int64_t stride) {
+        return cdiv(d->K, kTransposeEdge) * cdiv(rows, kTransposeEdge) * (stride ? d->batch : 1);
+    };
+    if (((d->layout & SPG_LAYOUT_A_KMAJOR) && blocks(d->M, d->stride_a) >= kTransposeMaxBlocks) ||
+        ((d->layout & SPG_LAYOUT_W_KMAJOR) && blocks(d->N, d->stride_w) >= kTransposeMaxBlocks))
         return SPG_EUNSUPPORTED;
     return SPG_OK;
 }

@@ -205,7 +205,11 @@ hipError_t launch_gemm_narrow(const GemmArgs &g, hipStream_t s);
 hipError_t launch_splitk_reduce(const GemmArgs &g, int64_t tiles, hipStream_t s);
 // [R, C] codes (row stride ld, batch stride bstride, 16-byte aligned rows)
 // -> [C, R] with row stride ldd (a multiple of 16, at least R), batch entries
-// C * ldd apart.  One launch for at most two of them.
+// C * ldd apart.  At most two of them, in one launch where their blocks of
+// kTransposeEdge squared are fewer than kTransposeMaxBlocks (256 threads each,
+// and a launch has fewer than 2^32), else one launch each; each alone must be
+// below that.
+constexpr int64_t kTransposeEdge = 128, kTransposeMaxBlocks = INT64_C(1) << 24;
 struct TransposeJob {
     const uint8_t *src;
     int64_t R, C, ld, bstride, batch;

@@ -18,7 +18,7 @@ namespace spg {
 
 namespace {
 
-constexpr int kTB = 128;           // block edge (bytes)
+constexpr int kTB = (int)kTransposeEdge;   // block edge (bytes)
 
 // Word (column, group of four rows) in LDS: 32 words a column, the group
 // XOR-ed with 8 ((column / 16) % 4) and neighbouring columns exchanged in the
@@ -112,21 +112,30 @@ hipError_t launch_transpose_u8(const TransposeJob *jobs, int n, hipStream_t s)
     Jobs a = {};
     int64_t blocks = 0;
     int used = 0;
+    auto launch = [&]() -> hipError_t {
+        if (used == 0) return hipSuccess;
+        transpose_u8_kernel<<<dim3((unsigned)blocks), 256, 0, s>>>(a);
+        a = {};
+        blocks = used = 0;
+        return hipGetLastError();
+    };
     for (int i = 0; i < n && i < 2; ++i) {
         const TransposeJob &j = jobs[i];
-        const int64_t nbc = (j.C + kTB - 1) / kTB, nbr = (j.R + kTB - 1) / kTB;
-        if (nbc * nbr * j.batch == 0) continue;
-        if (blocks + nbc * nbr * j.batch >= (INT64_C(1) << 31)) return hipErrorInvalidValue;   // checked by the caller
+        const int64_t nbc = (j.C + kTB - 1) / kTB, nbr = (j.R + kTB - 1) / kTB, mine = nbc * nbr * j.batch;
+        if (mine == 0) continue;
+        if (mine >= kTransposeMaxBlocks) return hipErrorInvalidValue;   // checked by the caller
+        if (blocks + mine >= kTransposeMaxBlocks) {
+            const hipError_t e = launch();
+            if (e != hipSuccess) return e;
+        }
         a.job[used] = j;
         a.nbc[used] = (uint32_t)nbc;
         a.per[used] = (uint32_t)(nbc * nbr);
-        blocks += nbc * nbr * j.batch;
+        blocks += mine;
         if (used == 0) a.first = (uint32_t)blocks;
         ++used;
     }
-    if (used == 0) return hipSuccess;
-    transpose_u8_kernel<<<dim3((unsigned)blocks), 256, 0, s>>>(a);
-    return hipGetLastError();
+    return launch();
 }
 
 }  // namespace spg

@@ -1229,6 +1229,28 @@ def test_gemm_kmajor_operands(spg, shape, fmt, epi, km, B):
             check_close(g, ref["y"], ref["S"], f"kmajor {shape} {fmt} {epi} {km} batch {b}")
 
 
+def test_gemm_kmajor_more_blocks_than_one_launch_takes(spg):
+    # 2^23 entries with both operands K-major: 2^24 transpose blocks of 256
+    # threads would be 2^32 threads, so each operand has a launch of its own
+    nb, n = 2 ** 23, 16
+    gen = torch.Generator("cuda").manual_seed(5)
+    A = torch.randint(0, 0x50, (nb, n, n), dtype=torch.uint8, device="cuda", generator=gen)
+    W = torch.randint(0x80, 0xD0, (nb, n, n), dtype=torch.uint8, device="cuda", generator=gen)
+    sa, sw = torch.rand(nb, device="cuda", generator=gen), torch.rand(nb, device="cuda", generator=gen)
+    got = spg.gemm_scaled(A, sa, W, sw, fmt="e4m3_tensor", a_kmajor=True, w_kmajor=True)
+    A, W = A.transpose(1, 2).contiguous(), W.transpose(1, 2).contiguous()
+    want = spg.gemm_scaled(A, sa, W, sw, fmt="e4m3_tensor")
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    del want
+    for b in (0, 1, nb // 2, nb - 1):
+        a, w = (oracle.E4M3_TABLE[t[b].cpu().numpy()] for t in (A, W))
+        s = float(sa[b]) * float(sw[b])
+        y, S = a @ w.T * s, np.abs(a) @ np.abs(w).T * s
+        ok, _ = oracle.within_tolerance(host_u16(got[b]), y, S)
+        assert ok.all()
+
+
+
 # ---------------------------------------------------------------------------
 # few tokens (M <= 64).  At most 32 tokens with at least 32 blocks of 16
 # output columns: the decode-width kernel (one workgroup per 16 columns, K

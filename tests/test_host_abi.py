@@ -321,6 +321,24 @@ def test_gemm_kmajor_workspace_holds_the_transposed_copies(spg):
     assert spg.lib.gemm_scaled_workspace_bytes(ctypes.byref(d), 0) == 3 * 64 * 128 + 64 * 128
 
 
+@pytest.mark.parametrize("fmt", [0, 1, 3])
+def test_gemm_kmajor_batch_limit(spg, fmt):
+    # the transpose launches one 256-thread workgroup per 128 x 128 block of
+    # an operand, and a launch has fewer than 2^32 threads: 2^24 blocks of one
+    # operand are refused, an operand that all entries share counts once
+    def plan(batch, layout, share_w=False, K=16):
+        d = desc(spg, 16, 16, K, fmt)
+        d.batch, d.layout, d.lda, d.ldw = batch, layout, 16 if layout & 1 else K, 16 if layout & 2 else K
+        d.stride_a, d.stride_w, d.stride_o = 16 * K, 0 if share_w else 16 * K, 256
+        p = spg.Plan()
+        return spg.lib.spg_gemm_plan(ctypes.byref(d), 0, 256, ctypes.byref(p))
+    assert plan(2 ** 23, 3) == 0                          # 2^23 blocks each: a launch for each
+    for layout in (1, 2, 3):
+        assert plan(2 ** 24, layout) == EUNSUP
+        assert plan(2 ** 23, layout, K=144) == EUNSUP     # two blocks an entry
+    assert plan(2 ** 23, 2, share_w=True, K=144) == 0
+
+
 def test_gemm_nvfp4_batch_unsupported(spg):
     d = desc(spg, 64, 64, 64, 2)
     d.batch = 2
