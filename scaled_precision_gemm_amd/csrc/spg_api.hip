@@ -283,6 +283,13 @@ void make_plan_block(const spg_gemm_desc *d, int epi, int units, spg_plan *p)
     p->workgroups = (p->tiles - p->tail_tiles) * p->split_k;
 }
 
+// A block-scaled plan's workgroups (of 256 threads at decode width, else 512)
+// are within what a launch takes, fewer than 2^32 threads.
+bool launchable(const spg_gemm_desc *d, const spg_plan &p)
+{
+    return d->format != SPG_FMT_E4M3_BLOCK128 || p.workgroups < (INT64_C(1) << (p.kernel == 6 ? 24 : 23));
+}
+
 void make_plan(const spg_gemm_desc *d, int epi, int units, spg_plan *p, bool aligned_scales = true)
 {
     memset(p, 0, sizeof(*p));
@@ -480,7 +487,7 @@ SPG_EXPORT int spg_gemm_plan(const spg_gemm_desc *d, int epilogue, int32_t units
     const int v = validate_desc(d, epilogue);
     if (v != SPG_OK) return v;
     make_plan(d, epilogue, units > 0 ? units : 256, plan);
-    return SPG_OK;
+    return launchable(d, *plan) ? SPG_OK : SPG_EUNSUPPORTED;
 }
 
 SPG_EXPORT size_t gemm_scaled_workspace_bytes(const spg_gemm_desc *d, int epilogue)
@@ -626,6 +633,7 @@ SPG_EXPORT int gemm_scaled(void *out, const void *A, const void *sa, const void 
 
     spg_plan p;
     make_plan(d, epilogue, device_units(), &p, aligned4(sa) && aligned4(sw));
+    if (!launchable(d, p)) return SPG_EUNSUPPORTED;
     size_t t_a = 0;
     const size_t t_bytes = transpose_bytes(d, &t_a);
     const size_t need = t_bytes + plan_workspace(&p);

@@ -60,6 +60,18 @@ def test_gemm_refusals():
     assert gemm(d) == EUNSUP                                   # row stride
 
 
+@pytest.mark.parametrize("M,N,most", [(16, 16, 2 ** 24), (33, 16, 2 ** 23), (200, 256, 2 ** 23)])
+def test_more_workgroups_than_a_launch_takes(M, N, most):
+    # 2^32 threads: refused before anything is enqueued (the pointers are not real)
+    for batch, want in ((most - 1, 0), (most, EUNSUP)):
+        d = desc(M, N, 16)
+        d.batch, d.stride_a, d.stride_w, d.stride_o = batch, M * 16, N * 16, M * N
+        plan = spg.Plan()
+        assert spg.lib.spg_gemm_plan(ctypes.byref(d), 0, 256, ctypes.byref(plan)) == want
+    assert plan.workgroups == {16: 2 ** 24, 33: 2 ** 23, 200: 2 ** 23}[M]
+    assert gemm(d) == EUNSUP
+
+
 def test_scales_of_each_entry_flags():
     d = desc(64, 64, 256)
     plan = spg.Plan()
