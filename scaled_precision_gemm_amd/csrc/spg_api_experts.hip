@@ -19,6 +19,7 @@ constexpr int64_t kMaxWords = INT64_C(1) << 29;        // floats within a 31-bit
 constexpr int64_t kMaxIndex = INT64_C(1) << 31;        // rows and (token, place) pairs are int32
 constexpr int64_t kMaxGrid = INT64_C(1) << 23;         // workgroups: at most 512 threads each, 2^32 in all
 constexpr int64_t kMaxGridYZ = 65535;
+constexpr int64_t kMaxTokens = INT64_C(1) << 25;       // routed tokens: 64 threads each at most
 
 // [a0, a1) and [b0, b1) share a byte.
 bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes)
@@ -226,7 +227,7 @@ int validate_route(const spg_route_desc *d)
     if (d->score != SPG_SCORE_SOFTMAX && d->score != SPG_SCORE_SIGMOID) return SPG_EINVAL;
     if (!isfinite(d->scale)) return SPG_EINVAL;
     if (d->E > kRouteMaxExperts || d->top > kRouteMaxTop || d->groups > kRouteMaxGroups) return SPG_EUNSUPPORTED;
-    if (d->T >= kMaxIndex / d->top || cdiv(d->T, 4) >= kMaxGrid || !addressable(d->T, d->ld)) return SPG_EUNSUPPORTED;
+    if (d->T >= kMaxIndex / d->top || d->T >= kMaxTokens || !addressable(d->T, d->ld)) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
 

@@ -171,6 +171,14 @@ def test_route_refusals(kw, call, want):
     assert route(route_desc(**kw), **call) == want
 
 
+@pytest.mark.parametrize("T,want", [(2 ** 25 - 1, EINVAL), (2 ** 25, EUNSUP)])
+def test_route_token_limit(T, want):
+    # fewer than 2^25 tokens are within the limits: what is then wrong is the missing pointer
+    d = route_desc(T=T, top=1)
+    assert route(d, logits=None) == want
+    assert spg.lib.expert_route_backward(FAR, None, FAR, FAKE, ctypes.byref(d), None) == want
+
+
 def test_order_workspace():
     n = spg.lib.expert_order_workspace_bytes
     assert n(2048, 8, 256) == 0 and n(0, 8, 8) == 0 and n(3000, 8, 0) == 0 and n(3000, 8, 1025) == 0 and n(3000, 0, 8) == 0

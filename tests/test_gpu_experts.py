@@ -314,6 +314,25 @@ def test_route_token_counts(spg, T):
         check_route(spg, x, 8, score="sigmoid", bias=np.linspace(-1, 1, 64, dtype=np.float32))
 
 
+def test_route_most_tokens(spg):
+    # the largest token count: choice, order and gradient, against torch on the GPU
+    T, E, top = 2 ** 25 - 1, 4, 2
+    x = torch.randn(T, E, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    r = spg.expert_route(x, top)
+    best = torch.sort(x.float(), dim=1, descending=True, stable=True)
+    assert torch.equal(r.experts, best.indices[:, :top].to(torch.int32))
+    w = torch.softmax(best.values[:, :top].double(), 1).float()
+    assert bool(((r.weights - w).abs() <= 2.0 ** -23 * w).all())     # two fp64 forms rounded to fp32: one step
+    flat = r.experts.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(r.rows, (order // top).to(torch.int32))
+    assert torch.equal(r.slots.reshape(-1)[order], torch.arange(T * top, dtype=torch.int32, device="cuda"))
+    assert torch.equal(r.offsets[1:].long(), torch.bincount(flat.long(), minlength=E).cumsum(0))
+    g = spg.expert_route_backward(torch.ones_like(r.weights), x, r.experts)
+    # equal weights' gradients: the shares' derivatives cancel up to fp32 rounding
+    assert g.shape == (T, E) and bool((g.float().abs() <= 2.0 ** -21).all())
+
+
 @pytest.mark.parametrize("E,groups,top_groups,top", [(256, 8, 4, 8), (160, 8, 3, 6), (60, 4, 1, 4), (64, 64, 9, 9),
                                                      (512, 16, 5, 20), (96, 3, 3, 8), (8, 2, 1, 4)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
