@@ -595,6 +595,7 @@ def gemm_scaled(A, sa, W, sw, epilogue="store", residual=None, fmt="e4m3_row",
         d.bias_scale = bias_scale.data_ptr()
     if out is None and out_shape is not None:
         out = torch.empty(out_shape, dtype=torch.bfloat16, device=A.device)
+    _need(workspace is None or workspace.device == A.device, f"the workspace must be on {A.device}")
     if nws > 0:
         if workspace is None or workspace.numel() < nws:
             workspace = torch.empty((nws,), dtype=torch.uint8, device=A.device)

@@ -354,6 +354,17 @@ def test_captured_step_replays_like_eager(spg, M, N, K, epi):
         assert np.array_equal(host(out), want), f"replay {r}"
 
 
+def test_workspace_of_another_device_is_refused(spg):
+    M, N, K = 96, 512, 8208                  # split along K: partial tiles in the workspace
+    ops = operands(spg, M, N, K, 5)
+    ws = spg.gemm_workspace(ops[0], ops[2], "e4m3_block128")
+    for fmt, o in (("e4m3_block128", ops), ("e4m3_row", (ops[0], ops[1][0].contiguous(), ops[2], torch.ones(N, device="cuda")))):
+        with pytest.raises(ValueError, match="workspace"):
+            spg.gemm_scaled(*o, fmt=fmt, workspace=torch.empty(ws.numel(), dtype=torch.uint8))
+        with pytest.raises(ValueError, match="workspace"):
+            spg.gemm_scaled(*o, fmt=fmt, workspace=torch.empty(16, dtype=torch.uint8))
+
+
 def test_two_streams_at_once(spg):
     ops = [operands(spg, *s, 400 + i) for i, s in enumerate([(96, 512, 8208), (16, 4096, 2048), (600, 768, 400)])]
     want = [host(spg.gemm_scaled(*o, fmt="e4m3_block128")) for o in ops]
