@@ -206,6 +206,22 @@ def test_grouped_one_weight_and_scales_of_each_expert(spg, counts, bm, epi):
         check(out[lo:hi], y, S, f"expert {e}")
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 5], [70, 0, 150, 33]])
+def test_grouped_input_gradient(spg, counts):
+    # dX of an expert's product: the same call with the codes and the scale
+    # blocks of its weight transposed
+    E, R, N, K = len(counts), sum(counts), 384, 272
+    qw, sw = spg.quantize_block128(dev(bf16_normal((E, N, K), 0.02, 2)), "block")
+    qy, sy = spg.quantize_block128(dev(bf16_normal((R, N), 0.01, 1)), "row")
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    dx = spg.gemm_grouped(qy, sy, qw.transpose(1, 2).contiguous(), sw.transpose(1, 2).contiguous(), i32(offsets))
+    y = row_values(qy, sy)
+    for e in range(E):
+        w, g = block_values(qw[e], sw[e]), y[offsets[e]:offsets[e + 1]]
+        if len(g):
+            check(dx[offsets[e]:offsets[e + 1]], g @ w, np.abs(g) @ np.abs(w), f"expert {e}")
+
+
 # ---- routing -----------------------------------------------------------------------
 
 def route_ref(x, top, score="softmax", bias=None, groups=1, top_groups=1, renorm=True, scale=1.0):
