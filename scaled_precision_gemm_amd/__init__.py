@@ -786,7 +786,9 @@ def expert_route(logits, top, score="softmax", bias=None, groups=1, top_groups=1
     best stay; experts are the `top` largest c among them, ties to the lowest
     index; weights are scale p / sum p (renormalize) or scale p.  Logits of
     -inf mask an expert: places that no expert is left for hold expert -1,
-    weight 0, slot -1."""
+    weight 0, slot -1.  With the row order, experts, offsets, rows and slots
+    are views of one allocation, which lives as long as any of them does (keep
+    experts.clone() for a backward pass to free the others)."""
     def check():
         d = _route_desc(logits, top, score, groups, top_groups, renormalize, scale)
         _need(bias is None or (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32

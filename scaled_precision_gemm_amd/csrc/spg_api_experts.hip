@@ -96,7 +96,7 @@ int64_t grouped_columns(const spg_grouped_desc *d, int epi, int bm)
 
 // Tile rows from the mean rows of an expert.  Tiles of 16 rows stream the
 // weights with many small workgroups (decode): up to 4 rows, or up to 8 where
-// 128-row tiles would leave compute units idle.  256-row tiles read a weight
+// 128-row tiles would leave compute units idle (of the 256 of an MI355X).  256-row tiles read a weight
 // panel half as often (and run an expert's last rows as a 128-row tile): above
 // 96 rows, where they still give every compute unit one.  Measured (us, cold
 // weights; 16-, 128-, 256-row tiles): 64 experts of 2048 x 2048 with 2 rows 43,

@@ -21,11 +21,13 @@
 //    stage (see the schedule below).
 //  * What bounds it: the matrix core at the clock that the card's power
 //    allows.  4096 x 34816 x 5120 SWIGLU: 590 us in a burst, 617 - 656
-//    us (2.3 PFLOP/s) sustained; the row-scaled kernel 552.  MFMAs are busy 55 % of the
-//    cycles (row-scaled 64 %): the four multiply-adds of a partial product
-//    take the issue slots of 7 % of a 16 x 16 x 128 MFMA's 32 cycles, a tile's
-//    fill and epilogue 6.8 us beside 1.57 us a stage.  4096 x 5120 x 6144 ADD
-//    129 us, 8192^3 417 - 428 us (2.6 PFLOP/s).
+//    us (2.3 PFLOP/s) sustained; the row-scaled kernel 552.  MFMAs are busy 55 -
+//    58 % of the cycles (row-scaled 64 %) and the vector unit, whose four
+//    multiply-adds of a partial product take half of a 16 x 16 x 128 MFMA's
+//    cycles, 50 %; a tile's fill and epilogue take 6.8 us beside 1.57 us a
+//    stage.  4096 x 5120 x 6144 ADD 129 us, 8192^3 417 - 428 us (2.6 PFLOP/s).
+//    128-row tiles take 0.92 us a stage, half the work, with MFMAs busy 36 % and
+//    the vector unit 32 % (1111 x 7168 x 5120): neither is what they wait for.
 //  * Experts' products: a workgroup finds its (expert, rows) tile from the
 //    offsets in device memory, and gathers A rows by index with per-lane copy
 //    addresses; the grid is the largest that the row count allows, and
