@@ -359,6 +359,49 @@ def test_route_groups(spg, E, groups, top_groups, top, score, T):
         check_route(spg, logits(T, E, groups), top, score=score, groups=groups, top_groups=top_groups, bias=b, scale=2.5)
 
 
+@pytest.mark.parametrize("E,groups,top_groups,top", [(256, 64, 20, 8), (1024, 64, 9, 32), (1000, 8, 3, 10)])
+@pytest.mark.parametrize("T", [5, 4200])
+def test_route_groups_of_many_experts(spg, E, groups, top_groups, top, T):
+    # the most scores and choices that a workgroup holds in LDS (82 and 70 KiB)
+    check_route(spg, logits(T, E, groups), top, score="sigmoid", groups=groups, top_groups=top_groups, scale=2.5)
+
+
+def test_route_and_sort_captured_with_chunk_counts(spg):
+    # more entries than one launch counts: the counts of chunks in a workspace,
+    # the call's own or one that two graphs share, replayed one after the other
+    T, E, top = 5000, 64, 8
+    x = torch.from_numpy(logits(T, E, 1)).cuda()
+    ws = spg.expert_workspace(T, top, E)
+
+    def step(w):
+        r = spg.expert_route(x, top, score="sigmoid", workspace=w)
+        return (*r, *spg.expert_sort(r.experts, E, workspace=w))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ws)
+        step(None)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for w in (ws, ws, None):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step(w)
+        graphs.append((graph, got))
+    for k in range(3):
+        x.copy_(torch.from_numpy(logits(T, E, 50 + k)).cuda())
+        want = [t.clone() for t in step(None)]
+        torch.cuda.synchronize()
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, got in graphs:
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {k}"
+        check_order(want[1].cpu().numpy(), E, *want[2:5])
+
+
 @pytest.mark.parametrize("T", [10, 200, 4200])
 def test_route_ties_go_to_the_lowest_index(spg, T):
     x = np.random.default_rng(5).integers(-1, 2, (T, 96)).astype(np.float32)
