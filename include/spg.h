@@ -517,6 +517,86 @@ int expert_combine_backward(const void *grad_out, int64_t ldg, const void *y, in
                             void *grad_y, int64_t ldgy, float *grad_weights, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* The norm before the products                                              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * rms_norm - the RMS norm of a residual stream, leaving as the operand of the
+ * product that follows:
+ *     h    = bf16(x + residual)              (x without a residual)
+ *     rstd = 1 / sqrt(mean(h^2) + eps)       over the H elements of a row
+ *     y    = h rstd (weight + weight_offset)
+ *   output SPG_NORM_BF16          : normed = bf16(y)
+ *          SPG_NORM_E4M3_ROW      : s = fl32(max |y| / 448) per row, q = E4M3 of
+ *                                   y / s: A of SPG_FMT_E4M3_ROW; scale [R]
+ *          SPG_NORM_E4M3_BLOCK128 : the same per 128 elements of a row: A of
+ *                                   SPG_FMT_E4M3_BLOCK128; scale [ceil(H /
+ *                                   128), R], group-major
+ * y is fp32 and is rounded once, to the output's type (the codes are not those
+ * of the rounded bf16 y); the squares are summed in 64 bits.  A row that
+ * holds a NaN or an infinity, or whose y overflows fp32, gets a scale (of its
+ * row, or of every group that such a y is in) that is NaN or infinite.  Codes
+ * of an all-zero row or group are signed zeros with scale 0.
+ *   x, residual : bf16 [R, H], row strides ldx, ldr; residual or NULL
+ *   weight   : [H], bf16 or (weight_fp32) fp32, contiguous
+ *   h        : bf16 [R, H], row stride ldh: with a residual required, without
+ *              one NULL (x is what is normed)
+ *   normed   : bf16 [R, H], row stride ldn: required for SPG_NORM_BF16, beside
+ *              codes bf16(y) as well, or NULL
+ *   q, scale : codes [R, H], row stride ldq, 16-byte aligned rows, H % 16 == 0;
+ *              NULL for SPG_NORM_BF16
+ *   rstd     : fp32 [R] for the gradients, or NULL
+ * bf16 rows need no alignment.  1 <= H <= 32768; R below 2^26 up to H = 2048,
+ * 2^24 up to 8192, 2^22 beyond (else SPG_EUNSUPPORTED); R == 0 is a no-op; eps
+ * >= 0 and weight_offset are finite.  h and normed may each be x or residual
+ * itself (the same pointer and row stride); any other overlap of an output
+ * with another or with an input is SPG_EINVAL.  One launch, no workspace.
+ */
+enum {
+    SPG_NORM_BF16 = 0,
+    SPG_NORM_E4M3_ROW = 1,
+    SPG_NORM_E4M3_BLOCK128 = 2
+};
+typedef struct spg_norm_desc {
+    int64_t R, H;
+    int64_t ldx, ldr, ldh, ldn, ldq;
+    double eps;
+    float weight_offset;
+    int32_t weight_fp32, output, reserved;
+} spg_norm_desc;
+
+int rms_norm(const void *x, const void *residual, const void *weight, void *h, void *normed, uint8_t *q, float *scale,
+             float *rstd, const spg_norm_desc *d, void *stream);
+
+/*
+ * rms_norm_backward - the gradients of y (quantization is passed straight
+ * through): with g = grad_out (weight + weight_offset), n = h rstd,
+ *     grad_x = rstd (g - n mean(g n)) + grad_residual     one rounding to bf16
+ *     grad_weight = sum over the rows of grad_out n       fp32
+ * grad_x is the gradient of x and of the residual alike.
+ *   grad_out, h, grad_residual : bf16 [R, H], row strides ldg, ldh, ldr; h and
+ *              rstd as rms_norm left them (h = x without a residual);
+ *              grad_residual, the gradient that reaches h past the norm, or NULL
+ *   grad_x   : bf16 [R, H], row stride ldx; it may be one of the three itself
+ *   grad_weight : fp32 [H], written whole (zeros for R == 0), or NULL
+ *   ws       : device workspace of at least rms_norm_backward_workspace_bytes(R,
+ *              H) with grad_weight (any contents; 4-byte aligned)
+ * Limits as rms_norm; other overlaps are SPG_EINVAL.  Sums in fp32, in an order
+ * that R and H alone decide: the same call gives the same bits.
+ */
+typedef struct spg_norm_grad_desc {
+    int64_t R, H;
+    int64_t ldg, ldh, ldr, ldx;
+    float weight_offset;
+    int32_t weight_fp32;
+} spg_norm_grad_desc;
+
+size_t rms_norm_backward_workspace_bytes(int64_t R, int64_t H);
+int rms_norm_backward(const void *grad_out, const void *h, const void *grad_residual, const void *weight,
+                      const float *rstd, void *grad_x, float *grad_weight, const spg_norm_grad_desc *d, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Tile / route selection (host only, no device access)                     */
 /* ------------------------------------------------------------------------ */
 

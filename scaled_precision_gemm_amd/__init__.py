@@ -20,6 +20,7 @@ __all__ = [
     "quantize_rowwise", "quantize_tensor", "quantize_block16", "quantize_block128", "gemm_scaled", "gemm_grouped",
     "expert_route", "expert_sort", "expert_route_backward", "expert_combine", "expert_combine_backward",
     "ExpertRoute", "expert_workspace", "grouped_tile_rows", "block128_scale_shape",
+    "rms_norm", "rms_norm_backward", "RmsNorm", "norm_workspace",
     "gemm_plan", "gemm_workspace", "route_select", "route_cost", "probe_mfma", "probe_read", "probe_fp4_rounding",
     "lib", "LIB_PATH",
     "FMT_E4M3_ROW", "FMT_E4M3_TENSOR", "FMT_NVFP4", "FMT_E4M3_BLOCK128", "EPI_STORE", "EPI_ADD", "EPI_SWIGLU",
@@ -38,6 +39,7 @@ _FMT = {"e4m3_row": FMT_E4M3_ROW, "e4m3_tensor": FMT_E4M3_TENSOR, "nvfp4": FMT_N
         "e4m3_block128": FMT_E4M3_BLOCK128}
 _TILING = {"row": 0, "column": 1, "block": 2}
 _SCORE = {"softmax": 0, "sigmoid": 1}
+_NORM = {"bf16": 0, "e4m3_row": 1, "e4m3_block128": 2}
 
 
 class SpgError(RuntimeError):
@@ -103,6 +105,23 @@ class RouteDesc(ctypes.Structure):
     ]
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int64), ("H", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+        ("ldh", ctypes.c_int64), ("ldn", ctypes.c_int64), ("ldq", ctypes.c_int64), ("eps", ctypes.c_double),
+        ("weight_offset", ctypes.c_float), ("weight_fp32", ctypes.c_int32), ("output", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class NormGradDesc(ctypes.Structure):
+    _fields_ = [
+        ("R", ctypes.c_int64), ("H", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldh", ctypes.c_int64),
+        ("ldr", ctypes.c_int64), ("ldx", ctypes.c_int64), ("weight_offset", ctypes.c_float),
+        ("weight_fp32", ctypes.c_int32),
+    ]
+
+
 # Exported symbols and their signatures (mirrors include/spg.h).
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 SIGNATURES = {
@@ -115,6 +134,9 @@ SIGNATURES = {
     "expert_route_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P]),
     "expert_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _I64, _P]),
     "expert_combine_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _P]),
+    "rms_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormDesc), _P]),
+    "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "rms_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormGradDesc), _P, _SZ, _P]),
     "spg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "quantize_rowwise": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _P]),
     "quantize_tensor_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -921,6 +943,144 @@ def expert_combine_backward(grad_out, y, weights, slots, grad_y=None):
     _run(lib.expert_combine_backward, "expert_combine_backward", y, grad_out.data_ptr(), ldg, y.data_ptr(), R, ldy,
          weights.data_ptr(), slots.data_ptr(), T, top, H, grad_y.data_ptr(), ldgy, grad_weights.data_ptr())
     return grad_y, grad_weights
+
+
+# ---------------------------------------------------------------------------
+# The norm before the products
+# ---------------------------------------------------------------------------
+
+RmsNorm = collections.namedtuple("RmsNorm", "out scale normed h rstd")
+
+
+def _like(name, t, shape, dt, dev):
+    """An optional output: 2-D rows of dtype dt and shape `shape` on dev."""
+    if t is not None:
+        _rows_ok(name, t, dt, dev)
+        _need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
+
+
+def _norm_weight(weight, H, dev):
+    _need(isinstance(weight, torch.Tensor) and weight.dtype in (torch.bfloat16, torch.float32) and weight.device == dev
+          and tuple(weight.shape) == (H,) and weight.is_contiguous(),
+          f"weight must be a contiguous bf16 or fp32 [{H}] tensor on {dev}")
+
+
+def rms_norm(x, weight, residual=None, output="bf16", eps=1e-6, weight_offset=0.0, normed=False, rstd=False, out=None,
+             scale=None, h=None):
+    """RMS norm of x (bf16 [R, H]), the residual (bf16 [R, H]) added first:
+    h = bf16(x + residual), y = h / sqrt(mean(h^2) + eps) * (weight +
+    weight_offset), weight bf16 or fp32 [H]; as RmsNorm(out, scale, normed, h,
+    rstd).
+
+    output "bf16": out = bf16(y), scale None.  "e4m3_row": out the E4M3 codes
+    of y (uint8 [R, H]) and scale fp32 [R], "e4m3_block128": scale fp32
+    [ceil(H/128), R], one per 128 elements of a row: the activations of
+    gemm_scaled and gemm_grouped in these formats (y is rounded once, to the
+    codes); H % 16 == 0.  normed (True, or a bf16 [R, H] tensor to write to)
+    asks for bf16(y) beside the codes.  h is the new residual stream, None
+    without a residual; it may be written over x or the residual (h=x,
+    h=residual), and so may a bf16 out or normed.  rstd=True keeps fp32 [R]
+    1 / sqrt(..) for rms_norm_backward."""
+    def check():
+        _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D bf16 tensor")
+        dev = x.device
+        R, H = x.shape
+        _rows_ok("x", x, torch.bfloat16, dev)
+        _need(isinstance(output, str) and output in _NORM, f"unknown output {output}")
+        _need(isinstance(eps, (int, float)) and math.isfinite(eps) and eps >= 0, "eps must be a finite number, not below 0")
+        _need(isinstance(weight_offset, (int, float)) and math.isfinite(weight_offset), "weight_offset must be a finite number")
+        _need(H >= 1, "rows must hold at least one element")
+        _norm_weight(weight, H, dev)
+        coded = output != "bf16"
+        _need(not coded or H % 16 == 0, "rows of codes must be a multiple of 16 elements")
+        _need(coded or normed is False, "a bf16 output is normed itself")
+        _need(coded or scale is None, "a bf16 output has no scale")
+        if residual is not None:
+            _like("residual", residual, (R, H), torch.bfloat16, dev)
+        _need(h is None or residual is not None, "h is an output of the residual's addition")
+        _like("h", h, (R, H), torch.bfloat16, dev)
+        if isinstance(normed, torch.Tensor):
+            _like("normed", normed, (R, H), torch.bfloat16, dev)
+        _like("out", out, (R, H), torch.uint8 if coded else torch.bfloat16, dev)
+        _need(not coded or out is None or _ld(out) % 16 == 0 and out.data_ptr() % 16 == 0,
+              "rows of codes must be 16-byte aligned")
+        want = (R,) if output == "e4m3_row" else ((H + 127) // 128, R)
+        _need(scale is None or isinstance(scale, torch.Tensor) and scale.dtype == torch.float32 and scale.device == dev
+              and tuple(scale.shape) == want and scale.is_contiguous(),
+              f"scale must be a contiguous fp32 {want} tensor on {dev}")
+        _need(x.is_cuda, "x must be a CUDA tensor")
+        n = out if not coded else normed if isinstance(normed, torch.Tensor) else None
+        d = NormDesc(R, H, _ld(x), H if residual is None else _ld(residual), H if h is None else _ld(h),
+                     H if n is None else _ld(n), H if not coded or out is None else _ld(out), eps, weight_offset,
+                     int(weight.dtype == torch.float32), _NORM[output], 0)
+        return d, coded, want
+
+    given = isinstance(normed, torch.Tensor)
+    d, coded, want = _checked(("norm", _sig(x), _sig(weight), _sig(residual), output, eps, weight_offset,
+                               _sig(normed) if given else bool(normed), _sig(out), _sig(scale), _sig(h)), check)
+    if h is None and residual is not None:
+        h = x.new_empty(x.shape)
+    if coded:
+        if out is None:
+            out = x.new_empty(x.shape, dtype=torch.uint8)
+        if scale is None:
+            scale = x.new_empty(want, dtype=torch.float32)
+        n = normed if given else x.new_empty(x.shape) if normed else None
+    else:
+        n = out = x.new_empty(x.shape) if out is None else out
+    r = x.new_empty((d.R,), dtype=torch.float32) if rstd else None
+    if d.R > 0:
+        _run(lib.rms_norm, "rms_norm", x, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(h), _ptr(n),
+             out.data_ptr() if coded else None, _ptr(scale), _ptr(r), ctypes.byref(d))
+    return RmsNorm(out, scale, n, h, r)
+
+
+def norm_workspace(R: int, H: int, device="cuda"):
+    """A device workspace for rms_norm_backward on [R, H], or None when it
+    needs none."""
+    n = lib.rms_norm_backward_workspace_bytes(R, H)
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offset=0.0, grad_x=None, grad_weight=True,
+                      workspace=None):
+    """(grad_x bf16 [R, H], grad_weight fp32 [H]) of rms_norm's y from grad_out
+    bf16 [R, H] (quantization passes gradients straight through), with the h
+    and rstd that it left (h: x itself where there was no residual).  grad_x is
+    the gradient of x and of the residual alike; grad_residual, the gradient
+    that reaches h past the norm, is added to it.  grad_x may be written over
+    grad_out, h or grad_residual.  grad_weight=False leaves the weight's
+    gradient out (None)."""
+    def check():
+        _need(isinstance(grad_out, torch.Tensor) and grad_out.dim() == 2, "grad_out must be a 2-D bf16 tensor")
+        dev = grad_out.device
+        R, H = grad_out.shape
+        _rows_ok("grad_out", grad_out, torch.bfloat16, dev)
+        _need(H >= 1, "rows must hold at least one element")
+        _need(isinstance(h, torch.Tensor), "h must be a tensor")
+        _like("h", h, (R, H), torch.bfloat16, dev)
+        _like("grad_residual", grad_residual, (R, H), torch.bfloat16, dev)
+        _like("grad_x", grad_x, (R, H), torch.bfloat16, dev)
+        _norm_weight(weight, H, dev)
+        _need(isinstance(rstd, torch.Tensor) and rstd.dtype == torch.float32 and rstd.device == dev
+              and tuple(rstd.shape) == (R,) and rstd.is_contiguous(), f"rstd must be a contiguous fp32 [{R}] tensor on {dev}")
+        _need(isinstance(weight_offset, (int, float)) and math.isfinite(weight_offset), "weight_offset must be a finite number")
+        _need(isinstance(grad_weight, bool), "grad_weight must be True or False")
+        _need(grad_out.is_cuda, "grad_out must be a CUDA tensor")
+        d = NormGradDesc(R, H, _ld(grad_out), _ld(h), H if grad_residual is None else _ld(grad_residual),
+                         H if grad_x is None else _ld(grad_x), weight_offset, int(weight.dtype == torch.float32))
+        return d, lib.rms_norm_backward_workspace_bytes(R, H) if grad_weight else 0
+
+    d, nws = _checked(("norm backward", _sig(grad_out), _sig(h), _sig(weight), _sig(rstd), _sig(grad_residual),
+                       weight_offset, _sig(grad_x), grad_weight), check)
+    if grad_x is None:
+        grad_x = grad_out.new_empty(grad_out.shape)
+    ws = _order_ws(workspace, nws, grad_out)
+    gw = grad_out.new_empty((d.H,), dtype=torch.float32) if grad_weight else None
+    if d.R > 0 or grad_weight:
+        _run(lib.rms_norm_backward, "rms_norm_backward", grad_out, grad_out.data_ptr(), h.data_ptr(), _ptr(grad_residual),
+             weight.data_ptr(), rstd.data_ptr(), grad_x.data_ptr(), _ptr(gw), ctypes.byref(d), _ptr(ws), nws)
+    return grad_x, gw
 
 
 def route_cost(bm, bn, per_unit, factor, M, N, batch, units) -> float:

@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "spg_api_checks.h"
 #include "spg_experts.h"
 #include "spg_gemm_block.h"
 
@@ -10,42 +11,11 @@ using namespace spg;
 
 namespace {
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
-bool aligned2(const void *p) { return ((uintptr_t)p & 1u) == 0; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 constexpr int64_t kMaxWords = INT64_C(1) << 29;        // floats within a 31-bit byte range
 constexpr int64_t kMaxIndex = INT64_C(1) << 31;        // rows and (token, place) pairs are int32
 constexpr int64_t kMaxGrid = INT64_C(1) << 23;         // workgroups: at most 512 threads each, 2^32 in all
 constexpr int64_t kMaxGridYZ = 65535;
 constexpr int64_t kMaxTokens = INT64_C(1) << 25;       // routed tokens: 64 threads each at most
-
-// [a0, a1) and [b0, b1) share a byte.
-bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes)
-{
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return abytes > 0 && bbytes > 0 && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
-}
-int64_t extent(int64_t rows, int64_t ld, int64_t cols) { return rows > 0 ? (rows - 1) * ld + cols : 0; }
-// Byte extents of n pieces `stride` apart stay far inside 64 bits.
-bool addressable(int64_t n, int64_t stride) { return n <= 1 || stride < (INT64_C(1) << 56) / n; }
-
-struct Range {
-    const void *p;
-    int64_t bytes;
-};
-// An output (outs[0 .. n)) shares a byte with another or with an input.
-bool any_overlap(const Range *outs, int n, const Range *ins, int m)
-{
-    for (int i = 0; i < n; ++i) {
-        for (int j = i + 1; j < n; ++j)
-            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
-        for (int j = 0; j < m; ++j)
-            if (overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
-    }
-    return false;
-}
 
 }  // namespace
 
