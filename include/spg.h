@@ -420,6 +420,43 @@ int gemm_grouped(void *out, const void *A, const float *sa, const void *W, const
 int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
 
 /*
+ * gemm_grouped_dw - the weight gradients of the experts' products, from bf16
+ * operands: over the rows r in [offsets[e], offsets[e + 1]) of expert e
+ *     out[e] = add[e] + sum_r dY[r]^T X[row_index[r]]        (X[r] without row_index)
+ * fp32 sums, one rounding to the output's type.  An expert without rows gets
+ * add[e], or zeros.  One expert with all rows is a dense layer's gradient.
+ *   rows      : rows of dY (and of row_index); rows outside every expert's range
+ *               are not read
+ *   x_rows    : rows of X; without row_index at least `rows`
+ *   dY, X     : bf16 [rows, N], [x_rows, K], row strides ldy, ldx (elements,
+ *               multiples of 8, at most 2^24), 16-byte aligned; with row_index X
+ *               spans less than 2^30 elements (else SPG_EUNSUPPORTED)
+ *   offsets, row_index : as gemm_grouped takes them, clamped in the same way; an
+ *               index outside [0, x_rows) stands for a row of zeros.  Where
+ *               ranges overlap, a row counts for every expert it is in
+ *   out, add  : [experts, N, K], bf16 or (out_fp32) fp32, row strides ldo, lda and
+ *               expert strides stride_o, stride_a (elements, multiples of 16
+ *               bytes), 16-byte aligned; add or NULL.  add may be the output itself (the
+ *               same strides); any other overlap is SPG_EINVAL
+ *   ws        : device workspace of at least gemm_grouped_dw_workspace_bytes(d)
+ *               (any contents; 16-byte aligned): partial sums where the tiles
+ *               are few, each expert's rows being cut into parts
+ * N % 8 == 0, K % 8 == 0, 1 <= experts <= 65536.  The order of the sums depends
+ * on the sizes and offsets alone: the same call gives the same bits.  Each
+ * element within 2^-8 |y| (bf16; 2^-24 fp32) + 2^-12 S of the exact value y, S
+ * the sum of |products|, and |add|.
+ */
+typedef struct spg_grouped_dw_desc {
+    int64_t rows, x_rows, N, K;
+    int64_t ldy, ldx, ldo, stride_o, lda, stride_a;
+    int32_t experts, out_fp32;
+} spg_grouped_dw_desc;
+
+size_t gemm_grouped_dw_workspace_bytes(const spg_grouped_dw_desc *d);
+int gemm_grouped_dw(void *out, const void *dY, const void *X, const int32_t *offsets, const int32_t *row_index,
+                    const void *add, const spg_grouped_dw_desc *d, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * expert_route - the experts of each token, their weights, and the row order
  * of the experts' products.  For a token with logits l:
  *   p = softmax(l) or 1 / (1 + exp(-l)); c = p + bias

@@ -20,7 +20,7 @@ __all__ = [
     "quantize_rowwise", "quantize_tensor", "quantize_block16", "quantize_block128", "gemm_scaled", "gemm_grouped",
     "expert_route", "expert_sort", "expert_route_backward", "expert_combine", "expert_combine_backward",
     "ExpertRoute", "expert_workspace", "grouped_tile_rows", "block128_scale_shape",
-    "rms_norm", "rms_norm_backward", "RmsNorm", "norm_workspace",
+    "gemm_grouped_dw", "grouped_dw_workspace", "rms_norm", "rms_norm_backward", "RmsNorm", "norm_workspace",
     "gemm_plan", "gemm_workspace", "route_select", "route_cost", "probe_mfma", "probe_read", "probe_fp4_rounding",
     "lib", "LIB_PATH",
     "FMT_E4M3_ROW", "FMT_E4M3_TENSOR", "FMT_NVFP4", "FMT_E4M3_BLOCK128", "EPI_STORE", "EPI_ADD", "EPI_SWIGLU",
@@ -105,6 +105,14 @@ class RouteDesc(ctypes.Structure):
     ]
 
 
+class GroupedDwDesc(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("x_rows", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ldy", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64), ("stride_o", ctypes.c_int64),
+        ("lda", ctypes.c_int64), ("stride_a", ctypes.c_int64), ("experts", ctypes.c_int32), ("out_fp32", ctypes.c_int32),
+    ]
+
+
 class NormDesc(ctypes.Structure):
     _fields_ = [
         ("R", ctypes.c_int64), ("H", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
@@ -134,6 +142,8 @@ SIGNATURES = {
     "expert_route_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.POINTER(RouteDesc), _P]),
     "expert_combine": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _I64, _P]),
     "expert_combine_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _P]),
+    "gemm_grouped_dw_workspace_bytes": (_SZ, [ctypes.POINTER(GroupedDwDesc)]),
+    "gemm_grouped_dw": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(GroupedDwDesc), _P, _SZ, _P]),
     "rms_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormDesc), _P]),
     "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
     "rms_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormGradDesc), _P, _SZ, _P]),
@@ -754,6 +764,73 @@ def gemm_grouped(A, sa, W, sw, offsets, epilogue="store", rows=None, out=None):
         _run(lib.gemm_grouped, "gemm_grouped", A, out.data_ptr(), A.data_ptr(), sa.data_ptr(), W.data_ptr(),
              sw.data_ptr(), offsets.data_ptr(), _ptr(rows), epi, ctypes.byref(d))
     return out
+
+
+def _grouped_dw(dY, X, offsets, rows, add, out, dtype):
+    _need(isinstance(dY, torch.Tensor) and isinstance(X, torch.Tensor), "dY and X must be tensors")
+    dev = dY.device
+    _rows_ok("dY", dY, torch.bfloat16, dev)
+    _rows_ok("X", X, torch.bfloat16, dev)
+    (R, N), (x_rows, K) = dY.shape, X.shape
+    _need(N % 8 == 0 and K % 8 == 0, "columns of dY and X must be multiples of 8")
+    for name, t in (("dY", dY), ("X", X)):
+        _need(_ld(t) % 8 == 0 and t.data_ptr() % 16 == 0, f"rows of {name} must be 16-byte aligned")
+    _need(isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.shape[0] >= 2,
+          "offsets must be int32 [experts + 1]")
+    E = offsets.shape[0] - 1
+    _index("offsets", offsets, (E + 1,), dev)
+    if rows is None:
+        _need(x_rows >= R, "X has fewer rows than dY")
+    else:
+        _index("rows", rows, (R,), dev)
+    _need(dtype in (torch.bfloat16, torch.float32), "dtype must be torch.bfloat16 or torch.float32")
+    strides = []
+    for name, t in (("out", out), ("add", add)):
+        if t is None:
+            strides.append((K, N * K))
+            continue
+        _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == dev and tuple(t.shape) == (E, N, K),
+              f"{name} must be a {dtype} {(E, N, K)} tensor on {dev}")
+        ld, st, unit = t.stride(1) if N > 1 else K, t.stride(0) if E > 1 else 0, 16 // t.element_size()
+        _need(t.numel() == 0 or (t.stride(2) == 1 or K == 1) and ld >= K and ld % unit == 0 and st % unit == 0
+              and t.data_ptr() % 16 == 0 and (E == 1 or st >= (N - 1) * ld + K),
+              f"rows of {name} must be contiguous, 16-byte aligned and must not overlap")
+        strides.append((ld, st))
+    d = GroupedDwDesc(R, x_rows, N, K, _ld(dY), _ld(X), *strides[0], *strides[1], E, int(dtype == torch.float32))
+    _need(dY.is_cuda, "operands must be CUDA tensors")
+    return d, lib.gemm_grouped_dw_workspace_bytes(ctypes.byref(d))
+
+
+def gemm_grouped_dw(dY, X, offsets, rows=None, add=None, out=None, dtype=torch.bfloat16, workspace=None):
+    """The weight gradients of gemm_grouped's products, from bf16 operands:
+    out[e] = add[e] + sum over r in [offsets[e], offsets[e + 1]) of dY[r]^T
+    X[rows[r]] (X[r] without rows), [experts, N, K] in `dtype` (bf16 or fp32);
+    fp32 sums, one rounding.
+
+    dY bf16 [R, N] in expert order; X bf16 [T, K]; offsets int32 [experts + 1]
+    and rows int32 [R] as expert_route returns them (an index outside X stands
+    for a row of zeros); N and K multiples of 8.  add [experts, N, K] in
+    `dtype`, which may be `out` itself (gradients of several chunks).  An
+    expert without rows gets add, or zeros.  offsets [0, R] makes it a dense
+    layer's weight gradient.  workspace: grouped_dw_workspace(...), else
+    allocated where the call needs one."""
+    d, nws = _checked(("grouped dw", _sig(dY), _sig(X), _sig(offsets), _sig(rows), _sig(add), _sig(out), dtype),
+                      lambda: _grouped_dw(dY, X, offsets, rows, add, out, dtype))
+    if out is None:
+        out = dY.new_empty((d.experts, d.N, d.K), dtype=dtype)
+    if d.N > 0 and d.K > 0:
+        ws = _order_ws(workspace, nws, dY)
+        _run(lib.gemm_grouped_dw, "gemm_grouped_dw", dY, out.data_ptr(), dY.data_ptr(), X.data_ptr(), offsets.data_ptr(),
+             _ptr(rows), _ptr(add), ctypes.byref(d), _ptr(ws), nws)
+    return out
+
+
+def grouped_dw_workspace(rows: int, experts: int, N: int, K: int, device="cuda"):
+    """A device workspace for gemm_grouped_dw of `rows` rows, or None when it
+    needs none."""
+    d = GroupedDwDesc(rows, rows, N, K, N, K, K, N * K, K, N * K, experts, 1)
+    n = lib.gemm_grouped_dw_workspace_bytes(ctypes.byref(d))
+    return torch.empty((n,), dtype=torch.uint8, device=device) if n > 0 else None
 
 
 def grouped_tile_rows(rows: int, experts: int, N: int, K: int, epilogue="store") -> int:

@@ -6,6 +6,7 @@
 #include "spg_api_checks.h"
 #include "spg_experts.h"
 #include "spg_gemm_block.h"
+#include "spg_grouped_dw.h"
 
 using namespace spg;
 
@@ -181,6 +182,115 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
     const hipError_t e = bm == 16 ? launch_gemm_block_narrow(a, bm, workgroups, (hipStream_t)stream)
                                   : launch_gemm_block_tiles(a, bm, workgroups, (hipStream_t)stream);
     return e == hipSuccess ? SPG_OK : SPG_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// weight gradient of the grouped product
+// ---------------------------------------------------------------------------
+
+namespace {
+
+int64_t dw_tiles(const spg_grouped_dw_desc *d) { return d->experts * cdiv(d->N, kDwTile) * cdiv(d->K, kDwTile); }
+
+// Parts of every expert's rows: as many as give every compute unit (of the 256
+// of an MI355X) a workgroup, of at least 256 rows on average.
+int32_t dw_slices(const spg_grouped_dw_desc *d)
+{
+    const int64_t tiles = dw_tiles(d);
+    if (tiles == 0) return 1;
+    int64_t s = 256 / tiles;
+    const int64_t most = d->rows / d->experts / 256;
+    s = s < most ? s : most;
+    s = s < kDwMaxSlices ? s : kDwMaxSlices;
+    return s < 1 ? 1 : (int32_t)s;
+}
+
+int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
+{
+    if (!d) return SPG_EINVAL;
+    if (d->rows < 0 || d->x_rows < 0 || d->N < 0 || d->K < 0 || (d->N % 8) || (d->K % 8) || d->experts < 1) return SPG_EINVAL;
+    if (d->ldy < d->N || d->ldx < d->K || (d->ldy & 7) || (d->ldx & 7)) return SPG_EINVAL;
+    const int64_t unit = d->out_fp32 ? 4 : 8;               // elements of 16 bytes
+    if (d->ldo < d->K || d->ldo % unit || d->stride_o % unit) return SPG_EINVAL;
+    if (add && (d->lda < d->K || d->lda % unit || d->stride_a % unit)) return SPG_EINVAL;
+    if (d->experts > 65536 || d->rows >= kMaxIndex || d->x_rows >= kMaxIndex || d->N >= kMaxWords || d->K >= kMaxWords ||
+        d->ldy > (INT64_C(1) << 24) || d->ldx > (INT64_C(1) << 24))
+        return SPG_EUNSUPPORTED;
+    if (gathered && extent(d->x_rows, d->ldx, d->K) >= (INT64_C(1) << 30)) return SPG_EUNSUPPORTED;
+    if (!addressable(d->N, d->ldo) || !addressable(d->experts, d->stride_o) ||
+        (add && (!addressable(d->N, d->lda) || !addressable(d->experts, d->stride_a))))
+        return SPG_EUNSUPPORTED;
+    // experts' matrices do not overlap
+    if (d->experts > 1 && d->stride_o < extent(d->N, d->ldo, d->K)) return SPG_EINVAL;
+    if (add && d->experts > 1 && d->stride_a < extent(d->N, d->lda, d->K)) return SPG_EINVAL;
+    // workgroups of the product, in whole rounds of eight rows of tiles, and of the sum
+    const int64_t rows = d->experts * dw_slices(d) * cdiv(d->N, kDwTile);
+    if ((rows + 7) * cdiv(d->K, kDwTile) >= kMaxGrid || (dw_slices(d) > 1 && dw_tiles(d) * 16 >= kMaxGrid))
+        return SPG_EUNSUPPORTED;
+    return SPG_OK;
+}
+
+}  // namespace
+
+SPG_EXPORT size_t gemm_grouped_dw_workspace_bytes(const spg_grouped_dw_desc *d)
+{
+    if (validate_dw(d, false, false) != SPG_OK) return 0;
+    const int32_t s = dw_slices(d);
+    return s > 1 ? (size_t)dw_tiles(d) * s * kDwTile * kDwTile * sizeof(float) : 0;
+}
+
+SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const int32_t *offsets, const int32_t *row_index,
+                               const void *add, const spg_grouped_dw_desc *d, void *ws, size_t ws_bytes, void *stream)
+{
+    const int v = validate_dw(d, row_index != nullptr, add != nullptr);
+    if (v != SPG_OK) return v;
+    if (!row_index && d->x_rows < d->rows) return SPG_EINVAL;
+    if (d->N == 0 || d->K == 0) return SPG_OK;
+    if (!out || !offsets || (d->rows > 0 && (!dY || (d->x_rows > 0 && !X)))) return SPG_EINVAL;
+    if (!aligned16(out) || !aligned16(dY) || !aligned16(X) || !aligned16(add) || !aligned4(offsets) || !aligned4(row_index))
+        return SPG_EINVAL;
+    const size_t need = gemm_grouped_dw_workspace_bytes(d);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return SPG_EWORKSPACE;
+    {
+        const int64_t size = d->out_fp32 ? 4 : 2, E = d->experts;
+        const Range ro = {out, size * ((E - 1) * d->stride_o + extent(d->N, d->ldo, d->K))};
+        const Range ra = {add, add ? size * ((E - 1) * d->stride_a + extent(d->N, d->lda, d->K)) : 0};
+        const Range outs[] = {ro, {ws, (int64_t)need}};
+        const Range ins[] = {{dY, 2 * extent(d->rows, d->ldy, d->N)}, {X, 2 * extent(d->x_rows, d->ldx, d->K)},
+                             {offsets, 4 * (E + 1)}, {row_index, row_index ? 4 * d->rows : 0}};
+        if (any_overlap(outs, 2, ins, 4) || overlap(ws, (int64_t)need, ra.p, ra.bytes)) return SPG_EINVAL;
+        // add may be the output itself
+        const bool same = add == out && (d->N <= 1 || d->lda == d->ldo) && (E <= 1 || d->stride_a == d->stride_o);
+        if (!same && overlap(ro.p, ro.bytes, ra.p, ra.bytes)) return SPG_EINVAL;
+    }
+    GroupedDwArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dy = (const uint16_t *)dY;
+    a.x = (const uint16_t *)X;
+    a.offsets = offsets;
+    a.row_index = row_index;
+    a.add = add;
+    a.out = out;
+    a.partials = (float *)ws;
+    a.R = d->rows;
+    a.x_rows = d->x_rows;
+    a.N = d->N;
+    a.K = d->K;
+    a.ldy = d->ldy;
+    a.ldx = d->ldx;
+    a.lda = d->lda;
+    a.stride_a = d->stride_a;
+    a.ldo = d->ldo;
+    a.stride_o = d->stride_o;
+    a.E = d->experts;
+    a.out_fp32 = d->out_fp32 != 0;
+    a.slices = dw_slices(d);
+    a.tiles_n = (uint32_t)cdiv(d->N, kDwTile);
+    a.tiles_k = (uint32_t)cdiv(d->K, kDwTile);
+    a.div_n = make_fastdiv(a.tiles_n);
+    a.div_k = make_fastdiv(a.tiles_k);
+    a.div_slice = make_fastdiv((uint32_t)a.slices);
+    return launch_grouped_dw(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 
 // ---------------------------------------------------------------------------
