@@ -634,6 +634,42 @@ int rms_norm_backward(const void *grad_out, const void *h, const void *grad_resi
                       size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* The norm over all gradients of a step, and clipping                       */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * gradient_norm - norm[0] = n = sqrt(sum over all tensors of g^2), fp32; the
+ * squares are formed and added in 64 bits.
+ * clip_gradients - the same, and dst = src f for every tensor, f = n > max_norm ?
+ * max_norm / n : 1, one fp32 product rounded to the tensor's type.  Where n is not
+ * finite, f = 1: the gradients stay as they are, and the caller sees norm.
+ *   list     : `count` tensors (host memory, read during the call); src and dst
+ *              hold n contiguous elements, bf16 or fp32, aligned as one element;
+ *              n may be 0 (pointers are not looked at).  gradient_norm ignores dst
+ *   dst      : may be src itself (then nothing is written where f = 1)
+ *   max_norm : finite, not negative
+ *   norm     : device, fp32 [1]
+ *   ws       : device workspace of at least gradient_workspace_bytes(list,
+ *              count) (any contents; 16-byte aligned)
+ * A tensor may stand in the list of gradient_norm more than once and counts
+ * each time; clip_gradients refuses tensors whose memory overlaps (SPG_EINVAL),
+ * norm and ws overlap nothing.  Sums in an order that the sizes alone decide.  At
+ * most 2^24 tensors of less than 2^44 elements.  One launch per 120 tensors for
+ * the sums and for the scaling, and one between.
+ */
+typedef struct spg_gradient {
+    const void *src;
+    void *dst;
+    int64_t n;
+    int64_t bf16;              /* else fp32 */
+} spg_gradient;
+
+size_t gradient_workspace_bytes(const spg_gradient *list, int64_t count);
+int gradient_norm(const spg_gradient *list, int64_t count, float *norm, void *ws, size_t ws_bytes, void *stream);
+int clip_gradients(const spg_gradient *list, int64_t count, double max_norm, float *norm, void *ws, size_t ws_bytes,
+                   void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Tile / route selection (host only, no device access)                     */
 /* ------------------------------------------------------------------------ */
 

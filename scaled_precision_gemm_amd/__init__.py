@@ -9,6 +9,7 @@ fails loudly when the library is not built.
 """
 from __future__ import annotations
 
+import array
 import collections
 import ctypes
 import math
@@ -21,6 +22,7 @@ __all__ = [
     "expert_route", "expert_sort", "expert_route_backward", "expert_combine", "expert_combine_backward",
     "ExpertRoute", "expert_workspace", "grouped_tile_rows", "block128_scale_shape",
     "gemm_grouped_dw", "grouped_dw_workspace", "rms_norm", "rms_norm_backward", "RmsNorm", "norm_workspace",
+    "gradient_norm", "clip_gradients",
     "gemm_plan", "gemm_workspace", "route_select", "route_cost", "probe_mfma", "probe_read", "probe_fp4_rounding",
     "lib", "LIB_PATH",
     "FMT_E4M3_ROW", "FMT_E4M3_TENSOR", "FMT_NVFP4", "FMT_E4M3_BLOCK128", "EPI_STORE", "EPI_ADD", "EPI_SWIGLU",
@@ -147,6 +149,9 @@ SIGNATURES = {
     "rms_norm": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormDesc), _P]),
     "rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
     "rms_norm_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(NormGradDesc), _P, _SZ, _P]),
+    "gradient_workspace_bytes": (_SZ, [_P, _I64]),
+    "gradient_norm": (ctypes.c_int, [_P, _I64, _P, _P, _SZ, _P]),
+    "clip_gradients": (ctypes.c_int, [_P, _I64, ctypes.c_double, _P, _P, _SZ, _P]),
     "spg_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "quantize_rowwise": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _P]),
     "quantize_tensor_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -1158,6 +1163,67 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offs
         _run(lib.rms_norm_backward, "rms_norm_backward", grad_out, grad_out.data_ptr(), h.data_ptr(), _ptr(grad_residual),
              weight.data_ptr(), rstd.data_ptr(), grad_x.data_ptr(), _ptr(gw), ctypes.byref(d), _ptr(ws), nws)
     return grad_x, gw
+
+
+# ---------------------------------------------------------------------------
+# The norm over all gradients of a step, and clipping
+# ---------------------------------------------------------------------------
+
+_GRAD_TYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _gradient_list(grads, out):
+    """The C ABI's list (src, dst, elements, bf16) of the tensors and the
+    first of them; None stands for a parameter without a gradient."""
+    _need(isinstance(grads, (list, tuple)), "gradients must be a list or tuple of tensors")
+    _need(out is None or isinstance(out, (list, tuple)) and len(out) == len(grads), "out must hold a tensor for each gradient")
+    rows, first, dev = array.array("q"), None, -1
+    for i, g in enumerate(grads):
+        o = g if out is None else out[i]
+        if g is None:
+            _need(o is None, f"gradient {i} is None and its output is not")
+            continue
+        _need(isinstance(g, torch.Tensor), f"gradient {i} must be a tensor")
+        kind = _GRAD_TYPE.get(g.dtype)
+        _need(kind is not None and g.is_contiguous(), f"gradient {i} must be a contiguous fp32 or bf16 tensor")
+        if first is None:
+            first, dev = g, g.device
+        _need(g.device == dev, f"gradient {i} must be on {dev}")
+        if o is not g:
+            _need(isinstance(o, torch.Tensor) and o.dtype == g.dtype and o.device == dev and o.shape == g.shape
+                  and o.is_contiguous(), f"output {i} must be a contiguous {g.dtype} {tuple(g.shape)} tensor on {dev}")
+        rows.extend((g.data_ptr(), o.data_ptr(), g.numel(), kind))
+    _need(first is not None, "at least one gradient")
+    _need(first.is_cuda, "gradients must be CUDA tensors")
+    return rows, first
+
+
+def _gradients(fn, what, grads, out, workspace, *more):
+    rows, first = _gradient_list(grads, out)
+    p, n = rows.buffer_info()[0], len(rows) // 4
+    nws = lib.gradient_workspace_bytes(p, n)
+    ws = _order_ws(workspace, max(nws, 16), first)
+    norm = first.new_empty((1,), dtype=torch.float32)
+    _run(fn, what, first, p, n, *more, norm.data_ptr(), ws.data_ptr(), nws)
+    return norm
+
+
+def gradient_norm(grads, workspace=None):
+    """The 2-norm over all elements of all tensors of the list `grads` (fp32 or
+    bf16, contiguous, on one device; None entries are left out), fp32 [1] on
+    that device.  64-bit sums."""
+    return _gradients(lib.gradient_norm, "gradient_norm", grads, None, workspace)
+
+
+def clip_gradients(grads, max_norm, out=None, workspace=None):
+    """Scales the tensors of the list `grads` in place (or into the tensors of
+    the list `out`, alike in shape and type) by max_norm / norm where their
+    norm, as gradient_norm gives it, is over max_norm; returns the norm before,
+    fp32 [1] on their device.  Where the norm is not finite the gradients stay
+    as they are.  The tensors must not share memory."""
+    _need(isinstance(max_norm, (int, float)) and math.isfinite(max_norm) and max_norm >= 0,
+          "max_norm must be a finite number, not below 0")
+    return _gradients(lib.clip_gradients, "clip_gradients", grads, out, workspace, float(max_norm))
 
 
 def route_cost(bm, bn, per_unit, factor, M, N, batch, units) -> float:
