@@ -24,6 +24,8 @@
 #include "spg_gemm_common.h"
 #include "spg_grouped_dw.h"
 
+#include <type_traits>
+
 namespace spg {
 
 namespace {
@@ -38,138 +40,191 @@ constexpr int kStageRows = 32, kLdsRow = 512;                    // one LDS row:
 constexpr int kOperand = kStageRows * kLdsRow, kSlotBytes = 2 * kOperand;
 constexpr int kDepth = 4;
 constexpr int kCopies = 4;                                       // copy instructions of a wave per stage
-constexpr int kRegion = 32 * 64 * 4;                             // epilogue: 32 n x 64 k in fp32 per wave
-static_assert(kDwWaves * kRegion <= kDepth * kSlotBytes, "the epilogue's LDS fits in the slots");
+constexpr int kRegion = 4096;                                    // epilogue: 32 n x 64 k bf16, 32 n x 32 k fp32
+static_assert(kDwWaves * kRegion <= kSlotBytes, "the epilogue's LDS is the one free slot");
+// row numbers of 32 stages of one wave's four rows, two such chunks
+constexpr int kChunkStages = 32, kIndexBytes = kChunkStages * 4 * 4;
 
 enum { kOutBf16, kOutFp32, kOutPartial };
-
-// Chunk of 8 (bf16) or 4 (fp32) elements: add + sum, rounded once.
-template <int OUT>
-__device__ __forceinline__ void store_chunk(const GroupedDwArgs &a, int e, int64_t n, int64_t k, const v4f &lo, const v4f &hi)
-{
-    const int64_t at = (int64_t)e * a.stride_o + n * a.ldo + k;
-    const int64_t from = (int64_t)e * a.stride_a + n * a.lda + k;
-    if (OUT == kOutBf16) {
-        v4f l = lo, h = hi;
-        if (a.add) {
-            const uint4 p = *reinterpret_cast<const uint4 *>((const uint16_t *)a.add + from);
-            l += v4f{bf16_lo(p.x), bf16_hi(p.x), bf16_lo(p.y), bf16_hi(p.y)};
-            h += v4f{bf16_lo(p.z), bf16_hi(p.z), bf16_lo(p.w), bf16_hi(p.w)};
-        }
-        __builtin_nontemporal_store(v4i{(int)pack_bf16x2(l[0], l[1]), (int)pack_bf16x2(l[2], l[3]),
-                                        (int)pack_bf16x2(h[0], h[1]), (int)pack_bf16x2(h[2], h[3])},
-                                    reinterpret_cast<v4i *>((uint16_t *)a.out + at));
-    } else {
-        v4f l = lo;
-        if (a.add) l += *reinterpret_cast<const v4f *>((const float *)a.add + from);
-        __builtin_nontemporal_store(l, reinterpret_cast<v4f *>((float *)a.out + at));
-    }
-}
 
 // Rows of expert e: the offsets are the caller's device data, clamped to [0,
 // R]; a decreasing pair is an empty expert.
 __device__ __forceinline__ void expert_range(const GroupedDwArgs &a, int e, int64_t &lo, int64_t &hi)
 {
+    typedef const __attribute__((address_space(4))) int32_t *Offsets;
+    const Offsets offsets = (Offsets)(uintptr_t)a.offsets;
     const int32_t R = (int32_t)a.R;
-    lo = min(max(a.offsets[e], 0), R);
-    hi = max((int32_t)lo, min(max(a.offsets[e + 1], 0), R));
+    lo = min(max(offsets[e], 0), R);
+    hi = max((int32_t)lo, min(max(offsets[e + 1], 0), R));
 }
 
-// Work items in the order expert, slice, row of tiles, tile.  A row of tiles
-// (which share their panel of dY) stays on one XCD and the rows are dealt to the
-// XCDs in turn, so every XCD gets its share of every expert, however many rows
-// that one has.
-struct DwWork {
+// One tile of an expert's gradient, over rows r0 .. r1 - 1: nk stages, of
+// which the pipeline below takes at least MIN (the last ones copy and add
+// nothing).
+struct DwTile {
     int e, slice;
     uint32_t tn, tk;
-    bool live;
+    int64_t r0, r1;
+    int nk, np;
 };
-__device__ __forceinline__ DwWork dw_work(const GroupedDwArgs &a)
+
+// Tile i of this XCD.  Tiles come in the order expert, slice, row of tiles, tile.
+// A row of tiles (which share their panel of dY) stays on one XCD and the rows
+// are dealt to the XCDs in turn, so every XCD gets its share of every expert,
+// however many rows that one has; eight rows of tiles later it begins with the
+// next XCD, so that an XCD does not read the same columns of every expert.
+template <int OUT, int MIN>
+__device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, uint32_t i)
 {
-    const uint32_t xcd = blockIdx.x & 7u, idx = blockIdx.x >> 3;
-    const uint32_t j = fdiv(idx, a.div_k);                        // rows of tiles of this XCD so far
-    DwWork w;
-    w.tk = idx - j * a.tiles_k;
-    const uint32_t row = j * 8u + xcd;
+    const uint32_t xcd = blockIdx.x & 7u;
+    const uint32_t j = fdiv(i, a.div_k);                          // rows of tiles of this XCD before it
+    DwTile t;
+    t.tk = i - j * a.tiles_k;
+    const uint32_t row = j * 8u + ((xcd + j) & 7u);
     const uint32_t es = fdiv(row, a.div_n);
-    w.tn = row - es * a.tiles_n;
-    w.e = (int)fdiv(es, a.div_slice);
-    w.slice = (int)(es - (uint32_t)w.e * (uint32_t)a.slices);
-    w.live = w.e < a.E;
-    return w;
+    t.tn = row - es * a.tiles_n;
+    t.e = (int)fdiv(es, a.div_slice);
+    t.slice = (int)(es - (uint32_t)t.e * (uint32_t)a.slices);
+    t.r0 = t.r1 = 0;
+    t.nk = 0;
+    if (t.e < a.E) {
+        expert_range(a, t.e, t.r0, t.r1);
+        t.nk = (int)((t.r1 - t.r0 + kStageRows - 1) / kStageRows);
+        if (OUT == kOutPartial) {
+            const int per = (t.nk + a.slices - 1) / a.slices, first = min(t.nk, t.slice * per);
+            t.r0 += (int64_t)first * kStageRows;
+            t.nk = min(t.nk - first, per);
+            t.r1 = min(t.r1, t.r0 + (int64_t)t.nk * kStageRows);
+        }
+    } else {
+        t.e = -1;
+    }
+    t.np = max(t.nk, MIN);
+    return t;
 }
 
 template <int OUT, bool GATHER>
 __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_dw_kernel(
     const GroupedDwArgs a)
 {
-    __shared__ __attribute__((aligned(2048))) uint8_t lds[kDepth * kSlotBytes];
-    const DwWork w = dw_work(a);
-    if (!w.live) return;
+    __shared__ __attribute__((aligned(2048))) uint8_t lds[kDepth * kSlotBytes + (GATHER ? kDwWaves * 2 * kIndexBytes : 0)];
+    constexpr int kMin = GATHER ? 6 : 3;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), ln = lane_id();
     const int wn = wave >> 2, wk = wave & 3;                      // 128 n, 64 k of the tile
-    const int64_t n0 = (int64_t)w.tn * kDwTile, k0 = (int64_t)w.tk * kDwTile;
-    int64_t r0, r1;
-    expert_range(a, w.e, r0, r1);
-    int nk = (int)((r1 - r0 + kStageRows - 1) / kStageRows);
-    if (OUT == kOutPartial) {
-        const int per = (nk + a.slices - 1) / a.slices, first = min(nk, w.slice * per);
-        r0 += (int64_t)first * kStageRows;
-        nk = min(nk - first, per);
-        r1 = min(r1, r0 + (int64_t)nk * kStageRows);
-    }
+    const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
+
+    // ---- this workgroup's tiles: every gridDim.x / 8-th of its XCD's
+    const uint32_t step = gridDim.x >> 3;
+    uint32_t item = blockIdx.x >> 3;
+    DwTile cur = dw_tile<OUT, kMin>(a, item);
+    if (cur.e < 0) return;
+    item += step;
+    DwTile nxt = dw_tile<OUT, kMin>(a, item);
 
     // ---- copies: wave w takes rows 4 w .. 4 w + 3 of a stage, two per
-    // instruction; lane L fetches row L / 32, physical chunk L % 32
-    const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
-    uint32_t cy[2], cx[2];                                        // byte of the row, kOOB past the last column
+    // instruction; lane L fetches row L / 32, physical chunk L % 32.  They run
+    // kDepth stages ahead, across the border of two tiles.
+    uint32_t cb[2];                                               // the chunk's first column
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t r = (uint32_t)(2 * i) + ((uint32_t)ln >> 5);            // row % 4
-        const uint32_t c = ((uint32_t)ln & 31u) ^ (r << 2);
-        cy[i] = n0 + c * 8 < a.N ? (uint32_t)(n0 + c * 8) * 2u : kOOB;
-        cx[i] = k0 + c * 8 < a.K ? (uint32_t)(k0 + c * 8) * 2u : kOOB;
-    }
+    for (int i = 0; i < 2; ++i) cb[i] = (((uint32_t)ln & 31u) ^ (((uint32_t)(2 * i) + ((uint32_t)ln >> 5)) << 2)) * 8u;
     const uint32_t ldy = (uint32_t)a.ldy * 2u, ldx = (uint32_t)a.ldx * 2u;
     const v4i rs_all = make_rsrc(a.x, GATHER && a.x_rows > 0 ? (uint32_t)((a.x_rows - 1) * a.ldx + a.K) * 2u : 0u);
-    // the stage's row numbers of this wave's four rows, -1 past the last one
-    // (scalar loads: they do not enter the count of copies in flight)
-    typedef const __attribute__((address_space(4))) int32_t *Indices;
-    const Indices row_index = (Indices)(uintptr_t)a.row_index;
-    auto indices = [&](int st, int32_t (&idx)[4]) {
+    struct {
+        const uint16_t *y, *x;                                    // the next stage's first rows
+        int rows;                                                 // of the tile from there on; not above 0: none
+        int left, at, buf;                                        // stages left; stage of the tile; index buffer
+        uint32_t vy[2], vx[2];                                    // byte offsets of the lane's chunks (gathered X: in its row)
+    } cp;
+    auto copy_tile = [&](const DwTile &t) {
+        cp.y = a.dy + t.r0 * a.ldy;
+        cp.x = a.x + (GATHER ? 0 : t.r0 * a.ldx);
+        cp.rows = (int)(t.r1 - t.r0);
+        cp.left = t.np;
+        cp.at = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + (int64_t)st * kStageRows + wave * 4 + i;
-            const int32_t v = row_index[r < r1 ? r : r1 - 1];     // (called with r1 > r0)
-            idx[i] = r < r1 && v >= 0 && (int64_t)v < a.x_rows ? v : -1;
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t row = (uint32_t)(wave * 4 + 2 * i + (ln >> 5));
+            const uint32_t cy = t.tn * kDwTile + cb[i], cx = t.tk * kDwTile + cb[i];
+            cp.vy[i] = cy < (uint32_t)a.N ? row * ldy + cy * 2u : kOOB;
+            cp.vx[i] = cx < (uint32_t)a.K ? (GATHER ? 0u : row * ldx) + cx * 2u : kOOB;
         }
     };
-    auto issue = [&](int st, int slot, const int32_t (&idx)[4]) {
+    copy_tile(cur);
+    cp.buf = 0;
+    const uint32_t index_at = lds_base + (uint32_t)(kDepth * kSlotBytes + wave * 2 * kIndexBytes);
+    // row numbers of chunk c of a tile's rows into buffer buf: each wave those
+    // of its own rows, read back by itself.  `since` counts the stages copied
+    // after them: from the third on, the pipeline's waits have seen them land.
+    int since = 0;
+    auto copy_indices = [&](int64_t r0, int64_t r1, int c, int buf) {
+        const int64_t first = r0 + (int64_t)c * (kChunkStages * kStageRows);
+        const int64_t n = max((int64_t)0, min(r1 - first, (int64_t)(kChunkStages * kStageRows)));
+        const v4i rs = make_rsrc(a.row_index + (n > 0 ? first : 0), (uint32_t)n * 4u);
+        const uint32_t base = (uint32_t)__builtin_amdgcn_readfirstlane((int)(index_at + (uint32_t)(buf * kIndexBytes)));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            dma4(base + 256u * k, (uint32_t)((16 * k + (ln >> 2)) * kStageRows + wave * 4 + (ln & 3)) * 4u, rs, 0);
+        since = 0;
+    };
+    // What the next stage's copies take, worked out ahead of the barrier that
+    // frees their slot; then copy instruction i of the four.  Rows past the
+    // tile's last one are past the buffers' ranges.
+    struct {
+        v4i y, x;
+        uint32_t vy[2], vx[2];
+    } pl;
+    auto plan = [&]() {
+        const bool border = cp.left == 0, chunk = cp.at > 0 && cp.at % kChunkStages == 0;
+        if (GATHER && (border || chunk)) {
+            if (since < 3) wait_vmem<0>();
+            cp.buf ^= 1;
+        }
+        if (border) copy_tile(nxt);
+        const uint32_t live = (uint32_t)max(0, min(kStageRows, cp.rows));
+        pl.y = make_rsrc(cp.y, live * ldy);
+        pl.x = GATHER ? rs_all : make_rsrc(cp.x, live * ldx);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            pl.vy[i] = cp.vy[i];
+            pl.vx[i] = cp.vx[i];
+            if (GATHER) {
+                const int row = wave * 4 + 2 * i + (ln >> 5);
+                const int32_t v = *reinterpret_cast<const int32_t *>(
+                    &lds[kDepth * kSlotBytes + (wave * 2 + cp.buf) * kIndexBytes + ((cp.at % kChunkStages) * 4 + 2 * i + (ln >> 5)) * 4]);
+                const bool ok = row < (int)live && cp.vx[i] != kOOB && v >= 0 && (int64_t)v < a.x_rows;
+                pl.vx[i] = ok ? (uint32_t)v * ldx + cp.vx[i] : kOOB;
+            }
+        }
+    };
+    auto issue_one = [&](int slot, int i) {
         const uint32_t base =
             (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_base + (uint32_t)(slot * kSlotBytes + wave * 4 * kLdsRow)));
-        const int64_t r = r0 + (int64_t)st * kStageRows;
-        const int left = (int)max((int64_t)0, min((int64_t)kStageRows, r1 - r));
-        const int64_t rb = left > 0 ? r : 0;
-        const v4i rs_y = make_rsrc(a.dy + rb * a.ldy, left > 0 ? (uint32_t)((left - 1) * a.ldy + a.N) * 2u : 0u);
-        const v4i rs_x = GATHER ? rs_all
-                                : make_rsrc(a.x + rb * a.ldx, left > 0 ? (uint32_t)((left - 1) * a.ldx + a.K) * 2u : 0u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = wave * 4 + 2 * i + (ln >> 5);
-            dma16(base + (uint32_t)(2 * i * kLdsRow), row < left && cy[i] != kOOB ? (uint32_t)row * ldy + cy[i] : kOOB, rs_y, 0);
+        if (i < 2)
+            dma16(base + (uint32_t)(2 * i * kLdsRow), pl.vy[i & 1], pl.y, 0);
+        else
+            dma16(base + (uint32_t)(kOperand + 2 * (i & 1) * kLdsRow), pl.vx[i & 1], pl.x, 0);
+    };
+    auto advance = [&]() {
+        ++since;
+        // the first stage of a later chunk: the chunk after it
+        if (GATHER && cp.at > 0 && cp.at % kChunkStages == 0) {
+            const int c = cp.at / kChunkStages + 1;
+            if (c * kChunkStages < cur.np)
+                copy_indices(cur.r0, cur.r1, c, cp.buf ^ 1);
+            else
+                copy_indices(nxt.r0, nxt.r1, 0, cp.buf ^ 1);
         }
+        cp.y += kStageRows * a.ldy;
+        if (!GATHER) cp.x += kStageRows * a.ldx;
+        cp.rows -= kStageRows;
+        ++cp.at;
+        --cp.left;
+    };
+    auto issue = [&](int slot) {
+        plan();
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = wave * 4 + 2 * i + (ln >> 5);
-            bool ok = row < left && cx[i] != kOOB;
-            uint32_t off = (uint32_t)row * ldx;
-            if (GATHER) {
-                const int32_t v = ln < 32 ? idx[2 * i] : idx[2 * i + 1];
-                ok = ok && v >= 0;
-                off = (uint32_t)v * ldx;
-            }
-            dma16(base + (uint32_t)(kOperand + 2 * i * kLdsRow), ok ? off + cx[i] : kOOB, rs_x, 0);
-        }
+        for (int i = 0; i < kCopies; ++i) issue_one(slot, i);
+        advance();
     };
 
     // ---- fragments: of a 32-column block, lane group l / 16 = (g1 g0) holds
@@ -192,97 +247,191 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(uintptr_t)(lds_base + at + 4 * kLdsRow));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
+    v8bf bx[2][2], by[2][4];
+    auto read_frag = [&](uint32_t sb, int h, int i) {             // i: 0, 1 X blocks, 2 .. 5 Y blocks
+        const uint32_t at = sb + (uint32_t)(h * 16 * kLdsRow);
+        if (i < 2)
+            bx[h][i & 1] = frag(at + fx[i & 1]);
+        else
+            by[h][(i - 2) & 3] = frag(at + fy[(i - 2) & 3]);
+    };
 
+    // ---- the pipeline.  One stage is two steps of 16 rows, each 8 MFMAs, m =
+    // 2 y + x; the next step's fragments are read under this step's MFMAs.
+    // Before the second step all of the stage's fragments are in registers
+    // and this wave's copies of the next stage have landed -> barrier: the
+    // slot is free, the next stage is published, and under the second step the
+    // copies of stage st + kDepth go into the slot.  The scheduling barriers
+    // pin that order (the compiler otherwise reads each fragment right before
+    // its MFMA); hazards and the waits of LDS reads are the compiler's.
+    //
+    // A tile's last kDepth stages copy the next tile's first ones, but for the
+    // very last: its slot is the epilogue's.  Before the epilogue all copies
+    // in flight have landed (stages 0 .. 2 of the next tile), so that the
+    // first two stages after it need no wait: one would wait for the
+    // epilogue's stores as well, which share the counter.
     v16f acc[2][4];
+    int slot = 0;
+    auto stage = [&](auto real_c, int st) {
+        constexpr bool REAL = decltype(real_c)::value;
+        const int next = slot + 1 == kDepth ? 0 : slot + 1;
+        const uint32_t sb = (uint32_t)(slot * kSlotBytes), nb = (uint32_t)(next * kSlotBytes);
+        const bool more = st != cur.np - 1;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.0f;
-
-    if (nk > 0) {
-        int32_t idx[4] = {-1, -1, -1, -1};
-#pragma unroll
-        for (int s = 0; s < kDepth - 1; ++s) {
-            if (GATHER) indices(s, idx);
-            issue(s, s, idx);
-        }
-        int slot = 0;
-        for (int st = 0; st < nk; ++st) {
-            // stage st has landed for every wave, and every wave is done with
-            // stage st - 1, whose slot takes stage st + kDepth - 1 (zeros past
-            // the last, so that every wait counts the same)
-            if (GATHER) indices(st + kDepth - 1, idx);
-            wait_vmem<(kDepth - 2) * kCopies>();
-            block_barrier();
-            issue(st + kDepth - 1, slot == 0 ? kDepth - 1 : slot - 1, idx);
-            const uint32_t sb = (uint32_t)(slot * kSlotBytes);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                v8bf bx[2], by[4];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) bx[b] = frag(sb + fx[b] + h * 16 * kLdsRow);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) by[b] = frag(sb + fy[b] + h * 16 * kLdsRow);
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx[x], by[y], acc[x][y], 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+                wait_lds();
+                if (st >= 2) wait_vmem<(kDepth - 2) * kCopies>();
+                block_barrier();
             }
-            slot = slot + 1 == kDepth ? 0 : slot + 1;
-        }
-        wait_vmem<0>();
-        wait_lds();
-        block_barrier();                                          // the slots become the epilogue's
-    }
-
-    // ---- epilogue: lane l of a block holds n = l % 32 and, per register
-    // group q, k = 8 q + 4 (l / 32) .. + 3.  32 n x 64 k at a time through
-    // the wave's own LDS region (16-byte chunk c of row n at c ^ (n % 16)), so
-    // that whole row segments leave.
-    float *const region = reinterpret_cast<float *>(&lds[wave * kRegion]);
-    const int l32 = ln & 31, kh = ln >> 5;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-        __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < 8; ++m) {
+                const int y = m >> 1, x = m & 1;
+                if (REAL) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx[h][x], by[h][y], acc[x][y], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (m < 6 && (REAL || h == 1)) read_frag(h == 0 ? sb : nb, h ^ 1, m);
+                if (h == 0 && m == 6 && more) plan();
+                if (h == 1 && m < kCopies && more) issue_one(slot, m);
+                if (h == 1 && m == kCopies && more) advance();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        slot = next;
+    };
+
+    if (GATHER) {
+        copy_indices(cur.r0, cur.r1, 0, 0);
+        wait_vmem<0>();
+    }
+#pragma unroll
+    for (int s = 0; s < kDepth - 1; ++s) issue(s);
+    wait_vmem<0>();
+    block_barrier();
+#pragma unroll
+    for (int i = 0; i < 6; ++i) read_frag(0, 0, i);
+    for (;;) {
+        // the slot behind the three stages that have landed; the row numbers
+        // behind the chunk that the copies are in (the first)
+        if (GATHER) {
+            if (cur.np > kChunkStages)
+                copy_indices(cur.r0, cur.r1, 1, cp.buf ^ 1);
+            else
+                copy_indices(nxt.r0, nxt.r1, 0, cp.buf ^ 1);
+        }
+        issue(slot == 0 ? kDepth - 1 : slot - 1);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = x * 8 + q * 2 + kh;
-                *reinterpret_cast<v4f *>(region + l32 * 64 + ((c ^ (l32 & 15)) << 2)) =
-                    v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]};
-            }
-        const int nb = wn * 128 + y * 32, kb = wk * 64;
-        if (OUT == kOutPartial) {
-            const int64_t tile = ((int64_t)w.e * a.tiles_n + w.tn) * a.tiles_k + w.tk;
-            float *const p = a.partials + (tile * a.slices + w.slice) * (kDwTile * kDwTile);
+            for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int r = it * 4 + (ln >> 4), c = ln & 15;
-                *reinterpret_cast<v4f *>(p + (nb + r) * kDwTile + kb + c * 4) =
-                    *reinterpret_cast<const v4f *>(region + r * 64 + ((c ^ (r & 15)) << 2));
-            }
-        } else if (OUT == kOutBf16) {
+                for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.0f;
+        for (int st = 0; st < cur.nk; ++st) stage(std::true_type{}, st);
+        for (int st = cur.nk; st < cur.np; ++st) stage(std::false_type{}, st);
+        wait_vmem<0>();
+
+        // ---- epilogue: lane l of a block holds n = l % 32 and, per register
+        // group q, k = 8 q + 4 (l / 32) .. + 3.  128-byte rows of the output
+        // go through the wave's own region (16-byte chunk c of row n at c ^
+        // (n / 2 % 8)), so that whole lines leave.
+        uint8_t *const region = &lds[(slot == 0 ? kDepth - 1 : slot - 1) * kSlotBytes + wave * kRegion];
+        const int l32 = ln & 31, kh = ln >> 5, r8 = ln >> 3, c8 = ln & 7;
+        const int64_t n0 = (int64_t)cur.tn * kDwTile + wn * 128, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
+        auto place = [&](int row, int c) { return region + row * 128 + ((c ^ ((row >> 1) & 7)) << 4); };
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const int r = it * 8 + (ln >> 3), c = (ln & 7) * 2;
-                const v4f lo = *reinterpret_cast<const v4f *>(region + r * 64 + ((c ^ (r & 15)) << 2));
-                const v4f hi = *reinterpret_cast<const v4f *>(region + r * 64 + (((c + 1) ^ (r & 15)) << 2));
-                const int64_t n = n0 + nb + r, k = k0 + kb + c * 4;
-                if (n < a.N && k < a.K) store_chunk<kOutBf16>(a, w.e, n, k, lo, hi);
-            }
-        } else {
+        for (int y = 0; y < 4; ++y) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (OUT == kOutBf16) {
+                if (a.add) {
+                    const uint16_t *from = (const uint16_t *)a.add + (int64_t)cur.e * a.stride_a;
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int r = it * 4 + (ln >> 4), c = ln & 15;
-                const v4f lo = *reinterpret_cast<const v4f *>(region + r * 64 + ((c ^ (r & 15)) << 2));
-                const int64_t n = n0 + nb + r, k = k0 + kb + c * 4;
-                if (n < a.N && k < a.K) store_chunk<kOutFp32>(a, w.e, n, k, lo, lo);
+                    for (int it = 0; it < 4; ++it) {
+                        const int64_t n = n0 + y * 32 + it * 8 + r8, k = k0 + c8 * 8;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (n < a.N && k < a.K) v = *reinterpret_cast<const uint4 *>(from + n * a.lda + k);
+                        *reinterpret_cast<uint4 *>(place(it * 8 + r8, c8)) = v;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint2 *const p = reinterpret_cast<uint2 *>(place(l32, x * 4 + q) + kh * 8);
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = acc[x][y][4 * q + i];
+                        if (a.add) {
+                            const uint2 r = *p;
+                            v[0] += bf16_lo(r.x);
+                            v[1] += bf16_hi(r.x);
+                            v[2] += bf16_lo(r.y);
+                            v[3] += bf16_hi(r.y);
+                        }
+                        *p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                    }
+                uint16_t *const to = (uint16_t *)a.out + (int64_t)cur.e * a.stride_o;
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const v4i v = *reinterpret_cast<const v4i *>(place(it * 8 + r8, c8));
+                    const int64_t n = n0 + y * 32 + it * 8 + r8, k = k0 + c8 * 8;
+                    if (n < a.N && k < a.K) __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(to + n * a.ldo + k));
+                }
+                continue;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<v4f *>(place(l32, q * 2 + kh)) =
+                        v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]};
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    v4f v = *reinterpret_cast<const v4f *>(place(it * 8 + r8, c8));
+                    const int row = it * 8 + r8, col = x * 32 + c8 * 4;
+                    if (OUT == kOutPartial) {
+                        const int64_t tile = ((int64_t)cur.e * a.tiles_n + cur.tn) * a.tiles_k + cur.tk;
+                        float *const p = a.partials + (tile * a.slices + cur.slice) * (kDwTile * kDwTile);
+                        *reinterpret_cast<v4f *>(p + (wn * 128 + y * 32 + row) * kDwTile + wk * 64 + col) = v;
+                    } else {
+                        const int64_t n = n0 + y * 32 + row, k = k0 + col;
+                        if (n < a.N && k < a.K) {
+                            if (a.add) v += *reinterpret_cast<const v4f *>((const float *)a.add + cur.e * a.stride_a + n * a.lda + k);
+                            __builtin_nontemporal_store(v, reinterpret_cast<v4f *>((float *)a.out + cur.e * a.stride_o + n * a.ldo + k));
+                        }
+                    }
+                }
             }
         }
+        if (nxt.e < 0) break;
+        cur = nxt;
+        item += step;
+        nxt = dw_tile<OUT, kMin>(a, item);
+        // every wave's copies of the next tile's first three stages have landed,
+        // and every wave is done with the epilogue's slot
+        wait_lds();
+        block_barrier();
+    }
+}
+
+// Chunk of 8 (bf16) or 4 (fp32) elements: add + sum, rounded once.
+template <int OUT>
+__device__ __forceinline__ void store_chunk(const GroupedDwArgs &a, int e, int64_t n, int64_t k, const v4f &lo, const v4f &hi)
+{
+    const int64_t at = (int64_t)e * a.stride_o + n * a.ldo + k;
+    const int64_t from = (int64_t)e * a.stride_a + n * a.lda + k;
+    if (OUT == kOutBf16) {
+        v4f l = lo, h = hi;
+        if (a.add) {
+            const uint4 p = *reinterpret_cast<const uint4 *>((const uint16_t *)a.add + from);
+            l += v4f{bf16_lo(p.x), bf16_hi(p.x), bf16_lo(p.y), bf16_hi(p.y)};
+            h += v4f{bf16_lo(p.z), bf16_hi(p.z), bf16_lo(p.w), bf16_hi(p.w)};
+        }
+        __builtin_nontemporal_store(v4i{(int)pack_bf16x2(l[0], l[1]), (int)pack_bf16x2(l[2], l[3]),
+                                        (int)pack_bf16x2(h[0], h[1]), (int)pack_bf16x2(h[2], h[3])},
+                                    reinterpret_cast<v4i *>((uint16_t *)a.out + at));
+    } else {
+        v4f l = lo;
+        if (a.add) l += *reinterpret_cast<const v4f *>((const float *)a.add + from);
+        __builtin_nontemporal_store(l, reinterpret_cast<v4f *>((float *)a.out + at));
     }
 }
 
@@ -325,9 +474,10 @@ hipError_t launch_out(const GroupedDwArgs &a, unsigned grid, hipStream_t s)
 
 hipError_t launch_grouped_dw(const GroupedDwArgs &a, hipStream_t s)
 {
-    // whole rounds of the eight XCDs; workgroups without a row of tiles end at once
-    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n;
-    const unsigned grid = (unsigned)((rows + 7) / 8 * 8 * a.tiles_k);
+    // one workgroup per compute unit (of the 256 of an MI355X), or as many on
+    // each XCD as it has tiles
+    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, most = (rows + 7) / 8 * a.tiles_k;
+    const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
     if (a.slices == 1) return a.out_fp32 ? launch_out<kOutFp32>(a, grid, s) : launch_out<kOutBf16>(a, grid, s);
     hipError_t e = launch_out<kOutPartial>(a, grid, s);
     if (e != hipSuccess) return e;
