@@ -47,15 +47,29 @@ constexpr int kChunkStages = 32, kIndexBytes = kChunkStages * 4 * 4;
 
 enum { kOutBf16, kOutFp32, kOutPartial };
 
-// Rows of expert e: the offsets are the caller's device data, clamped to [0,
-// R]; a decreasing pair is an empty expert.
-__device__ __forceinline__ void expert_range(const GroupedDwArgs &a, int e, int64_t &lo, int64_t &hi)
+// 64 consecutive experts from `base` on, one per lane: their rows (the offsets
+// are the caller's device data, clamped to [0, R]; a decreasing pair is an
+// empty expert) and their rank among the 64, most rows first.
+struct DwExperts {
+    int base;
+    int32_t first, rows;
+    int rank;
+};
+__device__ __forceinline__ DwExperts dw_experts(const GroupedDwArgs &a, int base)
 {
-    typedef const __attribute__((address_space(4))) int32_t *Offsets;
-    const Offsets offsets = (Offsets)(uintptr_t)a.offsets;
+    const int lane = lane_id(), e = base + lane;
     const int32_t R = (int32_t)a.R;
-    lo = min(max(offsets[e], 0), R);
-    hi = max((int32_t)lo, min(max(offsets[e + 1], 0), R));
+    DwExperts w = {base, 0, -1, 0};
+    if (e < a.E) {
+        w.first = min(max(a.offsets[e], 0), R);
+        w.rows = max(min(max(a.offsets[e + 1], 0), R) - w.first, 0);
+    }
+    const int n = min(64, a.E - base);
+    for (int i = 0; i < n; ++i) {
+        const int32_t r = __builtin_amdgcn_readlane(w.rows, i);
+        w.rank += r > w.rows || (r == w.rows && i < lane) ? 1 : 0;
+    }
+    return w;
 }
 
 // One tile of an expert's gradient, over rows r0 .. r1 - 1: nk stages, of
@@ -68,13 +82,14 @@ struct DwTile {
     int nk, np;
 };
 
-// Tile i of this XCD.  Tiles come in the order expert, slice, row of tiles, tile.
-// A row of tiles (which share their panel of dY) stays on one XCD and the rows
-// are dealt to the XCDs in turn, so every XCD gets its share of every expert,
-// however many rows that one has; eight rows of tiles later it begins with the
-// next XCD, so that an XCD does not read the same columns of every expert.
+// Tile i of this XCD.  Tiles come in the order expert (most rows first among
+// each 64), slice, row of tiles, tile.  A row of tiles (which share their panel
+// of dY) stays on one XCD and the rows are dealt to the XCDs in turn, so every
+// XCD gets its share of every expert, however many rows that one has; eight
+// rows of tiles later it begins with the next XCD, so that an XCD does not read
+// the same columns of every expert.
 template <int OUT, int MIN>
-__device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, uint32_t i)
+__device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, uint32_t i)
 {
     const uint32_t xcd = blockIdx.x & 7u;
     const uint32_t j = fdiv(i, a.div_k);                          // rows of tiles of this XCD before it
@@ -83,12 +98,17 @@ __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, uint32_t i)
     const uint32_t row = j * 8u + ((xcd + j) & 7u);
     const uint32_t es = fdiv(row, a.div_n);
     t.tn = row - es * a.tiles_n;
-    t.e = (int)fdiv(es, a.div_slice);
-    t.slice = (int)(es - (uint32_t)t.e * (uint32_t)a.slices);
+    const int place = (int)fdiv(es, a.div_slice);
+    t.slice = (int)(es - (uint32_t)place * (uint32_t)a.slices);
+    t.e = -1;
     t.r0 = t.r1 = 0;
     t.nk = 0;
-    if (t.e < a.E) {
-        expert_range(a, t.e, t.r0, t.r1);
+    if (place < a.E) {
+        if ((place & ~63) != w.base) w = dw_experts(a, place & ~63);
+        const int src = __builtin_ctzll(__ballot(w.rank == (place & 63) && w.rows >= 0));
+        t.e = w.base + src;
+        t.r0 = __builtin_amdgcn_readlane(w.first, src);
+        t.r1 = t.r0 + __builtin_amdgcn_readlane(w.rows, src);
         t.nk = (int)((t.r1 - t.r0 + kStageRows - 1) / kStageRows);
         if (OUT == kOutPartial) {
             const int per = (t.nk + a.slices - 1) / a.slices, first = min(t.nk, t.slice * per);
@@ -96,8 +116,6 @@ __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, uint32_t i)
             t.nk = min(t.nk - first, per);
             t.r1 = min(t.r1, t.r0 + (int64_t)t.nk * kStageRows);
         }
-    } else {
-        t.e = -1;
     }
     t.np = max(t.nk, MIN);
     return t;
@@ -113,13 +131,18 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     const int wn = wave >> 2, wk = wave & 3;                      // 128 n, 64 k of the tile
     const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
 
-    // ---- this workgroup's tiles: every gridDim.x / 8-th of its XCD's
-    const uint32_t step = gridDim.x >> 3;
-    uint32_t item = blockIdx.x >> 3;
-    DwTile cur = dw_tile<OUT, kMin>(a, item);
+    // ---- this workgroup's tiles: one of every `step` of its XCD's, from the
+    // front and from the back in turn: with the experts in the order of their
+    // rows, all workgroups get about as much
+    const uint32_t step = gridDim.x >> 3, first_item = blockIdx.x >> 3;
+    DwExperts experts = dw_experts(a, 0);
+    uint32_t round = 0;
+    auto tile = [&](uint32_t k) {
+        return dw_tile<OUT, kMin>(a, experts, k * step + ((k & 1) ? step - 1 - first_item : first_item));
+    };
+    DwTile cur = tile(0);
     if (cur.e < 0) return;
-    item += step;
-    DwTile nxt = dw_tile<OUT, kMin>(a, item);
+    DwTile nxt = tile(++round);
 
     // ---- copies: wave w takes rows 4 w .. 4 w + 3 of a stage, two per
     // instruction; lane L fetches row L / 32, physical chunk L % 32.  They run
@@ -403,8 +426,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         }
         if (nxt.e < 0) break;
         cur = nxt;
-        item += step;
-        nxt = dw_tile<OUT, kMin>(a, item);
+        nxt = tile(++round);
         // every wave's copies of the next tile's first three stages have landed,
         // and every wave is done with the epilogue's slot
         wait_lds();
