@@ -190,19 +190,28 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
 
 namespace {
 
-int64_t dw_tiles(const spg_grouped_dw_desc *d) { return d->experts * cdiv(d->N, kDwTile) * cdiv(d->K, kDwTile); }
-
-// Parts of every expert's rows: as many as give every compute unit (of the 256
-// of an MI355X) a workgroup, of at least 256 rows on average.
-int32_t dw_slices(const spg_grouped_dw_desc *d)
+// Tiles of 256 n x 256 k; 128 n where those would leave half of the compute
+// units (256 on an MI355X) idle, and every expert's rows then in as many parts,
+// of at least 256 rows on average, as give every unit a workgroup.
+struct DwPlan {
+    int32_t tile_n, slices;
+    int64_t tiles_n, tiles_k, tiles;
+};
+DwPlan dw_plan(const spg_grouped_dw_desc *d)
 {
-    const int64_t tiles = dw_tiles(d);
-    if (tiles == 0) return 1;
-    int64_t s = 256 / tiles;
+    DwPlan p = {256, 1, cdiv(d->N, 256), cdiv(d->K, kDwTile), 0};
+    if (d->experts * p.tiles_n * p.tiles_k <= 128) {
+        p.tile_n = 128;
+        p.tiles_n = cdiv(d->N, 128);
+    }
+    p.tiles = d->experts * p.tiles_n * p.tiles_k;
+    if (p.tiles == 0) return p;
+    int64_t s = 256 / p.tiles;
     const int64_t most = d->rows / d->experts / 256;
     s = s < most ? s : most;
     s = s < kDwMaxSlices ? s : kDwMaxSlices;
-    return s < 1 ? 1 : (int32_t)s;
+    p.slices = s < 1 ? 1 : (int32_t)s;
+    return p;
 }
 
 int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
@@ -223,10 +232,8 @@ int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
     // experts' matrices do not overlap
     if (d->experts > 1 && d->stride_o < extent(d->N, d->ldo, d->K)) return SPG_EINVAL;
     if (add && d->experts > 1 && d->stride_a < extent(d->N, d->lda, d->K)) return SPG_EINVAL;
-    // workgroups of the product, in whole rounds of eight rows of tiles, and of the sum
-    const int64_t rows = d->experts * dw_slices(d) * cdiv(d->N, kDwTile);
-    if ((rows + 7) * cdiv(d->K, kDwTile) >= kMaxGrid || (dw_slices(d) > 1 && dw_tiles(d) * 16 >= kMaxGrid))
-        return SPG_EUNSUPPORTED;
+    // tiles are counted in 32 bits
+    if ((d->experts * cdiv(d->N, 128) + 8) * cdiv(d->K, kDwTile) >= kMaxIndex / kDwMaxSlices) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
 
@@ -235,8 +242,8 @@ int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
 SPG_EXPORT size_t gemm_grouped_dw_workspace_bytes(const spg_grouped_dw_desc *d)
 {
     if (validate_dw(d, false, false) != SPG_OK) return 0;
-    const int32_t s = dw_slices(d);
-    return s > 1 ? (size_t)dw_tiles(d) * s * kDwTile * kDwTile * sizeof(float) : 0;
+    const DwPlan p = dw_plan(d);
+    return p.slices > 1 ? (size_t)p.tiles * p.slices * p.tile_n * kDwTile * sizeof(float) : 0;
 }
 
 SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const int32_t *offsets, const int32_t *row_index,
@@ -284,9 +291,11 @@ SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const i
     a.stride_o = d->stride_o;
     a.E = d->experts;
     a.out_fp32 = d->out_fp32 != 0;
-    a.slices = dw_slices(d);
-    a.tiles_n = (uint32_t)cdiv(d->N, kDwTile);
-    a.tiles_k = (uint32_t)cdiv(d->K, kDwTile);
+    const DwPlan p = dw_plan(d);
+    a.slices = p.slices;
+    a.tile_n = p.tile_n;
+    a.tiles_n = (uint32_t)p.tiles_n;
+    a.tiles_k = (uint32_t)p.tiles_k;
     a.div_n = make_fastdiv(a.tiles_n);
     a.div_k = make_fastdiv(a.tiles_k);
     a.div_slice = make_fastdiv((uint32_t)a.slices);

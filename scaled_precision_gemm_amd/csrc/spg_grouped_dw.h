@@ -11,14 +11,15 @@ struct GroupedDwArgs {
     const int32_t *row_index;           // [R] or null
     const void *add;                    // [E, N, K] in the output's type or null, row stride lda, expert stride stride_a
     void *out;                          // [E, N, K], ldo, stride_o
-    float *partials;                    // slices > 1: [tiles, slices, 256, 256]
+    float *partials;                    // slices > 1: [tiles, slices, tile_n, 256]
     int64_t R, x_rows, N, K, ldy, ldx, lda, stride_a, ldo, stride_o;
     int32_t E, out_fp32;
     int32_t slices;                     // parts of every expert's rows, summed by a second launch
-    uint32_t tiles_n, tiles_k;          // 256 x 256 tiles of one expert
+    int32_t tile_n;                     // tiles of tile_n (128 or 256) n x 256 k
+    uint32_t tiles_n, tiles_k;          // tiles of one expert
     FastDiv div_k, div_n, div_slice;    // by tiles_k, tiles_n, slices
 };
-constexpr int kDwTile = 256;
+constexpr int kDwTile = 256;             // k of a tile
 constexpr int kDwMaxSlices = 16;
 hipError_t launch_grouped_dw(const GroupedDwArgs &a, hipStream_t s);
 

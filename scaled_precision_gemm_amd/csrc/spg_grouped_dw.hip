@@ -36,12 +36,23 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kDwThreads = 512, kDwWaves = 8;
-constexpr int kStageRows = 32, kLdsRow = 512;                    // one LDS row: 256 columns
-constexpr int kOperand = kStageRows * kLdsRow, kSlotBytes = 2 * kOperand;
+constexpr int kStageRows = 32;
 constexpr int kDepth = 4;
-constexpr int kCopies = 4;                                       // copy instructions of a wave per stage
 constexpr int kRegion = 4096;                                    // epilogue: 32 n x 64 k bf16, 32 n x 32 k fp32
-static_assert(kDwWaves * kRegion <= kSlotBytes, "the epilogue's LDS is the one free slot");
+
+// Tiles of TN n x 256 k.
+template <int TN>
+struct DwGeometry {
+    static constexpr int kRowY = TN * 2, kRowX = 512;            // LDS rows
+    static constexpr int kY = kStageRows * kRowY, kX = kStageRows * kRowX;
+    static constexpr int kSlot = kY + kX;
+    static constexpr int kRowsPerCopy = 1024 / kRowY;            // of dY: a copy instruction moves 1 KiB
+    static constexpr int kCopyY = 4 / kRowsPerCopy, kCopyX = 2;  // of a wave per stage: its four rows
+    static constexpr int kCopies = kCopyY + kCopyX;
+    static constexpr int kWaveN = TN / 2, kBlocksY = kWaveN / 32;   // n of a wave
+    // the epilogue's regions: the free slot, and where that is smaller LDS of their own behind the slots
+    static constexpr int kOwnRegions = kDwWaves * kRegion > kSlot ? kDwWaves * kRegion : 0;
+};
 // row numbers of 32 stages of one wave's four rows, two such chunks
 constexpr int kChunkStages = 32, kIndexBytes = kChunkStages * 4 * 4;
 
@@ -121,14 +132,16 @@ __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, 
     return t;
 }
 
-template <int OUT, bool GATHER>
+template <int TN, int OUT, bool GATHER>
 __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_dw_kernel(
     const GroupedDwArgs a)
 {
-    __shared__ __attribute__((aligned(2048))) uint8_t lds[kDepth * kSlotBytes + (GATHER ? kDwWaves * 2 * kIndexBytes : 0)];
+    using G = DwGeometry<TN>;
+    constexpr int kIndexAt = kDepth * G::kSlot + G::kOwnRegions;
+    __shared__ __attribute__((aligned(2048))) uint8_t lds[kIndexAt + (GATHER ? kDwWaves * 2 * kIndexBytes : 0)];
     constexpr int kMin = GATHER ? 6 : 3;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), ln = lane_id();
-    const int wn = wave >> 2, wk = wave & 3;                      // 128 n, 64 k of the tile
+    const int wn = wave >> 2, wk = wave & 3;                      // TN / 2 n, 64 k of the tile
     const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
 
     // ---- this workgroup's tiles: one of every `step` of its XCD's, from the
@@ -144,19 +157,18 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     if (cur.e < 0) return;
     DwTile nxt = tile(++round);
 
-    // ---- copies: wave w takes rows 4 w .. 4 w + 3 of a stage, two per
-    // instruction; lane L fetches row L / 32, physical chunk L % 32.  They run
-    // kDepth stages ahead, across the border of two tiles.
-    uint32_t cb[2];                                               // the chunk's first column
-#pragma unroll
-    for (int i = 0; i < 2; ++i) cb[i] = (((uint32_t)ln & 31u) ^ (((uint32_t)(2 * i) + ((uint32_t)ln >> 5)) << 2)) * 8u;
+    // ---- copies: wave w takes rows 4 w .. 4 w + 3 of a stage, 1 KiB per
+    // instruction: X two rows (lane L row L / 32, physical chunk L % 32), dY two
+    // or four.  They run kDepth stages ahead, across the border of two tiles.
+    constexpr uint32_t kLanesY = G::kRowY / 16;                   // lanes of a row of dY
+    const uint32_t ryl = (uint32_t)ln / kLanesY, rxl = (uint32_t)ln >> 5;
     const uint32_t ldy = (uint32_t)a.ldy * 2u, ldx = (uint32_t)a.ldx * 2u;
     const v4i rs_all = make_rsrc(a.x, GATHER && a.x_rows > 0 ? (uint32_t)((a.x_rows - 1) * a.ldx + a.K) * 2u : 0u);
     struct {
         const uint16_t *y, *x;                                    // the next stage's first rows
         int rows;                                                 // of the tile from there on; not above 0: none
         int left, at, buf;                                        // stages left; stage of the tile; index buffer
-        uint32_t vy[2], vx[2];                                    // byte offsets of the lane's chunks (gathered X: in its row)
+        uint32_t vy[G::kCopyY], vx[2];                            // byte offsets of the lane's chunks (gathered X: in its row)
     } cp;
     auto copy_tile = [&](const DwTile &t) {
         cp.y = a.dy + t.r0 * a.ldy;
@@ -165,16 +177,21 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         cp.left = t.np;
         cp.at = 0;
 #pragma unroll
+        for (int i = 0; i < G::kCopyY; ++i) {
+            const uint32_t r = (uint32_t)(G::kRowsPerCopy * i) + ryl;      // row % 4
+            const uint32_t c = t.tn * TN + ((((uint32_t)ln % kLanesY) ^ (r << 2)) << 3);
+            cp.vy[i] = c < (uint32_t)a.N ? ((uint32_t)(wave * 4) + r) * ldy + c * 2u : kOOB;
+        }
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t row = (uint32_t)(wave * 4 + 2 * i + (ln >> 5));
-            const uint32_t cy = t.tn * kDwTile + cb[i], cx = t.tk * kDwTile + cb[i];
-            cp.vy[i] = cy < (uint32_t)a.N ? row * ldy + cy * 2u : kOOB;
-            cp.vx[i] = cx < (uint32_t)a.K ? (GATHER ? 0u : row * ldx) + cx * 2u : kOOB;
+            const uint32_t r = (uint32_t)(2 * i) + rxl;
+            const uint32_t c = t.tk * kDwTile + ((((uint32_t)ln & 31u) ^ (r << 2)) << 3);
+            cp.vx[i] = c < (uint32_t)a.K ? (GATHER ? 0u : ((uint32_t)(wave * 4) + r) * ldx) + c * 2u : kOOB;
         }
     };
     copy_tile(cur);
     cp.buf = 0;
-    const uint32_t index_at = lds_base + (uint32_t)(kDepth * kSlotBytes + wave * 2 * kIndexBytes);
+    const uint32_t index_at = lds_base + (uint32_t)(kIndexAt + wave * 2 * kIndexBytes);
     // row numbers of chunk c of a tile's rows into buffer buf: each wave those
     // of its own rows, read back by itself.  `since` counts the stages copied
     // after them: from the third on, the pipeline's waits have seen them land.
@@ -194,7 +211,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     // tile's last one are past the buffers' ranges.
     struct {
         v4i y, x;
-        uint32_t vy[2], vx[2];
+        uint32_t vy[G::kCopyY], vx[2];
     } pl;
     auto plan = [&]() {
         const bool border = cp.left == 0, chunk = cp.at > 0 && cp.at % kChunkStages == 0;
@@ -207,13 +224,14 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         pl.y = make_rsrc(cp.y, live * ldy);
         pl.x = GATHER ? rs_all : make_rsrc(cp.x, live * ldx);
 #pragma unroll
+        for (int i = 0; i < G::kCopyY; ++i) pl.vy[i] = cp.vy[i];
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-            pl.vy[i] = cp.vy[i];
             pl.vx[i] = cp.vx[i];
             if (GATHER) {
                 const int row = wave * 4 + 2 * i + (ln >> 5);
                 const int32_t v = *reinterpret_cast<const int32_t *>(
-                    &lds[kDepth * kSlotBytes + (wave * 2 + cp.buf) * kIndexBytes + ((cp.at % kChunkStages) * 4 + 2 * i + (ln >> 5)) * 4]);
+                    &lds[kIndexAt + (wave * 2 + cp.buf) * kIndexBytes + ((cp.at % kChunkStages) * 4 + 2 * i + (ln >> 5)) * 4]);
                 const bool ok = row < (int)live && cp.vx[i] != kOOB && v >= 0 && (int64_t)v < a.x_rows;
                 pl.vx[i] = ok ? (uint32_t)v * ldx + cp.vx[i] : kOOB;
             }
@@ -221,11 +239,11 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     };
     auto issue_one = [&](int slot, int i) {
         const uint32_t base =
-            (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_base + (uint32_t)(slot * kSlotBytes + wave * 4 * kLdsRow)));
-        if (i < 2)
-            dma16(base + (uint32_t)(2 * i * kLdsRow), pl.vy[i & 1], pl.y, 0);
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_base + (uint32_t)(slot * G::kSlot)));
+        if (i < G::kCopyY)
+            dma16(base + (uint32_t)(wave * 4 * G::kRowY + i * 1024), pl.vy[i < G::kCopyY ? i : 0], pl.y, 0);
         else
-            dma16(base + (uint32_t)(kOperand + 2 * (i & 1) * kLdsRow), pl.vx[i & 1], pl.x, 0);
+            dma16(base + (uint32_t)(G::kY + wave * 4 * G::kRowX + (i - G::kCopyY) * 1024), pl.vx[(i - G::kCopyY) & 1], pl.x, 0);
     };
     auto advance = [&]() {
         ++since;
@@ -246,7 +264,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     auto issue = [&](int slot) {
         plan();
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) issue_one(slot, i);
+        for (int i = 0; i < G::kCopies; ++i) issue_one(slot, i);
         advance();
     };
 
@@ -255,32 +273,35 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     // transposing reads of four rows; lane j of a group points at row j / 4,
     // columns 4 (j % 4) ..
     const uint32_t j = (uint32_t)ln & 15u, g0 = ((uint32_t)ln >> 4) & 1u, g1 = (uint32_t)ln >> 5, jr = j >> 2;
-    const uint32_t fbase = (8u * g1 + jr) * kLdsRow + 32u * g0 + 8u * (j & 3u);
-    uint32_t fy[4], fx[2];
+    const uint32_t frow = 8u * g1 + jr, fcol = 32u * g0 + 8u * (j & 3u);
+    uint32_t fy[G::kBlocksY], fx[2];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) fy[b] = fbase + ((uint32_t)(wn * 4) + ((uint32_t)b ^ jr)) * 64u;
+    for (int b = 0; b < G::kBlocksY; ++b) {
+        const uint32_t blk = (uint32_t)(wn * G::kBlocksY + b);
+        fy[b] = frow * G::kRowY + fcol + ((blk & 4u) + ((blk & 3u) ^ jr)) * 64u;
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t blk = (uint32_t)(wk * 2 + b);
-        fx[b] = kOperand + fbase + ((blk & 4u) + ((blk & 3u) ^ jr)) * 64u;
+        fx[b] = G::kY + frow * G::kRowX + fcol + ((blk & 4u) + ((blk & 3u) ^ jr)) * 64u;
     }
-    auto frag = [&](uint32_t at) -> v8bf {
+    auto frag = [&](uint32_t at, uint32_t four_rows) -> v8bf {
         typedef __attribute__((address_space(3))) v4s *L;
         const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(uintptr_t)(lds_base + at));
-        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(uintptr_t)(lds_base + at + 4 * kLdsRow));
+        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(uintptr_t)(lds_base + at + four_rows));
         return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    v8bf bx[2][2], by[2][4];
-    auto read_frag = [&](uint32_t sb, int h, int i) {             // i: 0, 1 X blocks, 2 .. 5 Y blocks
-        const uint32_t at = sb + (uint32_t)(h * 16 * kLdsRow);
+    constexpr int kYB = G::kBlocksY, kFrags = 2 + kYB, kMfma = 2 * kYB;   // of a step
+    v8bf bx[2][2], by[2][kYB];
+    auto read_frag = [&](uint32_t sb, int h, int i) {             // i: 0, 1 X blocks, then Y blocks
         if (i < 2)
-            bx[h][i & 1] = frag(at + fx[i & 1]);
+            bx[h][i & 1] = frag(sb + (uint32_t)(h * 16 * G::kRowX) + fx[i & 1], 4 * G::kRowX);
         else
-            by[h][(i - 2) & 3] = frag(at + fy[(i - 2) & 3]);
+            by[h][(i - 2) & (kYB - 1)] = frag(sb + (uint32_t)(h * 16 * G::kRowY) + fy[(i - 2) & (kYB - 1)], 4 * G::kRowY);
     };
 
-    // ---- the pipeline.  One stage is two steps of 16 rows, each 8 MFMAs, m =
-    // 2 y + x; the next step's fragments are read under this step's MFMAs.
+    // ---- the pipeline.  One stage is two steps of 16 rows, each 8 MFMAs (128
+    // n: 4), m = 2 y + x; the next step's fragments are read under this step's MFMAs.
     // Before the second step all of the stage's fragments are in registers
     // and this wave's copies of the next stage have landed -> barrier: the
     // slot is free, the next stage is published, and under the second step the
@@ -293,29 +314,32 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     // in flight have landed (stages 0 .. 2 of the next tile), so that the
     // first two stages after it need no wait: one would wait for the
     // epilogue's stores as well, which share the counter.
-    v16f acc[2][4];
+    v16f acc[2][kYB];
     int slot = 0;
     auto stage = [&](auto real_c, int st) {
         constexpr bool REAL = decltype(real_c)::value;
         const int next = slot + 1 == kDepth ? 0 : slot + 1;
-        const uint32_t sb = (uint32_t)(slot * kSlotBytes), nb = (uint32_t)(next * kSlotBytes);
+        const uint32_t sb = (uint32_t)(slot * G::kSlot), nb = (uint32_t)(next * G::kSlot);
         const bool more = st != cur.np - 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (h == 1) {
                 wait_lds();
-                if (st >= 2) wait_vmem<(kDepth - 2) * kCopies>();
+                if (st >= 2) wait_vmem<(kDepth - 2) * G::kCopies>();
                 block_barrier();
             }
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
+            for (int m = 0; m < kMfma; ++m) {
                 const int y = m >> 1, x = m & 1;
                 if (REAL) acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bx[h][x], by[h][y], acc[x][y], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                if (m < 6 && (REAL || h == 1)) read_frag(h == 0 ? sb : nb, h ^ 1, m);
-                if (h == 0 && m == 6 && more) plan();
-                if (h == 1 && m < kCopies && more) issue_one(slot, m);
-                if (h == 1 && m == kCopies && more) advance();
+                constexpr int kPer = (kFrags + kMfma - 1) / kMfma;      // fragments read per MFMA
+#pragma unroll
+                for (int i = m * kPer; i < (m + 1) * kPer && i < kFrags; ++i)
+                    if (REAL || h == 1) read_frag(h == 0 ? sb : nb, h ^ 1, i);
+                if (h == 0 && m == kMfma - 2 && more) plan();
+                if (h == 1 && m < G::kCopies && more) issue_one(slot, m);
+                if (h == 1 && m == kMfma - 1 && more) advance();
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -331,7 +355,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     wait_vmem<0>();
     block_barrier();
 #pragma unroll
-    for (int i = 0; i < 6; ++i) read_frag(0, 0, i);
+    for (int i = 0; i < kFrags; ++i) read_frag(0, 0, i);
     for (;;) {
         // the slot behind the three stages that have landed; the row numbers
         // behind the chunk that the copies are in (the first)
@@ -345,7 +369,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+            for (int y = 0; y < kYB; ++y)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.0f;
         for (int st = 0; st < cur.nk; ++st) stage(std::true_type{}, st);
@@ -356,12 +380,13 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         // group q, k = 8 q + 4 (l / 32) .. + 3.  128-byte rows of the output
         // go through the wave's own region (16-byte chunk c of row n at c ^
         // (n / 2 % 8)), so that whole lines leave.
-        uint8_t *const region = &lds[(slot == 0 ? kDepth - 1 : slot - 1) * kSlotBytes + wave * kRegion];
+        uint8_t *const region =
+            &lds[(G::kOwnRegions > 0 ? kDepth : slot == 0 ? kDepth - 1 : slot - 1) * G::kSlot + wave * kRegion];
         const int l32 = ln & 31, kh = ln >> 5, r8 = ln >> 3, c8 = ln & 7;
-        const int64_t n0 = (int64_t)cur.tn * kDwTile + wn * 128, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
+        const int64_t n0 = (int64_t)cur.tn * TN + wn * G::kWaveN, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
         auto place = [&](int row, int c) { return region + row * 128 + ((c ^ ((row >> 1) & 7)) << 4); };
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < kYB; ++y) {
             __builtin_amdgcn_sched_barrier(0);
             if (OUT == kOutBf16) {
                 if (a.add) {
@@ -412,8 +437,8 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
                     const int row = it * 8 + r8, col = x * 32 + c8 * 4;
                     if (OUT == kOutPartial) {
                         const int64_t tile = ((int64_t)cur.e * a.tiles_n + cur.tn) * a.tiles_k + cur.tk;
-                        float *const p = a.partials + (tile * a.slices + cur.slice) * (kDwTile * kDwTile);
-                        *reinterpret_cast<v4f *>(p + (wn * 128 + y * 32 + row) * kDwTile + wk * 64 + col) = v;
+                        float *const p = a.partials + (tile * a.slices + cur.slice) * (TN * kDwTile);
+                        *reinterpret_cast<v4f *>(p + (wn * G::kWaveN + y * 32 + row) * kDwTile + wk * 64 + col) = v;
                     } else {
                         const int64_t n = n0 + y * 32 + row, k = k0 + col;
                         if (n < a.N && k < a.K) {
@@ -459,21 +484,22 @@ __device__ __forceinline__ void store_chunk(const GroupedDwArgs &a, int e, int64
 
 // Sums the slices' partial tiles in their order: a workgroup per 16 rows of a
 // tile, eight columns of one row per thread and step.
-template <int OUT>
+template <int TN, int OUT>
 __global__ __launch_bounds__(256) void grouped_dw_reduce_kernel(const GroupedDwArgs a)
 {
-    const uint32_t tile = blockIdx.x >> 4;
+    constexpr uint32_t kParts = TN / 16;
+    const uint32_t tile = blockIdx.x / kParts;
     const uint32_t row = fdiv(tile, a.div_k), tk = tile - row * a.tiles_k;
     const uint32_t e = fdiv(row, a.div_n), tn = row - e * a.tiles_n;
-    const float *p = a.partials + (int64_t)tile * a.slices * (kDwTile * kDwTile);
+    const float *p = a.partials + (int64_t)tile * a.slices * (TN * kDwTile);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = (int)(blockIdx.x & 15u) * 16 + i * 8 + (int)(threadIdx.x >> 5), c = (int)(threadIdx.x & 31u) * 8;
-        const int64_t n = (int64_t)tn * kDwTile + r, k = (int64_t)tk * kDwTile + c;
+        const int r = (int)(blockIdx.x % kParts) * 16 + i * 8 + (int)(threadIdx.x >> 5), c = (int)(threadIdx.x & 31u) * 8;
+        const int64_t n = (int64_t)tn * TN + r, k = (int64_t)tk * kDwTile + c;
         if (n >= a.N || k >= a.K) continue;
         v4f lo = {}, hi = {};
         for (int s = 0; s < a.slices; ++s) {
-            const float *q = p + (int64_t)s * (kDwTile * kDwTile) + r * kDwTile + c;
+            const float *q = p + (int64_t)s * (TN * kDwTile) + r * kDwTile + c;
             lo += __builtin_nontemporal_load(reinterpret_cast<const v4f *>(q));
             hi += __builtin_nontemporal_load(reinterpret_cast<const v4f *>(q + 4));
         }
@@ -482,13 +508,31 @@ __global__ __launch_bounds__(256) void grouped_dw_reduce_kernel(const GroupedDwA
     }
 }
 
-template <int OUT>
+template <int TN, int OUT>
 hipError_t launch_out(const GroupedDwArgs &a, unsigned grid, hipStream_t s)
 {
     if (a.row_index)
-        grouped_dw_kernel<OUT, true><<<grid, kDwThreads, 0, s>>>(a);
+        grouped_dw_kernel<TN, OUT, true><<<grid, kDwThreads, 0, s>>>(a);
     else
-        grouped_dw_kernel<OUT, false><<<grid, kDwThreads, 0, s>>>(a);
+        grouped_dw_kernel<TN, OUT, false><<<grid, kDwThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int TN>
+hipError_t launch_tiles(const GroupedDwArgs &a, hipStream_t s)
+{
+    // one workgroup per compute unit (of the 256 of an MI355X), or as many on
+    // each XCD as it has tiles
+    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, most = (rows + 7) / 8 * a.tiles_k;
+    const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
+    if (a.slices == 1) return a.out_fp32 ? launch_out<TN, kOutFp32>(a, grid, s) : launch_out<TN, kOutBf16>(a, grid, s);
+    hipError_t e = launch_out<TN, kOutPartial>(a, grid, s);
+    if (e != hipSuccess) return e;
+    const unsigned parts = (unsigned)((int64_t)a.E * a.tiles_n * a.tiles_k * (TN / 16));
+    if (a.out_fp32)
+        grouped_dw_reduce_kernel<TN, kOutFp32><<<parts, 256, 0, s>>>(a);
+    else
+        grouped_dw_reduce_kernel<TN, kOutBf16><<<parts, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -496,19 +540,7 @@ hipError_t launch_out(const GroupedDwArgs &a, unsigned grid, hipStream_t s)
 
 hipError_t launch_grouped_dw(const GroupedDwArgs &a, hipStream_t s)
 {
-    // one workgroup per compute unit (of the 256 of an MI355X), or as many on
-    // each XCD as it has tiles
-    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, most = (rows + 7) / 8 * a.tiles_k;
-    const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
-    if (a.slices == 1) return a.out_fp32 ? launch_out<kOutFp32>(a, grid, s) : launch_out<kOutBf16>(a, grid, s);
-    hipError_t e = launch_out<kOutPartial>(a, grid, s);
-    if (e != hipSuccess) return e;
-    const unsigned parts = (unsigned)((int64_t)a.E * a.tiles_n * a.tiles_k * 16);
-    if (a.out_fp32)
-        grouped_dw_reduce_kernel<kOutFp32><<<parts, 256, 0, s>>>(a);
-    else
-        grouped_dw_reduce_kernel<kOutBf16><<<parts, 256, 0, s>>>(a);
-    return hipGetLastError();
+    return a.tile_n == 256 ? launch_tiles<256>(a, s) : launch_tiles<128>(a, s);
 }
 
 }  // namespace spg

@@ -117,6 +117,22 @@ def test_rows_in_slices(spg, R, N, K, E, dtype):
     run(spg, [R - 1, 1] + [0] * (E - 1) if E > 1 else [R], N, K, False, dtype, seed=R + 2)
 
 
+@pytest.mark.parametrize("gather", [False, True], ids=["in_order", "gathered"])
+@pytest.mark.parametrize("counts,N,K", [([40, 0, 1000, 33], 1800, 2056), ([300] * 150, 264, 248), ([5, 0] * 80, 264, 264),
+                                        ([0] * 70 + [2000] + [3] * 70, 256, 264), ([1100, 900] * 40, 520, 264)])
+def test_more_tiles_than_compute_units(spg, counts, N, K, gather):
+    # 256-row tiles, several a workgroup; experts without rows, shorter than the copies run ahead, and of several
+    # chunks of row numbers, next to each other in every order
+    run(spg, counts, N, K, gather, seed=N, tail=3, head=1)
+
+
+@pytest.mark.parametrize("last", [1, 33, 97, 129, 161, 1025, 1057, 1153])
+def test_chunks_of_row_numbers(spg, last):
+    # 1024 rows a chunk: tiles that end right behind a border, followed by others
+    for counts in ([last, 1024, 70], [1024 + last] * 3, [2048, last, 1, 1024]):
+        run(spg, counts, 1288, 4104, True, seed=last)
+
+
 def test_offsets_and_indices_out_of_range(spg):
     N, K, R, T = 256, 128, 64, 20
     dy, x = rand((R, N), 1), rand((T, K), 2)

@@ -50,7 +50,7 @@ DENSE = dict(rows=4096, x_rows=4096, experts=1)     # eight tiles, cut into slic
     (dict(stride_a=0), dict(add=at(5)), EINVAL), (dict(stride_a=2 ** 56), dict(add=at(5)), EUNSUP),
     (dict(rows=2 ** 31, x_rows=2 ** 31), {}, EUNSUP), (dict(x_rows=2 ** 31), {}, EUNSUP), (dict(N=2 ** 29), {}, EUNSUP),
     (dict(x_rows=1023), {}, EINVAL), (dict(x_rows=2 ** 22), dict(idx=at(4)), EUNSUP),
-    (dict(experts=65536, N=4096, K=4096), {}, EUNSUP),                                     # workgroups
+    (dict(experts=65536, N=2 ** 16, K=4096), {}, EUNSUP),                                  # tiles
     ({}, dict(out=None), EINVAL), ({}, dict(dy=None), EINVAL), ({}, dict(x=None), EINVAL), ({}, dict(off=None), EINVAL),
     ({}, dict(out=at(0, 8)), EINVAL), ({}, dict(dy=at(1, 8)), EINVAL), ({}, dict(x=at(2, 8)), EINVAL),
     ({}, dict(off=at(3, 2)), EINVAL), ({}, dict(idx=at(4, 2)), EINVAL), ({}, dict(add=at(5, 8)), EINVAL),
@@ -74,10 +74,11 @@ def test_workspace():
     f = lambda **kw: spg.lib.gemm_grouped_dw_workspace_bytes(ctypes.byref(desc(**kw)))  # noqa: E731
     tile = 256 * 256 * 4
     assert f() == 0 and f(N=516) == 0                       # 256 rows an expert; an invalid call
-    assert f(**DENSE) == 2 * 16 * tile                      # two tiles in sixteen parts
-    assert f(rows=4000, x_rows=4000, N=4096, K=2048, experts=1) == 128 * 2 * tile
-    assert f(rows=4000, x_rows=4000, N=4096, K=4096, experts=1) == 0
-    assert spg.grouped_dw_workspace(4096, 1, 512, 256, "cpu").numel() == 2 * 16 * tile
+    assert f(**DENSE) == 4 * 16 * tile // 2                 # four tiles of 128 x 256 in sixteen parts
+    assert f(rows=4000, x_rows=4000, N=2048, K=2048, experts=1) == 128 * 2 * tile // 2
+    assert f(rows=4000, x_rows=4000, N=4096, K=2048, experts=1) == 0
+    assert f(rows=4000, x_rows=4000, N=4096, K=2304, experts=1) == 0    # 144 tiles of 256 x 256
+    assert spg.grouped_dw_workspace(4096, 1, 512, 256, "cpu").numel() == 4 * 16 * tile // 2
     assert spg.grouped_dw_workspace(1024, 4, 512, 256, "cpu") is None
 
 
