@@ -132,7 +132,7 @@ __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, 
     return t;
 }
 
-template <int TN, int OUT, bool GATHER>
+template <int TN, int OUT, bool GATHER, bool ADD>
 __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_dw_kernel(
     const GroupedDwArgs a)
 {
@@ -374,78 +374,82 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
                 for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.0f;
         for (int st = 0; st < cur.nk; ++st) stage(std::true_type{}, st);
         for (int st = cur.nk; st < cur.np; ++st) stage(std::false_type{}, st);
-        wait_vmem<0>();
-
         // ---- epilogue: lane l of a block holds n = l % 32 and, per register
         // group q, k = 8 q + 4 (l / 32) .. + 3.  128-byte rows of the output
         // go through the wave's own region (16-byte chunk c of row n at c ^
-        // (n / 2 % 8)), so that whole lines leave.
-        uint8_t *const region =
-            &lds[(G::kOwnRegions > 0 ? kDepth : slot == 0 ? kDepth - 1 : slot - 1) * G::kSlot + wave * kRegion];
+        // (n / 2 % 8)), so that whole lines leave: passes of 32 n x 64 k (bf16)
+        // or x 32 k (fp32).  What is added is loaded a pass ahead (two passes
+        // ahead would spill registers).
         const int l32 = ln & 31, kh = ln >> 5, r8 = ln >> 3, c8 = ln & 7;
         const int64_t n0 = (int64_t)cur.tn * TN + wn * G::kWaveN, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
+        constexpr int kPasses = OUT == kOutBf16 ? kYB : 2 * kYB, kSize = OUT == kOutBf16 ? 2 : 4;
+        // element (pass row it * 8 + r8, 16-byte chunk c8): its n and k
+        auto row_of = [&](int p, int it) { return n0 + (OUT == kOutBf16 ? p : p >> 1) * 32 + it * 8 + r8; };
+        auto col_of = [&](int p) { return k0 + (OUT == kOutBf16 ? c8 * 8 : (p & 1) * 32 + c8 * 4); };
+        v4i ad[2][ADD ? 4 : 1];
+        auto load_add = [&](int p) {
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int64_t n = row_of(p, it), k = col_of(p);
+                const int64_t at = (int64_t)cur.e * a.stride_a + n * a.lda + k;
+                ad[p & 1][ADD ? it : 0] = v4i{0, 0, 0, 0};
+                if (n < a.N && k < a.K)
+                    ad[p & 1][ADD ? it : 0] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>((const uint8_t *)a.add + at * kSize));
+            }
+        };
+        if constexpr (ADD) load_add(0);
+        wait_vmem<0>();
+        uint8_t *const region =
+            &lds[(G::kOwnRegions > 0 ? kDepth : slot == 0 ? kDepth - 1 : slot - 1) * G::kSlot + wave * kRegion];
         auto place = [&](int row, int c) { return region + row * 128 + ((c ^ ((row >> 1) & 7)) << 4); };
 #pragma unroll
-        for (int y = 0; y < kYB; ++y) {
+        for (int p = 0; p < kPasses; ++p) {
             __builtin_amdgcn_sched_barrier(0);
-            if (OUT == kOutBf16) {
-                if (a.add) {
-                    const uint16_t *from = (const uint16_t *)a.add + (int64_t)cur.e * a.stride_a;
+            if constexpr (ADD)
+                if (p + 1 < kPasses) load_add(p + 1);
+            if constexpr (OUT == kOutBf16) {
+                if (ADD) {
 #pragma unroll
-                    for (int it = 0; it < 4; ++it) {
-                        const int64_t n = n0 + y * 32 + it * 8 + r8, k = k0 + c8 * 8;
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (n < a.N && k < a.K) v = *reinterpret_cast<const uint4 *>(from + n * a.lda + k);
-                        *reinterpret_cast<uint4 *>(place(it * 8 + r8, c8)) = v;
-                    }
+                    for (int it = 0; it < 4; ++it) *reinterpret_cast<v4i *>(place(it * 8 + r8, c8)) = ad[p & 1][ADD ? it : 0];
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint2 *const p = reinterpret_cast<uint2 *>(place(l32, x * 4 + q) + kh * 8);
+                        uint2 *const at = reinterpret_cast<uint2 *>(place(l32, x * 4 + q) + kh * 8);
                         float v[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = acc[x][y][4 * q + i];
-                        if (a.add) {
-                            const uint2 r = *p;
+                        for (int i = 0; i < 4; ++i) v[i] = acc[x][p][4 * q + i];
+                        if (ADD) {
+                            const uint2 r = *at;
                             v[0] += bf16_lo(r.x);
                             v[1] += bf16_hi(r.x);
                             v[2] += bf16_lo(r.y);
                             v[3] += bf16_hi(r.y);
                         }
-                        *p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                        *at = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
                     }
-                uint16_t *const to = (uint16_t *)a.out + (int64_t)cur.e * a.stride_o;
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const v4i v = *reinterpret_cast<const v4i *>(place(it * 8 + r8, c8));
-                    const int64_t n = n0 + y * 32 + it * 8 + r8, k = k0 + c8 * 8;
-                    if (n < a.N && k < a.K) __builtin_nontemporal_store(v, reinterpret_cast<v4i *>(to + n * a.ldo + k));
-                }
-                continue;
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     *reinterpret_cast<v4f *>(place(l32, q * 2 + kh)) =
-                        v4f{acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2], acc[x][y][4 * q + 3]};
+                        v4f{acc[p & 1][p >> 1][4 * q], acc[p & 1][p >> 1][4 * q + 1], acc[p & 1][p >> 1][4 * q + 2],
+                            acc[p & 1][p >> 1][4 * q + 3]};
+            }
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    v4f v = *reinterpret_cast<const v4f *>(place(it * 8 + r8, c8));
-                    const int row = it * 8 + r8, col = x * 32 + c8 * 4;
-                    if (OUT == kOutPartial) {
-                        const int64_t tile = ((int64_t)cur.e * a.tiles_n + cur.tn) * a.tiles_k + cur.tk;
-                        float *const p = a.partials + (tile * a.slices + cur.slice) * (TN * kDwTile);
-                        *reinterpret_cast<v4f *>(p + (wn * G::kWaveN + y * 32 + row) * kDwTile + wk * 64 + col) = v;
-                    } else {
-                        const int64_t n = n0 + y * 32 + row, k = k0 + col;
-                        if (n < a.N && k < a.K) {
-                            if (a.add) v += *reinterpret_cast<const v4f *>((const float *)a.add + cur.e * a.stride_a + n * a.lda + k);
-                            __builtin_nontemporal_store(v, reinterpret_cast<v4f *>((float *)a.out + cur.e * a.stride_o + n * a.ldo + k));
-                        }
-                    }
+            for (int it = 0; it < 4; ++it) {
+                v4i v = *reinterpret_cast<const v4i *>(place(it * 8 + r8, c8));
+                const int64_t n = row_of(p, it), k = col_of(p);
+                if constexpr (OUT == kOutPartial) {
+                    const int64_t tile = ((int64_t)cur.e * a.tiles_n + cur.tn) * a.tiles_k + cur.tk;
+                    float *const to = a.partials + (tile * a.slices + cur.slice) * (TN * kDwTile);
+                    *reinterpret_cast<v4i *>(to + (n - (int64_t)cur.tn * TN) * kDwTile + (k - (int64_t)cur.tk * kDwTile)) = v;
+                } else {
+                    if (n >= a.N || k >= a.K) continue;
+                    if (OUT == kOutFp32 && ADD)
+                        v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + __builtin_bit_cast(v4f, ad[p & 1][ADD ? it : 0]));
+                    const int64_t at = (int64_t)cur.e * a.stride_o + n * a.ldo + k;
+                    __builtin_nontemporal_store(v, reinterpret_cast<v4i *>((uint8_t *)a.out + at * kSize));
                 }
             }
         }
@@ -511,10 +515,19 @@ __global__ __launch_bounds__(256) void grouped_dw_reduce_kernel(const GroupedDwA
 template <int TN, int OUT>
 hipError_t launch_out(const GroupedDwArgs &a, unsigned grid, hipStream_t s)
 {
+    if constexpr (OUT != kOutPartial) {
+        if (a.add) {
+            if (a.row_index)
+                grouped_dw_kernel<TN, OUT, true, true><<<grid, kDwThreads, 0, s>>>(a);
+            else
+                grouped_dw_kernel<TN, OUT, false, true><<<grid, kDwThreads, 0, s>>>(a);
+            return hipGetLastError();
+        }
+    }
     if (a.row_index)
-        grouped_dw_kernel<TN, OUT, true><<<grid, kDwThreads, 0, s>>>(a);
+        grouped_dw_kernel<TN, OUT, true, false><<<grid, kDwThreads, 0, s>>>(a);
     else
-        grouped_dw_kernel<TN, OUT, false><<<grid, kDwThreads, 0, s>>>(a);
+        grouped_dw_kernel<TN, OUT, false, false><<<grid, kDwThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
