@@ -96,7 +96,7 @@ SPG_EXPORT size_t rms_norm_backward_workspace_bytes(int64_t R, int64_t H)
 {
     if (validate_norm_size(R, H) != SPG_OK || R == 0) return 0;
     const int64_t parts = norm_grad_parts(R, H);
-    return parts > 1 ? (size_t)parts * (size_t)H * sizeof(float) : 0;
+    return parts > 1 ? (size_t)parts * (size_t)norm_grad_width(H) * sizeof(float) : 0;
 }
 
 SPG_EXPORT int rms_norm_backward(const void *grad_out, const void *h, const void *grad_residual, const void *weight,

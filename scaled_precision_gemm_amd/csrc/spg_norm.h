@@ -28,13 +28,14 @@ struct NormGradArgs {
     const float *rstd;                       // [R]
     uint16_t *dx;                            // [R, H], lddx
     float *dw;                               // [H] or null
-    float *partials;                         // [norm_grad_parts, H] where there is more than one
+    float *partials;                         // [norm_grad_parts, norm_grad_width] where there is more than one
     int64_t R, H, lddy, ldh, lddr, lddx;
     float w0;
     int32_t w32;
 };
 // Workgroups of the gradient's launch, each with a partial sum of dw.
 int64_t norm_grad_parts(int64_t R, int64_t H);
+int64_t norm_grad_width(int64_t H);            // floats of a partial sum, at least H
 hipError_t launch_rms_norm_backward(const NormGradArgs &a, hipStream_t s);
 
 }  // namespace spg

@@ -199,12 +199,19 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
                 hv[u][v] = pack8(f);
             }
     }
+    // the weights' round trip: in front of the sum for short rows, whose time
+    // is latency; behind it for others, where their registers hold more waves
+    // back than the trip costs
+    constexpr bool EARLY = U * V == 1;
     float w[V][8];
+    auto load_weights = [&]() {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int col = (t + v * TEAM) * 8;
-        weights8(a.weight, a.w32, a.w0, col, H - col, w[v]);
-    }
+        for (int v = 0; v < V; ++v) {
+            const int col = (t + v * TEAM) * 8;
+            weights8(a.weight, a.w32, a.w0, col, H - col, w[v]);
+        }
+    };
+    if (EARLY) load_weights();
     double ss[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -216,6 +223,10 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss[u] = __builtin_fma((double)f[i], (double)f[i], ss[u]);
         }
+    }
+    if (!EARLY) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_weights();
     }
     team_fold<TEAM>(ss, lds_sum, [](double p, double q) { return p + q; });
     float rstd[U];
@@ -301,144 +312,185 @@ hipError_t launch_team(const NormArgs &a, hipStream_t s)
 //   dx = rstd (g - xh m) + dres        one rounding to bf16
 //   dw = sum over the rows of dy xh    fp32
 //
-// A workgroup walks over rows blockIdx.x, + gridDim.x, ...; a lane keeps its
-// columns' weights and sums of dw in registers, and the next row's loads are
-// in flight while this row is summed.  Every workgroup leaves one partial sum
-// of dw, which a second launch adds in the workgroups' order.
-template <int TEAM, int V>
+// A workgroup walks over rows, U a team at once (all of their loads in flight
+// before the first product); a lane keeps its columns' weights and sums of dw
+// in registers.  Every workgroup leaves one partial sum of dw, which a second
+// launch adds in the workgroups' order.  Partial sums lie as the lanes hold
+// them: element i of vector t + TEAM v at (i V + v) TEAM + t.
+template <int TEAM, int V, int U>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_backward_kernel(const NormGradArgs a)
 {
-    constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM;
-    __shared__ float lds_sum[2][THREADS / 64][1];
-    __shared__ float lds_dw[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? TEAM * V * 8 : 1];
+    constexpr int THREADS = TEAM < 256 ? 256 : TEAM, TEAMS = THREADS / TEAM, WIDTH = TEAM * V * 8;
+    __shared__ float lds_sum[2][THREADS / 64][U];
+    __shared__ float lds_dw[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? WIDTH : 1];
     const int t = (int)threadIdx.x % TEAM, team = (int)threadIdx.x / TEAM;
     const int H = (int)a.H;
-    float w[V][8], dw[V][8];
+    // (the longest rows' weights would not fit beside the rest: read again per row)
+    constexpr bool KEEP = TEAM * V < 4096;
+    float w[KEEP ? V : 1][8], dw[V][8];
+    auto weights = [&](int v) {
+        const int col = (t + v * TEAM) * 8;
+        weights8(a.weight, a.w32, a.w0, col, H - col, w[KEEP ? v : 0]);
+    };
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int col = (t + v * TEAM) * 8;
-        weights8(a.weight, a.w32, a.w0, col, H - col, w[v]);
+        if (KEEP) weights(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
     }
-    uint4 nd[V], nh[V], nr[V];
-    float ns = 0.0f;
-    auto fetch = [&](int64_t row) {
+    int parity = 0;
+    for (int64_t first = (int64_t)blockIdx.x * (TEAMS * U); first < a.R; first += (int64_t)gridDim.x * (TEAMS * U), parity ^= 1) {
+        uint4 cd[U][V], ch[U][V], cr[U][V];
+        float rstd[U], dot[U];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (t + v * TEAM) * 8;
-            nd[v] = nh[v] = nr[v] = make_uint4(0, 0, 0, 0);
-            if (row < a.R && col < H) {
-                nd[v] = load8(a.dy + row * a.lddy + col, H - col);
-                nh[v] = load8(a.h + row * a.ldh + col, H - col);
-                if (a.dres) nr[v] = load8(a.dres + row * a.lddr + col, H - col);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = first + team + u * TEAMS;
+            rstd[u] = row < a.R ? a.rstd[row] : 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int col = (t + v * TEAM) * 8;
+                cd[u][v] = ch[u][v] = cr[u][v] = make_uint4(0, 0, 0, 0);
+                if (row < a.R && col < H) {
+                    cd[u][v] = load8(a.dy + row * a.lddy + col, H - col);
+                    ch[u][v] = load8(a.h + row * a.ldh + col, H - col);
+                    if (a.dres) cr[u][v] = load8(a.dres + row * a.lddr + col, H - col);
+                }
             }
         }
-        ns = row < a.R ? a.rstd[row] : 0.0f;
-    };
-    const int64_t step = (int64_t)gridDim.x * TEAMS;
-    fetch((int64_t)blockIdx.x * TEAMS + team);
-    int parity = 0;
-    for (int64_t first = (int64_t)blockIdx.x * TEAMS; first < a.R; first += step, parity ^= 1) {
-        const int64_t row = first + team;
-        uint4 cd[V], ch[V], cr[V];
-        const float rstd = ns;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            cd[v] = nd[v];
-            ch[v] = nh[v];
-            cr[v] = nr[v];
-        }
-        fetch(row + step);
-        float dot[1] = {0.0f};
+        for (int u = 0; u < U; ++u) {
+            dot[u] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float d[8], h[8];
-            unpack8(cd[v], d);
-            unpack8(ch[v], h);
+            for (int v = 0; v < V; ++v) {
+                float d[8], h[8];
+                unpack8(cd[u][v], d);
+                unpack8(ch[u][v], h);
+                if (!KEEP) weights(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = d[i] * (h[i] * rstd);
-                dot[0] = __builtin_fmaf(p, w[v][i], dot[0]);
-                dw[v][i] += p;
+                for (int i = 0; i < 8; ++i) {
+                    const float p = d[i] * (h[i] * rstd[u]);
+                    dot[u] = __builtin_fmaf(p, w[KEEP ? v : 0][i], dot[u]);
+                    dw[v][i] += p;
+                }
             }
         }
         team_fold<TEAM>(dot, lds_sum[parity], [](float p, float q) { return p + q; });
-        const float m = dot[0] / (float)H;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (t + v * TEAM) * 8;
-            float d[8], h[8], r[8];
-            unpack8(cd[v], d);
-            unpack8(ch[v], h);
-            unpack8(cr[v], r);
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = first + team + u * TEAMS;
+            const float m = dot[u] / (float)H;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = __builtin_fmaf(__builtin_fmaf(-(h[i] * rstd), m, d[i] * w[v][i]), rstd, r[i]);
-            if (row < a.R && col < H) store8(a.dx + row * a.lddx + col, pack8(r), H - col);
+            for (int v = 0; v < V; ++v) {
+                const int col = (t + v * TEAM) * 8;
+                float d[8], h[8], r[8];
+                unpack8(cd[u][v], d);
+                unpack8(ch[u][v], h);
+                unpack8(cr[u][v], r);
+                if (!KEEP) weights(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    r[i] = __builtin_fmaf(__builtin_fmaf(-(h[i] * rstd[u]), m, d[i] * w[KEEP ? v : 0][i]), rstd[u], r[i]);
+                if (row < a.R && col < H) store8(a.dx + row * a.lddx + col, pack8(r), H - col);
+            }
         }
     }
     if (!a.dw) return;
-    float *out = gridDim.x > 1 ? a.partials + (int64_t)blockIdx.x * a.H : a.dw;
+    // one workgroup: its sums are the result
+    float *const part = a.partials + (int64_t)blockIdx.x * WIDTH;
+    auto leave = [&](int at, float s) {
+        if (gridDim.x > 1)
+            part[at] = s;
+        else if (const int col = (at % (TEAM * V)) * 8 + at / (TEAM * V); col < H)
+            a.dw[col] = s;
+    };
     if constexpr (TEAMS > 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) lds_dw[team][(t + v * TEAM) * 8 + i] = dw[v][i];
+            for (int i = 0; i < 8; ++i) lds_dw[team][(i * V + v) * TEAM + t] = dw[v][i];
         __syncthreads();
-        for (int c = (int)threadIdx.x; c < H; c += THREADS) {
-            float s = lds_dw[0][c];
-            for (int k = 1; k < TEAMS; ++k) s += lds_dw[k][c];
-            out[c] = s;
+        for (int at = (int)threadIdx.x; at < WIDTH; at += THREADS) {
+            float s = lds_dw[0][at];
+            for (int k = 1; k < TEAMS; ++k) s += lds_dw[k][at];
+            leave(at, s);
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int col = (t + v * TEAM) * 8;
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < H) out[col + i] = dw[v][i];
-        }
+            for (int i = 0; i < 8; ++i) leave((i * V + v) * TEAM + t, dw[v][i]);
     }
 }
 
-// dw[c] = sum of the partial sums [parts, H]: 32 columns a workgroup, eight
-// runs of parts side by side, joined in order.
-__global__ __launch_bounds__(256) void norm_dw_reduce_kernel(const float *partials, int parts, int64_t H, float *dw)
+// Sum of the partial sums [parts, width]: 16 places a workgroup, 64 runs of at
+// most kRun parts side by side (each run's loads all in flight), joined eight by
+// eight in order.
+constexpr int kRun = 8;
+__global__ __launch_bounds__(1024) void norm_dw_reduce_kernel(const float *partials, int parts, int width, int64_t H, float *dw)
 {
-    __shared__ float lds[8][32];
-    const int c = (int)threadIdx.x & 31, k = (int)threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 32 + c;
-    const int per = (parts + 7) / 8, end = min(parts, (k + 1) * per);
+    __shared__ float lds[64][16], lds8[8][16];
+    const int c = (int)threadIdx.x & 15, k = (int)threadIdx.x >> 4;
+    const int at = (int)blockIdx.x * 16 + c;
+    const int per = (parts + 63) / 64;
     float s = 0.0f;
-    if (col < H)
-        for (int p = k * per; p < end; ++p) s += partials[(int64_t)p * H + col];
+    for (int p0 = 0; p0 < per; p0 += kRun) {
+        float v[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int p = k * per + p0 + i;
+            v[i] = p0 + i < per && p < parts ? partials[(int64_t)p * width + at] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) s += v[i];
+    }
     lds[k][c] = s;
     __syncthreads();
-    if (k == 0 && col < H) {
-        for (int i = 1; i < 8; ++i) s += lds[i][c];
-        dw[col] = s;
+    if (k < 8) {
+        s = lds[8 * k][c];
+        for (int i = 1; i < 8; ++i) s += lds[8 * k + i][c];
+        lds8[k][c] = s;
+    }
+    __syncthreads();
+    if (k == 0) {
+        s = lds8[0][c];
+        for (int i = 1; i < 8; ++i) s += lds8[i][c];
+        const int vecs = width / 8, col = (at % vecs) * 8 + at / vecs;
+        if (col < H) dw[col] = s;
     }
 }
 
 constexpr int64_t kGradWorkgroups = 512;
 
-int grad_team(int64_t H) { return H <= 512 ? 16 : H <= 2048 ? 64 : H <= 8192 ? 256 : 1024; }
-
-template <int TEAM, int V>
-hipError_t launch_grad(const NormGradArgs &a, hipStream_t s)
+// Calls f(team, vectors, rows at once) for rows of H elements.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+auto with_grad_shape(int64_t H, F &&f)
 {
-    rms_norm_backward_kernel<TEAM, V><<<(unsigned)norm_grad_parts(a.R, a.H), TEAM < 256 ? 256 : TEAM, 0, s>>>(a);
-    return hipGetLastError();
+    if (H <= 128) return f(Int<16>{}, Int<1>{}, Int<4>{});
+    if (H <= 256) return f(Int<16>{}, Int<2>{}, Int<2>{});
+    if (H <= 512) return f(Int<16>{}, Int<4>{}, Int<2>{});
+    if (H <= 1024) return f(Int<64>{}, Int<2>{}, Int<2>{});
+    if (H <= 2048) return f(Int<64>{}, Int<4>{}, Int<2>{});
+    if (H <= 4096) return f(Int<256>{}, Int<2>{}, Int<2>{});
+    if (H <= 6144) return f(Int<256>{}, Int<3>{}, Int<2>{});
+    if (H <= 8192) return f(Int<256>{}, Int<4>{}, Int<2>{});
+    if (H <= 16384) return f(Int<1024>{}, Int<2>{}, Int<1>{});
+    return f(Int<1024>{}, Int<4>{}, Int<1>{});
 }
 
 }  // namespace
 
 int64_t norm_grad_parts(int64_t R, int64_t H)
 {
-    const int team = grad_team(H), teams = team < 256 ? 256 / team : 1;
-    const int64_t n = (R + teams - 1) / teams;
+    const int64_t rows = with_grad_shape(H, [](auto team, auto, auto u) { return (team < 256 ? 256 / team : 1) * u; });
+    const int64_t n = (R + rows - 1) / rows;
     return n < 1 ? 1 : n < kGradWorkgroups ? n : kGradWorkgroups;     // no rows: one, which writes zeros
+}
+
+int64_t norm_grad_width(int64_t H)
+{
+    return with_grad_shape(H, [](auto team, auto v, auto) { return 8 * team * v; });
 }
 
 hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
@@ -460,24 +512,17 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
 
 hipError_t launch_rms_norm_backward(const NormGradArgs &a, hipStream_t s)
 {
-    const int64_t H = a.H;
-    const hipError_t e = H <= 128     ? launch_grad<16, 1>(a, s)
-                         : H <= 256   ? launch_grad<16, 2>(a, s)
-                         : H <= 512   ? launch_grad<16, 4>(a, s)
-                         : H <= 1024  ? launch_grad<64, 2>(a, s)
-                         : H <= 2048  ? launch_grad<64, 4>(a, s)
-                         : H <= 4096  ? launch_grad<256, 2>(a, s)
-                         : H <= 6144  ? launch_grad<256, 3>(a, s)
-                         : H <= 8192  ? launch_grad<256, 4>(a, s)
-                         : H <= 16384 ? launch_grad<1024, 2>(a, s)
-                                      : launch_grad<1024, 4>(a, s);
-    if (e != hipSuccess || !a.dw) return e;
     const int64_t parts = norm_grad_parts(a.R, a.H);
-    if (parts > 1) {
-        norm_dw_reduce_kernel<<<(unsigned)((H + 31) / 32), 256, 0, s>>>(a.partials, (int)parts, H, a.dw);
+    const hipError_t e = with_grad_shape(a.H, [&](auto team, auto v, auto u) {
+        constexpr int TEAM = decltype(team)::value;
+        rms_norm_backward_kernel<TEAM, decltype(v)::value, decltype(u)::value>
+            <<<(unsigned)parts, TEAM < 256 ? 256 : TEAM, 0, s>>>(a);
         return hipGetLastError();
-    }
-    return hipSuccess;
+    });
+    if (e != hipSuccess || !a.dw || parts == 1) return e;
+    const int64_t width = norm_grad_width(a.H);
+    norm_dw_reduce_kernel<<<(unsigned)(width / 16), 1024, 0, s>>>(a.partials, (int)parts, (int)width, a.H, a.dw);
+    return hipGetLastError();
 }
 
 }  // namespace spg
