@@ -12,6 +12,7 @@ from __future__ import annotations
 import array
 import collections
 import ctypes
+import itertools
 import math
 import os
 
@@ -1041,6 +1042,11 @@ def _like(name, t, shape, dt, dev):
         _need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
 
 
+def _new_like(x, dtype=None):
+    """A contiguous tensor of x's shape on its device."""
+    return x.new_empty(x.shape, dtype=dtype)
+
+
 def _norm_weight(weight, H, dev):
     _need(isinstance(weight, torch.Tensor) and weight.dtype in (torch.bfloat16, torch.float32) and weight.device == dev
           and tuple(weight.shape) == (H,) and weight.is_contiguous(),
@@ -1100,16 +1106,19 @@ def rms_norm(x, weight, residual=None, output="bf16", eps=1e-6, weight_offset=0.
     given = isinstance(normed, torch.Tensor)
     d, coded, want = _checked(("norm", _sig(x), _sig(weight), _sig(residual), output, eps, weight_offset,
                                _sig(normed) if given else bool(normed), _sig(out), _sig(scale), _sig(h)), check)
+    # (empty_like takes 1.2 us of host time where new_empty takes 1.8; on a
+    # contiguous tensor both are contiguous)
+    like = torch.empty_like if x.is_contiguous() else _new_like
     if h is None and residual is not None:
-        h = x.new_empty(x.shape)
+        h = like(x)
     if coded:
         if out is None:
-            out = x.new_empty(x.shape, dtype=torch.uint8)
+            out = like(x, dtype=torch.uint8)
         if scale is None:
             scale = x.new_empty(want, dtype=torch.float32)
-        n = normed if given else x.new_empty(x.shape) if normed else None
+        n = normed if given else like(x) if normed else None
     else:
-        n = out = x.new_empty(x.shape) if out is None else out
+        n = out = like(x) if out is None else out
     r = x.new_empty((d.R,), dtype=torch.float32) if rstd else None
     if d.R > 0:
         _run(lib.rms_norm, "rms_norm", x, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(h), _ptr(n),
@@ -1156,7 +1165,7 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offs
     d, nws = _checked(("norm backward", _sig(grad_out), _sig(h), _sig(weight), _sig(rstd), _sig(grad_residual),
                        weight_offset, _sig(grad_x), grad_weight), check)
     if grad_x is None:
-        grad_x = grad_out.new_empty(grad_out.shape)
+        grad_x = (torch.empty_like if grad_out.is_contiguous() else _new_like)(grad_out)
     ws = _order_ws(workspace, nws, grad_out)
     gw = grad_out.new_empty((d.H,), dtype=torch.float32) if grad_weight else None
     if d.R > 0 or grad_weight:
@@ -1172,30 +1181,41 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offs
 _GRAD_TYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+def _gradient_fields(name, ts):
+    """Addresses, elements and types of a list of tensors, and its first
+    tensor.  Every check reads one property of all tensors (a list of 200 takes
+    a quarter of the time that it takes with a tensor's checks side by side)."""
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} {i} must be a tensor")
+    kinds = [_GRAD_TYPE.get(t.dtype) for t in ts]
+    ok = [t.is_contiguous() for t in ts]
+    _need(None not in kinds and all(ok), f"every {name} must be a contiguous fp32 or bf16 tensor")
+    dev = ts[0].device
+    index = {t.get_device() for t in ts}
+    _need(len(index) == 1 and (index != {-1} or all([t.device == dev for t in ts])), f"every {name} must be on {dev}")
+    return [t.data_ptr() for t in ts], [t.numel() for t in ts], kinds, ts[0]
+
+
 def _gradient_list(grads, out):
     """The C ABI's list (src, dst, elements, bf16) of the tensors and the
     first of them; None stands for a parameter without a gradient."""
     _need(isinstance(grads, (list, tuple)), "gradients must be a list or tuple of tensors")
     _need(out is None or isinstance(out, (list, tuple)) and len(out) == len(grads), "out must hold a tensor for each gradient")
-    rows, first, dev = array.array("q"), None, -1
-    for i, g in enumerate(grads):
-        o = g if out is None else out[i]
-        if g is None:
-            _need(o is None, f"gradient {i} is None and its output is not")
-            continue
-        _need(isinstance(g, torch.Tensor), f"gradient {i} must be a tensor")
-        kind = _GRAD_TYPE.get(g.dtype)
-        _need(kind is not None and g.is_contiguous(), f"gradient {i} must be a contiguous fp32 or bf16 tensor")
-        if first is None:
-            first, dev = g, g.device
-        _need(g.device == dev, f"gradient {i} must be on {dev}")
-        if o is not g:
-            _need(isinstance(o, torch.Tensor) and o.dtype == g.dtype and o.device == dev and o.shape == g.shape
-                  and o.is_contiguous(), f"output {i} must be a contiguous {g.dtype} {tuple(g.shape)} tensor on {dev}")
-        rows.extend((g.data_ptr(), o.data_ptr(), g.numel(), kind))
-    _need(first is not None, "at least one gradient")
+    if any([g is None for g in grads]):
+        if out is not None:
+            _need(all([(g is None) == (o is None) for g, o in zip(grads, out)]), "an output is None where its gradient is")
+            out = [o for o in out if o is not None]
+        grads = [g for g in grads if g is not None]
+    _need(len(grads) > 0, "at least one gradient")
+    src, n, kinds, first = _gradient_fields("gradient", grads)
+    dst = src
+    if out is not None:
+        dst, m, okinds, ofirst = _gradient_fields("output", out)
+        _need(m == n and okinds == kinds and ofirst.device == first.device,
+              f"outputs must have their gradients' elements and types, on {first.device}")
     _need(first.is_cuda, "gradients must be CUDA tensors")
-    return rows, first
+    return array.array("q", itertools.chain.from_iterable(zip(src, dst, n, kinds))), first
 
 
 def _gradients(fn, what, grads, out, workspace, *more):
@@ -1217,7 +1237,7 @@ def gradient_norm(grads, workspace=None):
 
 def clip_gradients(grads, max_norm, out=None, workspace=None):
     """Scales the tensors of the list `grads` in place (or into the tensors of
-    the list `out`, alike in shape and type) by max_norm / norm where their
+    the list `out`, of the same types and numbers of elements) by max_norm / norm where their
     norm, as gradient_norm gives it, is over max_norm; returns the norm before,
     fp32 [1] on their device.  Where the norm is not finite the gradients stay
     as they are.  The tensors must not share memory."""

@@ -180,9 +180,7 @@ __device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float
 __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable t, const float *factor)
 {
     const float f = *factor;
-    const uint32_t chunks = t.first[t.count];
-    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-        const uint32_t c = chunks - 1 - k;
+    for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const int i = find_tensor(t, c);
         if (f == 1.0f && t.src[i] == t.dst[i]) continue;        // nothing changes
         const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
