@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     using G = DwGeometry<TN>;
     constexpr int kIndexAt = kDepth * G::kSlot + G::kOwnRegions;
     __shared__ __attribute__((aligned(2048))) uint8_t lds[kIndexAt + (GATHER ? kDwWaves * 2 * kIndexBytes : 0)];
-    constexpr int kMin = GATHER ? 6 : 3;
+    constexpr int kMin = GATHER ? 7 : 3;                          // (gathered: so that plan() need not wait)
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), ln = lane_id();
     const int wn = wave >> 2, wk = wave & 3;                      // TN / 2 n, 64 k of the tile
     const uint32_t lds_base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t *)&lds[0];
@@ -194,7 +194,9 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     const uint32_t index_at = lds_base + (uint32_t)(kIndexAt + wave * 2 * kIndexBytes);
     // row numbers of chunk c of a tile's rows into buffer buf: each wave those
     // of its own rows, read back by itself.  `since` counts the stages copied
-    // after them: from the third on, the pipeline's waits have seen them land.
+    // after them.  A stage's copies are planned ahead of its own wait: four
+    // stages after, the waits of the stages before have seen the row numbers
+    // land (the first two stages of a tile have none); sooner, plan() waits.
     int since = 0;
     auto copy_indices = [&](int64_t r0, int64_t r1, int c, int buf) {
         const int64_t first = r0 + (int64_t)c * (kChunkStages * kStageRows);
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     auto plan = [&]() {
         const bool border = cp.left == 0, chunk = cp.at > 0 && cp.at % kChunkStages == 0;
         if (GATHER && (border || chunk)) {
-            if (since < 3) wait_vmem<0>();
+            if (since < 4) wait_vmem<0>();
             cp.buf ^= 1;
         }
         if (border) copy_tile(nxt);
