@@ -318,6 +318,24 @@ def test_gradients_against_differences(spg):
         assert abs(d - (gw.double() * u).sum()) <= (128 * HALF * A * u.abs()).sum() + 1e-6
 
 
+def test_past_32_bits(spg):
+    # rows past 2^32 bytes and 2^31 elements in every tensor
+    R, H = 280000, 8192
+    x, w = torch.zeros((R, H), dtype=BF, device="cuda"), rand((H,), 1)
+    some = [0, 1, 131071, 131072, 262143, 262144, R - 1]
+    x[some] = rand((len(some), H), 2)
+    h, rstd, y = ref_forward(x[some], w, x[some])
+    g = spg.rms_norm(x, w, residual=x, output="e4m3_block128", normed=True, rstd=True)
+    assert torch.equal(g.h[some], h)
+    check_bf16(g.normed[some], y)
+    check_codes(spg, g.out[some], g.scale[:, some].contiguous(), y, "e4m3_block128")
+    gx, gw = spg.rms_norm_backward(x, g.h, w, g.rstd)
+    rd = g.rstd[some].double()
+    check_grads(gx[some], None, ref_backward(x[some], h, w, rd), R)
+    want, A = ref_backward(x[some], h, w, rd)[2:]
+    assert bool(((gw.double() - want).abs() <= 96 * HALF * A).all())
+
+
 # ---- streams, graphs -----------------------------------------------------------------
 
 def test_captured_and_replayed(spg):
