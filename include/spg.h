@@ -655,7 +655,7 @@ int rms_norm_backward(const void *grad_out, const void *h, const void *grad_resi
  * each time; clip_gradients refuses tensors whose memory overlaps (SPG_EINVAL),
  * norm and ws overlap nothing.  Sums in an order that the sizes alone decide.  At
  * most 2^24 tensors of less than 2^44 elements.  One launch per 120 tensors for
- * the sums and for the scaling, and one between.
+ * the sums and for the scaling, and beyond some 8 million elements one between.
  */
 typedef struct spg_gradient {
     const void *src;

@@ -14,6 +14,7 @@ import collections
 import ctypes
 import itertools
 import math
+import operator
 import os
 
 import torch
@@ -1181,20 +1182,20 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offs
 _GRAD_TYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _gradient_fields(name, ts):
     """Addresses, elements and types of a list of tensors, and its first
     tensor.  Every check reads one property of all tensors (a list of 200 takes
-    a quarter of the time that it takes with a tensor's checks side by side)."""
-    for i, t in enumerate(ts):
-        if not isinstance(t, torch.Tensor):
-            raise ValueError(f"{name} {i} must be a tensor")
-    kinds = [_GRAD_TYPE.get(t.dtype) for t in ts]
-    ok = [t.is_contiguous() for t in ts]
-    _need(None not in kinds and all(ok), f"every {name} must be a contiguous fp32 or bf16 tensor")
-    dev = ts[0].device
-    index = {t.get_device() for t in ts}
+    a third of the time that it takes with a tensor's checks side by side)."""
+    T = torch.Tensor
+    _need(all([issubclass(t, T) for t in set(map(type, ts))]), f"every {name} must be a tensor")
+    kinds = list(map(_GRAD_TYPE.get, map(_dtype_of, ts)))
+    _need(None not in kinds and all(map(T.is_contiguous, ts)), f"every {name} must be a contiguous fp32 or bf16 tensor")
+    dev, index = ts[0].device, set(map(T.get_device, ts))
     _need(len(index) == 1 and (index != {-1} or all([t.device == dev for t in ts])), f"every {name} must be on {dev}")
-    return [t.data_ptr() for t in ts], [t.numel() for t in ts], kinds, ts[0]
+    return list(map(T.data_ptr, ts)), list(map(T.numel, ts)), kinds, ts[0]
 
 
 def _gradient_list(grads, out):

@@ -291,6 +291,9 @@ SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const i
     a.stride_o = d->stride_o;
     a.E = d->experts;
     a.out_fp32 = d->out_fp32 != 0;
+    const int64_t line = d->out_fp32 ? 32 : 64;
+    a.lines = ((uintptr_t)out & 127u) == 0 && d->ldo % line == 0 && d->stride_o % line == 0 &&
+              (!add || (((uintptr_t)add & 127u) == 0 && d->lda % line == 0 && d->stride_a % line == 0));
     const DwPlan p = dw_plan(d);
     a.slices = p.slices;
     a.tile_n = p.tile_n;

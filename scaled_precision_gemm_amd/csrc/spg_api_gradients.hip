@@ -38,7 +38,7 @@ int64_t bytes_of(const spg_gradient &g) { return g.n * (g.bf16 ? 2 : 4); }
 template <typename F>
 int each_launch(const spg_gradient *list, int64_t count, F &&f)
 {
-    GradTable t;
+    GradTensors t;
     t.count = 0;
     t.first[0] = 0;
     for (int64_t i = 0; i < count; ++i) {
@@ -62,7 +62,7 @@ int each_launch(const spg_gradient *list, int64_t count, F &&f)
 int64_t all_parts(const spg_gradient *list, int64_t count)
 {
     int64_t parts = 0;
-    each_launch(list, count, [&](const GradTable &t) {
+    each_launch(list, count, [&](const GradTensors &t) {
         parts += grad_parts(t.first[t.count]);
         return (int)SPG_OK;
     });
@@ -125,16 +125,19 @@ int run_gradients(const spg_gradient *list, int64_t count, bool clip, double max
     double *const partials = (double *)((uint8_t *)ws + kHead);
     const hipStream_t s = (hipStream_t)stream;
     int64_t at = 0;
-    int e = each_launch(list, count, [&](const GradTable &t) {
+    int e = each_launch(list, count, [&](const GradTensors &t) {
         const hipError_t r = launch_grad_sums(t, partials + at, s);
         at += grad_parts(t.first[t.count]);
         return r == hipSuccess ? SPG_OK : SPG_EHIP;
     });
     if (e != SPG_OK) return e;
-    if (launch_grad_norm(partials, parts, max_norm, norm, factor, s) != hipSuccess) return SPG_EHIP;
+    // few partial sums: every workgroup of the scaling adds them itself
+    const bool self = clip && parts > 0 && parts <= kGradSelfSum;
+    if (!self && launch_grad_norm(partials, parts, max_norm, norm, factor, s) != hipSuccess) return SPG_EHIP;
     if (!clip) return SPG_OK;
-    return each_launch(list, count, [&](const GradTable &t) {
-        return launch_grad_scale(t, factor, s) == hipSuccess ? SPG_OK : SPG_EHIP;
+    return each_launch(list, count, [&](const GradTensors &t) {
+        const hipError_t r = launch_grad_scale(t, factor, self ? partials : nullptr, parts, max_norm, norm, s);
+        return r == hipSuccess ? SPG_OK : SPG_EHIP;
     });
 }
 

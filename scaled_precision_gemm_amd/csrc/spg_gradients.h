@@ -10,20 +10,26 @@ namespace spg {
 constexpr int kGradTensors = 120;
 constexpr int64_t kGradChunk = 16384;          // elements of a workgroup's step
 constexpr int64_t kGradWorkgroups = 2048;      // of a launch, each with one partial sum
+// Up to this many partial sums every workgroup of the scaling adds them itself.
+constexpr int64_t kGradSelfSum = 512;
 
+template <int N>
 struct GradTable {
-    const void *src[kGradTensors];
-    void *dst[kGradTensors];
-    int64_t n[kGradTensors];
-    uint32_t first[kGradTensors + 1];          // chunks before the tensor
-    uint8_t bf16[kGradTensors];                // else fp32
+    const void *src[N];
+    void *dst[N];
+    int64_t n[N];
+    uint32_t first[N + 1];                     // chunks before the tensor
+    uint8_t bf16[N];                           // else fp32
     int32_t count;
 };
+using GradTensors = GradTable<kGradTensors>;
 
-hipError_t launch_grad_sums(const GradTable &t, double *partials, hipStream_t s);
+hipError_t launch_grad_sums(const GradTensors &t, double *partials, hipStream_t s);
 // norm[0] = the root of the partial sums' sum; factor[0], where given, what scales the gradients
 hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, float *factor, hipStream_t s);
-hipError_t launch_grad_scale(const GradTable &t, const float *factor, hipStream_t s);
+// By *factor; or, partials given, by the factor of their sum (parts of them), and norm[0] where given as above.
+hipError_t launch_grad_scale(const GradTensors &t, const float *factor, const double *partials, int64_t parts, double max_norm,
+                             float *norm, hipStream_t s);
 
 inline int64_t grad_parts(int64_t chunks) { return chunks < kGradWorkgroups ? chunks : kGradWorkgroups; }
 

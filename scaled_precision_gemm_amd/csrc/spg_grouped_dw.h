@@ -14,6 +14,7 @@ struct GroupedDwArgs {
     float *partials;                    // slices > 1: [tiles, slices, tile_n, 256]
     int64_t R, x_rows, N, K, ldy, ldx, lda, stride_a, ldo, stride_o;
     int32_t E, out_fp32;
+    int32_t lines;                      // rows of out and add begin on 128-byte lines
     int32_t slices;                     // parts of every expert's rows, summed by a second launch
     int32_t tile_n;                     // tiles of tile_n (128 or 256) n x 256 k
     uint32_t tiles_n, tiles_k;          // tiles of one expert

@@ -380,7 +380,11 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         // group q, k = 8 q + 4 (l / 32) .. + 3.  128-byte rows of the output
         // go through the wave's own region (16-byte chunk c of row n at c ^
         // (n / 2 % 8)), so that whole lines leave: passes of 32 n x 64 k (bf16)
-        // or x 32 k (fp32).  What is added is loaded a pass ahead (two passes
+        // or x 32 k (fp32).  Where rows begin on lines nothing is read or written
+        // twice and both go past the caches (ordinary stores of 64 x 2048 x 2048
+        // bf16 with 512 rows an expert 358 us, 323 so); elsewhere neighbouring
+        // waves meet in a line, which the L2 has to put together (64 x 1000 x 792
+        // bf16, few rows: 54 us past the caches, 28 through them).  What is added is loaded a pass ahead (two passes
         // ahead would spill registers).
         const int l32 = ln & 31, kh = ln >> 5, r8 = ln >> 3, c8 = ln & 7;
         const int64_t n0 = (int64_t)cur.tn * TN + wn * G::kWaveN, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
@@ -395,8 +399,8 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
                 const int64_t n = row_of(p, it), k = col_of(p);
                 const int64_t at = (int64_t)cur.e * a.stride_a + n * a.lda + k;
                 ad[p & 1][ADD ? it : 0] = v4i{0, 0, 0, 0};
-                if (n < a.N && k < a.K)
-                    ad[p & 1][ADD ? it : 0] = __builtin_nontemporal_load(reinterpret_cast<const v4i *>((const uint8_t *)a.add + at * kSize));
+                const v4i *const from = reinterpret_cast<const v4i *>((const uint8_t *)a.add + at * kSize);
+                if (n < a.N && k < a.K) ad[p & 1][ADD ? it : 0] = a.lines ? __builtin_nontemporal_load(from) : *from;
             }
         };
         if constexpr (ADD) load_add(0);
@@ -451,7 +455,11 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
                     if (OUT == kOutFp32 && ADD)
                         v = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, v) + __builtin_bit_cast(v4f, ad[p & 1][ADD ? it : 0]));
                     const int64_t at = (int64_t)cur.e * a.stride_o + n * a.ldo + k;
-                    __builtin_nontemporal_store(v, reinterpret_cast<v4i *>((uint8_t *)a.out + at * kSize));
+                    v4i *const to = reinterpret_cast<v4i *>((uint8_t *)a.out + at * kSize);
+                    if (a.lines)
+                        __builtin_nontemporal_store(v, to);
+                    else
+                        *to = v;
                 }
             }
         }

@@ -13,7 +13,7 @@
 // output's type (not to bf16 in between).
 //
 // A stream: 2 to 4 bytes in, 1 to 5 out per element.  A row is read once and
-// stays in the registers of its team of 16, 64, 256 or 1024 lanes, each with V
+// stays in the registers of its team of 8 to 1024 lanes, each with V
 // vectors of eight elements; a lane's loads are all in flight before the first
 // square.
 #include "spg_gemm_common.h"
@@ -149,71 +149,67 @@ __device__ __forceinline__ void load_weights(float (&w)[V][8], const void *weigh
         for (int i = 0; i < 8; ++i) w[v][i] += w0;
 }
 
-// E4M3 codes of eight fp32 values by their group's scale.  The quotient y / s
-// is y times fl32(1 / s), two roundings away from it, as y itself is a few away
-// from its exact value; scales that leave fp32's normal range on the way take
-// the quantizers' scaled division (RowScale), zero and non-finite ones IEEE
-// division.
-__device__ __forceinline__ uint2 encode8_f32(const float (&y)[8], const RowScale &t)
+// A group's scale s = fl32(amax / 448), amax = max |y|, y = y0 m: codes are
+// those of y0 (m / s), with m / s in two roundings.  Scales far from 1, zero and
+// those that are not finite take IEEE division of y.
+struct GroupScale {
+    float s, f;
+    bool plain;
+};
+__device__ __forceinline__ GroupScale group_scale(uint32_t amax0, float m)
+{
+    GroupScale t;
+    t.s = __uint_as_float(amax0) * m / 448.0f;          // rounding keeps the order: max |y0| m is max |y|
+    t.plain = t.s > 0x1p-100f && t.s < 0x1p100f;
+    float r = __builtin_amdgcn_rcpf(t.s);
+    r = __builtin_fmaf(__builtin_fmaf(-t.s, r, 1.0f), r, r);
+    t.f = m * r;
+    return t;
+}
+__device__ __forceinline__ uint2 encode8_f32(const float (&y0)[8], float m, const GroupScale &t)
 {
     uint32_t out[2];
-    if (t.s > 0x1p-100f && t.s < 0x1p100f) {
+    if (t.plain) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(y[4 * h + i] * t.r, -448.0f, 448.0f);
+            for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(y0[4 * h + i] * t.f, -448.0f, 448.0f);
             const int d = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
             out[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], d, true);
         }
-    } else if (t.fast) {
+        return make_uint2(out[0], out[1]);
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int d = __builtin_amdgcn_cvt_pk_fp8_f32(quot<true>(y[4 * h], t), quot<true>(y[4 * h + 1], t), 0, false);
-            d = __builtin_amdgcn_cvt_pk_fp8_f32(quot<true>(y[4 * h + 2], t), quot<true>(y[4 * h + 3], t), d, true);
-            out[h] = (uint32_t)d;
-        }
-    } else {
+    for (int h = 0; h < 2; ++h) {
+        out[h] = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            out[h] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = y[4 * h + i];
-                out[h] |= (t.s > 0.0f ? encode_e4m3(v / t.s) : (__float_as_uint(v) >> 24) & 0x80u) << (8 * i);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float v = y0[4 * h + i] * m;
+            out[h] |= (t.s > 0.0f ? encode_e4m3(v / t.s) : (__float_as_uint(v) >> 24) & 0x80u) << (8 * i);
         }
     }
     return make_uint2(out[0], out[1]);
 }
-// The scale of a group whose largest |y| is amax.  1 / s is taken of s itself:
-// in the range above it equals RowScale's, whose s k is s for all but the
-// smallest of them.
-__device__ __forceinline__ RowScale norm_scale(uint32_t amax)
-{
-    RowScale t = row_scale(__uint_as_float(amax));
-    if (t.s > 0x1p-100f && t.s < 0x1p100f) t.r = 1.0f / t.s;
-    return t;
-}
 
 // Sums and maxima over the TEAM lanes of a row, a power of two: inside a wave
-// by rotations within 16 lanes and exchanges of 16- and 32-lane halves, all in
+// by moves within 16 lanes and exchanges of 16- and 32-lane halves, all in
 // the vector unit, then over the workgroup's waves in LDS, in a fixed order.
 template <int CTRL>
-__device__ __forceinline__ uint32_t rotate16(uint32_t v)
+__device__ __forceinline__ uint32_t move16(uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
 template <int CTRL>
-__device__ __forceinline__ double rotate16(double v)
+__device__ __forceinline__ double move16(double v)
 {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(double, (uint64_t)rotate16<CTRL>((uint32_t)u) | (uint64_t)rotate16<CTRL>((uint32_t)(u >> 32)) << 32);
+    return __builtin_bit_cast(double, (uint64_t)move16<CTRL>((uint32_t)u) | (uint64_t)move16<CTRL>((uint32_t)(u >> 32)) << 32);
 }
 template <int CTRL>
-__device__ __forceinline__ float rotate16(float v)
+__device__ __forceinline__ float move16(float v)
 {
-    return __uint_as_float(rotate16<CTRL>(__float_as_uint(v)));
+    return __uint_as_float(move16<CTRL>(__float_as_uint(v)));
 }
 // The values of the two halves (of 32 lanes where HALF is 16, else of 64), each
 // in both: first, second.
@@ -251,10 +247,10 @@ __device__ __forceinline__ void halves(double v, double &p, double &q)
 template <int TEAM, typename T, typename F>
 __device__ __forceinline__ T wave_fold(T v, F &&f)
 {
-    v = f(v, rotate16<0x128>(v));      // by 8, 4, 2, 1 lanes of the 16
-    v = f(v, rotate16<0x124>(v));
-    v = f(v, rotate16<0x122>(v));
-    v = f(v, rotate16<0x121>(v));
+    v = f(v, move16<0xB1>(v));                           // lanes 1 0 3 2 of a quad
+    v = f(v, move16<0x4E>(v));                           // 2 3 0 1
+    v = f(v, move16<0x141>(v));                          // 7 .. 0 of eight
+    if (TEAM > 8) v = f(v, move16<0x140>(v));            // 15 .. 0 of sixteen
     if (TEAM > 16) {
         T p, q;
         halves<16>(v, p, q);
@@ -286,13 +282,13 @@ __device__ __forceinline__ void team_fold(T (&v)[U], T (*lds)[U], F &&f)
 
 // 1 / sqrt(m) for m >= 0: the hardware's estimate and two steps of Newton's
 // method in 64 bits.  m = 0 gives infinity, infinity 0, NaN NaN.
-__device__ __forceinline__ float inverse_root(double m)
+__device__ __forceinline__ double inverse_root(double m)
 {
     const double y = __builtin_amdgcn_rsq(m);
     double z = y;
 #pragma unroll
     for (int i = 0; i < 2; ++i) z = __builtin_fma(0.5 * z, __builtin_fma(-m * z, z, 1.0), z);
-    return (float)(m > 0.0 && m < __builtin_inf() ? z : y);
+    return m > 0.0 && m < __builtin_inf() ? z : y;
 }
 
 // One team of TEAM lanes per row, U rows a team at once; lane t holds the
@@ -351,12 +347,18 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
     }
     team_fold<TEAM>(ss, lds_sum, [](double p, double q) { return p + q; });
     keep_packed(hv);
-    float rstd[U];
+    // rstd = c m with a power of two c: h c is exact and near 1 whatever the
+    // row's size, y0 = (h c) w, y = y0 m
+    float c[U], m[U];
     uint32_t amax[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        rstd[u] = inverse_root(ss[u] / (double)H + a.eps);
-        if (a.rstd && t == 0 && row[u] < a.R) a.rstd[row[u]] = rstd[u];
+        const double rstd = inverse_root(ss[u] / (double)H + a.eps);
+        if (a.rstd && t == 0 && row[u] < a.R) a.rstd[row[u]] = (float)rstd;
+        const int e = min(max((int)((__builtin_bit_cast(uint64_t, rstd) >> 52) & 0x7FF) - 1023, -126), 127);
+        const bool ordinary = rstd > 0.0 && rstd < __builtin_inf();
+        c[u] = ordinary ? __uint_as_float((uint32_t)(e + 127) << 23) : (float)rstd;
+        m[u] = ordinary ? (float)(rstd * __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52)) : 1.0f;
         amax[u] = 0;
         if (a.residual) {
 #pragma unroll
@@ -369,7 +371,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
     auto values = [&](int u, int v, float (&y)[8]) {
         unpack8(hv[u][v], y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (y[i] * rstd[u]) * w[v][i];
+        for (int i = 0; i < 8; ++i) y[i] = (y[i] * c[u]) * w[v][i];
     };
     auto largest = [](const float (&y)[8]) {
         uint32_t m = 0;
@@ -391,9 +393,9 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        RowScale rs;
+        GroupScale rs;
         if constexpr (OUTPUT == SPG_NORM_E4M3_ROW) {
-            rs = norm_scale(amax[u]);
+            rs = group_scale(amax[u], m[u]);
             if (t == 0 && row[u] < a.R) a.scale[row[u]] = rs.s;
         }
 #pragma unroll
@@ -403,13 +405,17 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(const
             values(u, v, y);
             const bool in = row[u] < a.R && col < H;
             if constexpr (OUTPUT == SPG_NORM_E4M3_BLOCK128) {
-                rs = norm_scale(wave_fold<16>(in ? largest(y) : 0u, [](uint32_t p, uint32_t q) { return p > q ? p : q; }));
+                rs = group_scale(wave_fold<16>(in ? largest(y) : 0u, [](uint32_t p, uint32_t q) { return p > q ? p : q; }), m[u]);
                 if (in && (t & 15) == 0) a.scale[(int64_t)(col >> 7) * a.R + row[u]] = rs.s;
             }
             if (!in) continue;
             if constexpr (OUTPUT != SPG_NORM_BF16)
-                *reinterpret_cast<uint2 *>(a.q + row[u] * a.ldq + col) = encode8_f32(y, rs);    // H % 16 == 0
-            if (OUTPUT == SPG_NORM_BF16 || a.normed) store8(a.normed + row[u] * a.ldn + col, pack8(y), H - col);
+                *reinterpret_cast<uint2 *>(a.q + row[u] * a.ldq + col) = encode8_f32(y, m[u], rs);    // H % 16 == 0
+            if (OUTPUT == SPG_NORM_BF16 || a.normed) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= m[u];
+                store8(a.normed + row[u] * a.ldn + col, pack8(y), H - col);
+            }
         }
     }
 }
@@ -423,7 +429,7 @@ hipError_t launch_team(const NormArgs &a, hipStream_t s)
         rms_norm_kernel<TEAM, V, U, SPG_NORM_BF16><<<grid, THREADS, 0, s>>>(a);
     else if (a.output == SPG_NORM_E4M3_ROW)
         rms_norm_kernel<TEAM, V, U, SPG_NORM_E4M3_ROW><<<grid, THREADS, 0, s>>>(a);
-    else
+    else if constexpr (TEAM >= 16)
         rms_norm_kernel<TEAM, V, U, SPG_NORM_E4M3_BLOCK128><<<grid, THREADS, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -587,6 +593,7 @@ using Int = std::integral_constant<int, N>;
 template <typename F>
 auto with_grad_shape(int64_t H, F &&f)
 {
+    if (H <= 64) return f(Int<8>{}, Int<1>{}, Int<4>{});
     if (H <= 128) return f(Int<16>{}, Int<1>{}, Int<4>{});
     if (H <= 256) return f(Int<16>{}, Int<2>{}, Int<2>{});
     if (H <= 512) return f(Int<16>{}, Int<4>{}, Int<2>{});
@@ -605,7 +612,9 @@ int64_t norm_grad_parts(int64_t R, int64_t H)
     const int64_t rows = with_grad_shape(H, [](auto team, auto, auto u) { return (team < 256 ? 256 / team : 1) * u; });
     const int64_t most = with_grad_shape(H, [](auto team, auto, auto) { return team < 1024 ? 512 : 256; });
     const int64_t n = (R + rows - 1) / rows;
-    return n < 1 ? 1 : n < most ? n : most;     // no rows: one, which writes zeros
+    // one workgroup for up to four of its steps (1 us each; a second launch and
+    // its workspace take 8), and for no rows, where it writes zeros
+    return n <= 4 ? 1 : n < most ? n : most;
 }
 
 int64_t norm_grad_width(int64_t H)
@@ -616,6 +625,8 @@ int64_t norm_grad_width(int64_t H)
 hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
 {
     const int64_t H = a.H;
+    // (128-element groups are 16 lanes)
+    if (H <= 64 && a.output != SPG_NORM_E4M3_BLOCK128) return launch_team<8, 1, 4>(a, s);
     if (H <= 128) return launch_team<16, 1, 4>(a, s);
     if (H <= 256) return launch_team<16, 2, 2>(a, s);
     if (H <= 512) return launch_team<16, 4, 1>(a, s);

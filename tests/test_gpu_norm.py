@@ -81,7 +81,7 @@ def run(spg, R, H, output, residual=True, wt=BF, w0=0.0, normed=False, seed=0, e
 
 
 # every team and number of vectors, both sides of each border; few rows and many
-SIZES = [16, 128, 144, 256, 272, 512, 528, 1024, 1040, 2048, 2064, 4096, 4112, 5120, 6144, 6160, 8192, 8208, 16384, 16400,
+SIZES = [16, 64, 80, 128, 144, 256, 272, 512, 528, 1024, 1040, 2048, 2064, 4096, 4112, 5120, 6144, 6160, 8192, 8208, 16384, 16400,
          32768]
 
 
@@ -94,7 +94,7 @@ def test_sizes(spg, H, output):
         run(spg, 300, H, output, seed=H)
 
 
-@pytest.mark.parametrize("H", [1, 2, 7, 8, 9, 63, 127, 129, 255, 513, 1023, 1025, 2047, 4099, 8191, 8193, 20001, 32767])
+@pytest.mark.parametrize("H", [1, 2, 7, 8, 9, 63, 64, 65, 127, 129, 255, 513, 1023, 1025, 2047, 4099, 8191, 8193, 20001, 32767])
 def test_odd_sizes(spg, H):
     for R in (1, 5, 66):
         run(spg, R, H, "bf16", residual=R == 5, wt=F32 if R == 66 else BF, seed=H + R)
@@ -255,13 +255,13 @@ def run_backward(spg, R, H, dres=True, wt=BF, w0=0.0, seed=0):
     return gx, gw
 
 
-@pytest.mark.parametrize("H", [1, 7, 128, 130, 256, 511, 512, 1000, 1024, 2048, 4096, 5120, 6151, 8192, 16384, 32768])
+@pytest.mark.parametrize("H", [1, 7, 64, 65, 128, 130, 256, 511, 512, 1000, 1024, 2048, 4096, 5120, 6151, 8192, 16384, 32768])
 def test_backward_sizes(spg, H):
-    for R in (1, 2, 67):
+    for R in (1, 2, 67) if H < 4096 else (1, 2, 7, 9, 67):
         run_backward(spg, R, H, dres=R != 2, wt=F32 if R == 2 else BF, w0=1.0 if R == 67 else 0.0, seed=H + R)
 
 
-@pytest.mark.parametrize("R,H", [(511, 5120), (512, 4096), (513, 5120), (2049, 2048), (5000, 640), (20000, 128)])
+@pytest.mark.parametrize("R,H", [(511, 5120), (512, 4096), (513, 5120), (2049, 2048), (5000, 640), (20000, 128), (50000, 64), (300, 7)])
 def test_backward_many_rows(spg, R, H):
     run_backward(spg, R, H)
 

@@ -63,7 +63,7 @@ def test_norm_needs_a_desc():
     assert spg.lib.rms_norm_backward(at(0), at(1), None, at(2), at(3), at(4), None, None, None, 0, None) == EINVAL
 
 
-def backward(R=64, H=256, dy=at(0), h=at(1), dres=None, weight=at(2), rstd=at(3), dx=at(4), dw=at(5), ws=at(6),
+def backward(R=256, H=256, dy=at(0), h=at(1), dres=None, weight=at(2), rstd=at(3), dx=at(4), dw=at(5), ws=at(6),
              ws_bytes=None, **kw):
     d = dict(R=R, H=H, ldg=H, ldh=H, ldr=H, ldx=H, weight_offset=0.0, weight_fp32=0)
     d.update(kw)
@@ -92,8 +92,8 @@ def test_backward_refusals(kw, want):
 
 def test_backward_workspace():
     f = spg.lib.rms_norm_backward_workspace_bytes
-    assert f(0, 256) == f(1, 5120) == f(2, 5120) == f(-1, 256) == f(8, 0) == f(8, 40000) == 0
-    assert f(3, 4096) == 2 * 4096 * 4          # two rows a workgroup, one partial sum each
+    assert f(0, 256) == f(1, 5120) == f(8, 5120) == f(-1, 256) == f(9, 0) == f(9, 40000) == 0
+    assert f(9, 4096) == 5 * 4096 * 4          # two rows a workgroup, one partial sum each
     for H, parts in ((128, 512), (640, 512), (4096, 512), (5120, 256), (20000, 256)):
         assert parts * H * 4 <= f(10 ** 6, H) <= parts * 2 * H * 4
     assert spg.norm_workspace(1, 5120, "cpu") is None and spg.norm_workspace(9, 5120, "cpu").numel() == f(9, 5120)
