@@ -149,21 +149,29 @@ __device__ __forceinline__ void load_weights(float (&w)[V][8], const void *weigh
         for (int i = 0; i < 8; ++i) w[v][i] += w0;
 }
 
-// A group's scale s = fl32(amax / 448), amax = max |y|, y = y0 m: codes are
-// those of y0 (m / s), with m / s in two roundings.  Scales far from 1, zero and
-// those that are not finite take IEEE division of y.
+// A group's scale s = fl32(amax / 448), amax = max |y| = max |y0| m.  m falls
+// out of a quotient by the unrounded scale, y0 (448 / max |y0|), whose factor is
+// held as a sum of two numbers: the codes' quotients are within a last bit (the
+// products of bf16 weights y0 are exact).  Scales far from 1, zero and those
+// that are not finite take IEEE division of y by s.
 struct GroupScale {
-    float s, f;
+    float s, f, f2;
     bool plain;
 };
 __device__ __forceinline__ GroupScale group_scale(uint32_t amax0, float m)
 {
     GroupScale t;
-    t.s = __uint_as_float(amax0) * m / 448.0f;          // rounding keeps the order: max |y0| m is max |y|
+    const float a = __uint_as_float(amax0);
+    t.s = a * m / 448.0f;          // rounding keeps the order: max |y0| m is max |y|
     t.plain = t.s > 0x1p-100f && t.s < 0x1p100f;
-    float r = __builtin_amdgcn_rcpf(t.s);
-    r = __builtin_fmaf(__builtin_fmaf(-t.s, r, 1.0f), r, r);
-    t.f = m * r;
+    const float r = __builtin_amdgcn_rcpf(a);
+    t.f = 448.0f * r;
+    t.f = __builtin_fmaf(__builtin_fmaf(-t.f, a, 448.0f), r, t.f);
+    t.f2 = __builtin_fmaf(-t.f, a, 448.0f) * r;
+    if (t.f2 < 0.0f) {             // both of one sign: y0 = -0 stays -0
+        t.f = __uint_as_float(__float_as_uint(t.f) - 1);
+        t.f2 = __builtin_fmaf(-t.f, a, 448.0f) * r;
+    }
     return t;
 }
 __device__ __forceinline__ uint2 encode8_f32(const float (&y0)[8], float m, const GroupScale &t)
@@ -174,7 +182,7 @@ __device__ __forceinline__ uint2 encode8_f32(const float (&y0)[8], float m, cons
         for (int h = 0; h < 2; ++h) {
             float q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(y0[4 * h + i] * t.f, -448.0f, 448.0f);
+            for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_fmed3f(__builtin_fmaf(y0[4 * h + i], t.f, y0[4 * h + i] * t.f2), -448.0f, 448.0f);
             const int d = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
             out[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], d, true);
         }
@@ -627,8 +635,8 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
     const int64_t H = a.H;
     // (128-element groups are 16 lanes)
     if (H <= 64 && a.output != SPG_NORM_E4M3_BLOCK128) return launch_team<8, 1, 4>(a, s);
-    if (H <= 128) return launch_team<16, 1, 4>(a, s);
-    if (H <= 256) return launch_team<16, 2, 2>(a, s);
+    if (H <= 128) return launch_team<16, 1, 2>(a, s);
+    if (H <= 256) return launch_team<16, 2, 1>(a, s);
     if (H <= 512) return launch_team<16, 4, 1>(a, s);
     if (H <= 1024) return launch_team<64, 2, 1>(a, s);
     if (a.R <= 256 && H <= 2048) return launch_team<256, 1, 1>(a, s);
