@@ -169,6 +169,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         int rows;                                                 // of the tile from there on; not above 0: none
         int left, at, buf;                                        // stages left; stage of the tile; index buffer
         uint32_t vy[G::kCopyY], vx[2];                            // byte offsets of the lane's chunks (gathered X: in its row)
+        uint32_t most[2];                                         // gathered X: rows that the lane may read, 0 past K
     } cp;
     auto copy_tile = [&](const DwTile &t) {
         cp.y = a.dy + t.r0 * a.ldy;
@@ -186,6 +187,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         for (int i = 0; i < 2; ++i) {
             const uint32_t r = (uint32_t)(2 * i) + rxl;
             const uint32_t c = t.tk * kDwTile + ((((uint32_t)ln & 31u) ^ (r << 2)) << 3);
+            cp.most[i] = c < (uint32_t)a.K ? (uint32_t)a.x_rows : 0u;
             cp.vx[i] = c < (uint32_t)a.K ? (GATHER ? 0u : ((uint32_t)(wave * 4) + r) * ldx) + c * 2u : kOOB;
         }
     };
@@ -209,33 +211,39 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         since = 0;
     };
     // What the next stage's copies take, worked out ahead of the barrier that
-    // frees their slot; then copy instruction i of the four.  Rows past the
-    // tile's last one are past the buffers' ranges.
+    // frees their slot, in three parts that stand behind MFMAs of their own (in
+    // one, the vector instructions of both waves of a SIMD held its matrix core
+    // up: 64 x 2048 x 2048 bf16 over 32768 gathered rows 340 us, 333 so); then copy
+    // instruction i of the stage's.  Rows past the tile's last one are past the
+    // buffers' ranges.
     struct {
         v4i y, x;
-        uint32_t vy[G::kCopyY], vx[2];
+        uint32_t live, vx[2];
+        int32_t row[2];
     } pl;
-    auto plan = [&]() {
-        const bool border = cp.left == 0, chunk = cp.at > 0 && cp.at % kChunkStages == 0;
-        if (GATHER && (border || chunk)) {
-            if (since < 4) wait_vmem<0>();
-            cp.buf ^= 1;
-        }
-        if (border) copy_tile(nxt);
-        const uint32_t live = (uint32_t)max(0, min(kStageRows, cp.rows));
-        pl.y = make_rsrc(cp.y, live * ldy);
-        pl.x = GATHER ? rs_all : make_rsrc(cp.x, live * ldx);
+    auto plan = [&](int part) {
+        if (part == 0) {
+            const bool border = cp.left == 0, chunk = cp.at > 0 && cp.at % kChunkStages == 0;
+            if (GATHER && (border || chunk)) {
+                if (since < 4) wait_vmem<0>();
+                cp.buf ^= 1;
+            }
+            if (border) copy_tile(nxt);
+            pl.live = (uint32_t)max(0, min(kStageRows, cp.rows));
+            pl.y = make_rsrc(cp.y, pl.live * ldy);
+            pl.x = GATHER ? rs_all : make_rsrc(cp.x, pl.live * ldx);
+            if (GATHER) {
 #pragma unroll
-        for (int i = 0; i < G::kCopyY; ++i) pl.vy[i] = cp.vy[i];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2; ++i)
+                    pl.row[i] = *reinterpret_cast<const int32_t *>(
+                        &lds[kIndexAt + (wave * 2 + cp.buf) * kIndexBytes + ((cp.at % kChunkStages) * 4 + 2 * i + (ln >> 5)) * 4]);
+            }
+        } else {
+            const int i = part - 1;
             pl.vx[i] = cp.vx[i];
             if (GATHER) {
-                const int row = wave * 4 + 2 * i + (ln >> 5);
-                const int32_t v = *reinterpret_cast<const int32_t *>(
-                    &lds[kIndexAt + (wave * 2 + cp.buf) * kIndexBytes + ((cp.at % kChunkStages) * 4 + 2 * i + (ln >> 5)) * 4]);
-                const bool ok = row < (int)live && cp.vx[i] != kOOB && v >= 0 && (int64_t)v < a.x_rows;
-                pl.vx[i] = ok ? (uint32_t)v * ldx + cp.vx[i] : kOOB;
+                const bool ok = wave * 4 + 2 * i + (ln >> 5) < (int)pl.live && (uint32_t)pl.row[i] < cp.most[i];
+                pl.vx[i] = ok ? (uint32_t)pl.row[i] * ldx + cp.vx[i] : kOOB;
             }
         }
     };
@@ -243,7 +251,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         const uint32_t base =
             (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_base + (uint32_t)(slot * G::kSlot)));
         if (i < G::kCopyY)
-            dma16(base + (uint32_t)(wave * 4 * G::kRowY + i * 1024), pl.vy[i < G::kCopyY ? i : 0], pl.y, 0);
+            dma16(base + (uint32_t)(wave * 4 * G::kRowY + i * 1024), cp.vy[i < G::kCopyY ? i : 0], pl.y, 0);
         else
             dma16(base + (uint32_t)(G::kY + wave * 4 * G::kRowX + (i - G::kCopyY) * 1024), pl.vx[(i - G::kCopyY) & 1], pl.x, 0);
     };
@@ -264,7 +272,8 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         --cp.left;
     };
     auto issue = [&](int slot) {
-        plan();
+#pragma unroll
+        for (int part = 0; part < 3; ++part) plan(part);
 #pragma unroll
         for (int i = 0; i < G::kCopies; ++i) issue_one(slot, i);
         advance();
@@ -339,7 +348,7 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 #pragma unroll
                 for (int i = m * kPer; i < (m + 1) * kPer && i < kFrags; ++i)
                     if (REAL || h == 1) read_frag(h == 0 ? sb : nb, h ^ 1, i);
-                if (h == 0 && m == kMfma - 2 && more) plan();
+                if (h == 0 && m >= kMfma - 4 && m < kMfma - 1 && more) plan(m - (kMfma - 4));
                 if (h == 1 && m < G::kCopies && more) issue_one(slot, m);
                 if (h == 1 && m == kMfma - 1 && more) advance();
                 __builtin_amdgcn_sched_barrier(0);
