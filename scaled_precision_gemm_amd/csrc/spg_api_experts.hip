@@ -191,8 +191,13 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
 namespace {
 
 // Tiles of 256 n x 256 k; 128 n where those would leave half of the compute
-// units (256 on an MI355X) idle, and every expert's rows then in as many parts,
-// of at least 256 rows on average, as give every unit a workgroup.
+// units (256 on an MI355X) idle (fp32, us: 4096 x 2048 over 4000 rows 97 -> 76, 8
+// experts of 1024 x 512 and 1024 rows 28.5 -> 23.7; 5120 x 5120 over 4096 rows, 400
+// tiles, 221 -> 265).  Those experts' rows are cut into s parts, at most one a unit:
+// a tile's walk takes rows / 76 us, which s divides, the second launch 3 us, and
+// every partial tile 0.06 (512 x 512 over 4096 rows, 8 tiles: s = 1 58 us, 4 23, 8
+// 19, 16 20; 2048 x 2048 over 4096 rows, 128 tiles: 1 65, 2 53; over 1024 rows 22.7
+// and 29.6).
 struct DwPlan {
     int32_t tile_n, slices;
     int64_t tiles_n, tiles_k, tiles;
@@ -206,11 +211,16 @@ DwPlan dw_plan(const spg_grouped_dw_desc *d)
     }
     p.tiles = d->experts * p.tiles_n * p.tiles_k;
     if (p.tiles == 0) return p;
-    int64_t s = 256 / p.tiles;
-    const int64_t most = d->rows / d->experts / 256;
-    s = s < most ? s : most;
-    s = s < kDwMaxSlices ? s : kDwMaxSlices;
-    p.slices = s < 1 ? 1 : (int32_t)s;
+    const int64_t rows = d->rows / d->experts, units = 256 / p.tiles;
+    const int64_t most = units < kDwMaxSlices ? units : kDwMaxSlices;
+    int64_t best = rows * 100 / 76;                         // hundredths of a us
+    for (int64_t s = 2; s <= most; ++s) {
+        const int64_t t = rows * 100 / (76 * s) + 300 + 6 * p.tiles * s;
+        if (t < best) {
+            best = t;
+            p.slices = (int32_t)s;
+        }
+    }
     return p;
 }
 

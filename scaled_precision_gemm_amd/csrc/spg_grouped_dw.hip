@@ -505,30 +505,38 @@ __device__ __forceinline__ void store_chunk(const GroupedDwArgs &a, int e, int64
     }
 }
 
-// Sums the slices' partial tiles in their order: a workgroup per 16 rows of a
-// tile, eight columns of one row per thread and step.
+// Sums the slices' partial tiles in their order: a workgroup per 4 rows of a
+// tile, eight columns of one row per thread, kBatch slices' loads in flight.
+constexpr int kReduceRows = 4, kBatch = 4;
 template <int TN, int OUT>
-__global__ __launch_bounds__(256) void grouped_dw_reduce_kernel(const GroupedDwArgs a)
+__global__ __launch_bounds__(32 * kReduceRows) void grouped_dw_reduce_kernel(const GroupedDwArgs a)
 {
-    constexpr uint32_t kParts = TN / 16;
+    constexpr uint32_t kParts = TN / kReduceRows;
     const uint32_t tile = blockIdx.x / kParts;
     const uint32_t row = fdiv(tile, a.div_k), tk = tile - row * a.tiles_k;
     const uint32_t e = fdiv(row, a.div_n), tn = row - e * a.tiles_n;
-    const float *p = a.partials + (int64_t)tile * a.slices * (TN * kDwTile);
+    const int r = (int)(blockIdx.x % kParts) * kReduceRows + (int)(threadIdx.x >> 5), c = (int)(threadIdx.x & 31u) * 8;
+    const int64_t n = (int64_t)tn * TN + r, k = (int64_t)tk * kDwTile + c;
+    if (n >= a.N || k >= a.K) return;
+    const float *p = a.partials + (int64_t)tile * a.slices * (TN * kDwTile) + r * kDwTile + c;
+    v4f lo = {}, hi = {};
+    for (int s0 = 0; s0 < a.slices; s0 += kBatch) {
+        v4f l[kBatch], h[kBatch];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = (int)(blockIdx.x % kParts) * 16 + i * 8 + (int)(threadIdx.x >> 5), c = (int)(threadIdx.x & 31u) * 8;
-        const int64_t n = (int64_t)tn * TN + r, k = (int64_t)tk * kDwTile + c;
-        if (n >= a.N || k >= a.K) continue;
-        v4f lo = {}, hi = {};
-        for (int s = 0; s < a.slices; ++s) {
-            const float *q = p + (int64_t)s * (TN * kDwTile) + r * kDwTile + c;
-            lo += __builtin_nontemporal_load(reinterpret_cast<const v4f *>(q));
-            hi += __builtin_nontemporal_load(reinterpret_cast<const v4f *>(q + 4));
+        for (int i = 0; i < kBatch; ++i) {
+            const float *q = p + (int64_t)min(s0 + i, a.slices - 1) * (TN * kDwTile);
+            l[i] = *reinterpret_cast<const v4f *>(q);
+            h[i] = *reinterpret_cast<const v4f *>(q + 4);
         }
-        store_chunk<OUT>(a, (int)e, n, k, lo, hi);
-        if (OUT == kOutFp32) store_chunk<OUT>(a, (int)e, n, k + 4, hi, hi);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s0 + i < a.slices) {
+                lo += l[i];
+                hi += h[i];
+            }
     }
+    store_chunk<OUT>(a, (int)e, n, k, lo, hi);
+    if (OUT == kOutFp32) store_chunk<OUT>(a, (int)e, n, k + 4, hi, hi);
 }
 
 template <int TN, int OUT>
@@ -560,11 +568,11 @@ hipError_t launch_tiles(const GroupedDwArgs &a, hipStream_t s)
     if (a.slices == 1) return a.out_fp32 ? launch_out<TN, kOutFp32>(a, grid, s) : launch_out<TN, kOutBf16>(a, grid, s);
     hipError_t e = launch_out<TN, kOutPartial>(a, grid, s);
     if (e != hipSuccess) return e;
-    const unsigned parts = (unsigned)((int64_t)a.E * a.tiles_n * a.tiles_k * (TN / 16));
+    const unsigned parts = (unsigned)((int64_t)a.E * a.tiles_n * a.tiles_k * (TN / kReduceRows));
     if (a.out_fp32)
-        grouped_dw_reduce_kernel<TN, kOutFp32><<<parts, 256, 0, s>>>(a);
+        grouped_dw_reduce_kernel<TN, kOutFp32><<<parts, 32 * kReduceRows, 0, s>>>(a);
     else
-        grouped_dw_reduce_kernel<TN, kOutBf16><<<parts, 256, 0, s>>>(a);
+        grouped_dw_reduce_kernel<TN, kOutBf16><<<parts, 32 * kReduceRows, 0, s>>>(a);
     return hipGetLastError();
 }
 

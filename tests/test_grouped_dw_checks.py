@@ -74,11 +74,11 @@ def test_workspace():
     f = lambda **kw: spg.lib.gemm_grouped_dw_workspace_bytes(ctypes.byref(desc(**kw)))  # noqa: E731
     tile = 256 * 256 * 4
     assert f() == 0 and f(N=516) == 0                       # 256 rows an expert; an invalid call
-    assert f(**DENSE) == 4 * 16 * tile // 2                 # four tiles of 128 x 256 in sixteen parts
+    assert f(**DENSE) == 4 * 15 * tile // 2                 # four tiles of 128 x 256 in fifteen parts
     assert f(rows=4000, x_rows=4000, N=2048, K=2048, experts=1) == 128 * 2 * tile // 2
     assert f(rows=4000, x_rows=4000, N=4096, K=2048, experts=1) == 0
     assert f(rows=4000, x_rows=4000, N=4096, K=2304, experts=1) == 0    # 144 tiles of 256 x 256
-    assert spg.grouped_dw_workspace(4096, 1, 512, 256, "cpu").numel() == 4 * 16 * tile // 2
+    assert spg.grouped_dw_workspace(4096, 1, 512, 256, "cpu").numel() == 4 * 15 * tile // 2
     assert spg.grouped_dw_workspace(1024, 4, 512, 256, "cpu") is None
 
 
