@@ -10,19 +10,18 @@ namespace spg {
 constexpr int kGradTensors = 120;
 constexpr int64_t kGradChunk = 16384;          // elements of a workgroup's step
 constexpr int64_t kGradWorkgroups = 2048;      // of a launch, each with one partial sum
-// Up to this many partial sums every workgroup of the scaling adds them itself.
+// Up to this many partial sums every workgroup of the scaling adds them itself, a
+// launch less (one tensor of 1000 elements: 18.4 us with it, 16.0 without).
 constexpr int64_t kGradSelfSum = 512;
 
-template <int N>
-struct GradTable {
-    const void *src[N];
-    void *dst[N];
-    int64_t n[N];
-    uint32_t first[N + 1];                     // chunks before the tensor
-    uint8_t bf16[N];                           // else fp32
+struct GradTensors {
+    const void *src[kGradTensors];
+    void *dst[kGradTensors];
+    int64_t n[kGradTensors];
+    uint32_t first[kGradTensors + 1];          // chunks before the tensor
+    uint32_t bf16[kGradTensors];               // else fp32
     int32_t count;
 };
-using GradTensors = GradTable<kGradTensors>;
 
 hipError_t launch_grad_sums(const GradTensors &t, double *partials, hipStream_t s);
 // norm[0] = the root of the partial sums' sum; factor[0], where given, what scales the gradients

@@ -5,12 +5,16 @@
 //   g' = g (n > max ? max / n : 1)               fp32, one rounding to g's type
 //
 // A stream: every gradient is read for the sum and, where it is scaled, read
-// and written once more.  Chunks of kGradChunk elements, none across two
-// tensors, are dealt to at most kGradWorkgroups workgroups in turn; a
-// workgroup leaves one partial sum, and they are added in order, so the same
-// tensors give the same bits.  Squares are formed and added in 64 bits: 10^8 of
-// them added in fp32 would lose the last ones, and fp32's largest values
-// squared overflow it.
+// and written once more: 336 million bf16 elements in nine tensors take 149 us
+// for the sums and 228 for the scaling, 2.0 GB at 5.3 TB/s, what a copy reaches.
+// Few small tensors take the launches' time: 16 us a call for one of 1000
+// elements, 0.6 us for every further one (the host's).
+//
+// Chunks of kGradChunk elements, none across two tensors, are dealt to at most
+// kGradWorkgroups workgroups in turn; a workgroup leaves one partial sum, and
+// they are added in order, so the same tensors give the same bits.  Squares are
+// formed and added in 64 bits: 10^8 of them added in fp32 would lose the last
+// ones, and fp32's largest values squared overflow it.
 #include "spg_gemm_common.h"
 #include "spg_gradients.h"
 
@@ -38,9 +42,25 @@ __device__ __forceinline__ uint4 load16(const void *p)
     return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
 
+// Vectors v0 + 256 i of `vecs` (at least one), zeros past them.  No branch
+// stands between the loads and nothing is moved between them, so that all are
+// in flight at once.
+template <bool BF16>
+__device__ __forceinline__ void load_vectors(uint4 (&r)[8], const uint8_t *b, int v0, int vecs)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int v = v0 + i * kThreads;
+        r[i] = load16<BF16>(b + (int64_t)(v < vecs ? v : 0) * 16);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (v0 + i * kThreads >= vecs) r[i] = make_uint4(0, 0, 0, 0);
+}
+
 // The tensor of chunk c: the last one whose first chunk is not behind it.
-template <int N>
-__device__ __forceinline__ int find_tensor(const GradTable<N> &t, uint32_t c)
+__device__ __forceinline__ int find_tensor(const GradTensors &t, uint32_t c)
 {
     int lo = 0, hi = t.count;
     while (hi - lo > 1) {
@@ -65,12 +85,7 @@ __device__ __forceinline__ double chunk_sum(const void *p, int n)
     const int vecs = n / W;
     for (int v0 = (int)threadIdx.x; v0 < vecs; v0 += kThreads * 8) {
         uint4 r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int v = v0 + i * kThreads;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (v < vecs) r[i] = load16<BF16>(b + (int64_t)v * 16);
-        }
+        load_vectors<BF16>(r, b, v0, vecs);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
@@ -102,8 +117,7 @@ __device__ __forceinline__ double block_sum(double s, double *lds)
     return s;
 }
 
-template <int N>
-__global__ __launch_bounds__(kThreads) void grad_sums_kernel(const GradTable<N> t, double *partials)
+__global__ __launch_bounds__(kThreads) void grad_sums_kernel(const GradTensors t, double *partials)
 {
     __shared__ double lds[kThreads / 64];
     double s = 0.0;
@@ -150,12 +164,7 @@ __device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float
     const int vecs = n / W;
     for (int v0 = (int)threadIdx.x; v0 < vecs; v0 += kThreads * 8) {
         uint4 r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int v = v0 + i * kThreads;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (v < vecs) r[i] = load16<BF16>(b + (int64_t)v * 16);
-        }
+        load_vectors<BF16>(r, b, v0, vecs);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int v = v0 + i * kThreads;
@@ -185,8 +194,7 @@ __device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float
     }
 }
 
-template <int N>
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable<N> t, const float *factor, const double *partials,
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTensors t, const float *factor, const double *partials,
                                                               int64_t parts, double max_norm, float *norm)
 {
     __shared__ double lds[kThreads / 64];
@@ -212,39 +220,13 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTable<N>
     }
 }
 
-// Calls f with the smallest table that holds t: a launch copies its arguments
-// (one tensor: 19 us a call with the whole table, 15 with eight places).
-template <int N, typename F>
-hipError_t shortened(const GradTensors &t, F &&f)
-{
-    GradTable<N> s;
-    for (int i = 0; i < t.count; ++i) {
-        s.src[i] = t.src[i];
-        s.dst[i] = t.dst[i];
-        s.n[i] = t.n[i];
-        s.first[i] = t.first[i];
-        s.bf16[i] = t.bf16[i];
-    }
-    s.first[t.count] = t.first[t.count];
-    s.count = t.count;
-    f(s);
-    return hipGetLastError();
-}
-template <typename F>
-hipError_t with_table(const GradTensors &t, F &&f)
-{
-    if (t.count <= 8) return shortened<8>(t, f);
-    if (t.count <= 32) return shortened<32>(t, f);
-    f(t);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_grad_sums(const GradTensors &t, double *partials, hipStream_t s)
 {
     const unsigned grid = (unsigned)grad_parts(t.first[t.count]);
-    return with_table(t, [&](const auto &u) { grad_sums_kernel<<<grid, kThreads, 0, s>>>(u, partials); });
+    grad_sums_kernel<<<grid, kThreads, 0, s>>>(t, partials);
+    return hipGetLastError();
 }
 
 hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, float *factor, hipStream_t s)
@@ -257,9 +239,8 @@ hipError_t launch_grad_scale(const GradTensors &t, const float *factor, const do
                              float *norm, hipStream_t s)
 {
     const unsigned grid = (unsigned)grad_parts(t.first[t.count]);
-    return with_table(t, [&](const auto &u) {
-        grad_scale_kernel<<<grid, kThreads, 0, s>>>(u, factor, partials, parts, max_norm, norm);
-    });
+    grad_scale_kernel<<<grid, kThreads, 0, s>>>(t, factor, partials, parts, max_norm, norm);
+    return hipGetLastError();
 }
 
 }  // namespace spg
