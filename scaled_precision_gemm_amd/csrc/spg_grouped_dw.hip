@@ -8,10 +8,11 @@
 // each of 16 lanes four elements of one column out of four rows of 16
 // elements, and the operands need no transposed copy.
 //
-//  * 256 x 256 tiles of dW_e over eight waves (two a SIMD), each 128 n x 64 k
-//    as 4 x 2 blocks of v_mfma_f32_32x32x16_bf16: 128 accumulators a lane.
-//    X is the first MFMA operand, so a lane's four consecutive results are
-//    four consecutive k of one row n.
+//  * 256 x 256 tiles of dW_e (128 x 256 where those are few) over eight waves
+//    (two a SIMD), each 128 n x 64 k as 4 x 2 blocks of
+//    v_mfma_f32_32x32x16_bf16: 128 accumulators a lane.  X is the first MFMA
+//    operand, so a lane's four consecutive results are four consecutive k of
+//    one row n.
 //  * A stage is 32 rows of both operands, 32 KiB, copied straight into one of
 //    kDepth LDS slots (buffer loads to LDS).  Rows past the expert's last
 //    one are out of the buffer's range and read as zeros in both operands, so
@@ -20,7 +21,17 @@
 //    takes 64 bytes of four consecutive rows 512 bytes apart, which then lie
 //    in four different quarters of the 64 banks.
 //  * Experts' rows are read from the offsets on the device, so a captured graph
-//    serves any routing.
+//    serves any routing.  Workgroups stay and take tile after tile, copying the
+//    next one's first stages under the last one's end.
+//
+// What bounds it: long sums the power limit, 32768 rows x 4096 x 4096 870 us, 1.27
+// PFLOP/s, MFMAs busy 68 % at 1.63 GHz (without the copies 720 us, 82 % at 1.645;
+// three, four or five slots, and copies that all hit the L2, alike).  64 experts'
+// 2048 x 2048 over 512 rows each, 310-340 us, 38 %: sixteen stages of 1570 cycles
+// a tile and 5400 for its end, whose output of 537 MB takes 103 us at the memory's
+// rate; fewer cycles there (no zeroing of accumulators, an epilogue in two
+// regions) lower the clock, not the time.  Few rows an expert: the output at 5.2
+// TB/s.
 #include "spg_gemm_common.h"
 #include "spg_grouped_dw.h"
 
@@ -393,8 +404,10 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
         // twice and both go past the caches (ordinary stores of 64 x 2048 x 2048
         // bf16 with 512 rows an expert 358 us, 323 so); elsewhere neighbouring
         // waves meet in a line, which the L2 has to put together (64 x 1000 x 792
-        // bf16, few rows: 54 us past the caches, 28 through them).  What is added is loaded a pass ahead (two passes
-        // ahead would spill registers).
+        // bf16, few rows: 54 us past the caches, 28 through them).  What is added is
+        // loaded a pass ahead (two passes ahead would spill registers; as the
+        // accumulators' first values it came to 290 us where this takes 275: 64
+        // experts of 2048 x 1024 in fp32 over 32768 rows).
         const int l32 = ln & 31, kh = ln >> 5, r8 = ln >> 3, c8 = ln & 7;
         const int64_t n0 = (int64_t)cur.tn * TN + wn * G::kWaveN, k0 = (int64_t)cur.tk * kDwTile + wk * 64;
         constexpr int kPasses = OUT == kOutBf16 ? kYB : 2 * kYB, kSize = OUT == kOutBf16 ? 2 : 4;

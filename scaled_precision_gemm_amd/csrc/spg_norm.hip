@@ -15,7 +15,10 @@
 // A stream: 2 to 4 bytes in, 1 to 5 out per element.  A row is read once and
 // stays in the registers of its team of 8 to 1024 lanes, each with V
 // vectors of eight elements; a lane's loads are all in flight before the first
-// square.
+// square.  With a residual and row scales 4096 x 5120 (147 MB) takes 30 us, 4.9
+// TB/s, and 500000 x 128 82 us, 5.4 TB/s: the memory's rate.  44440 x 128 in bf16
+// (23 MB) takes 8 us, half of it start and drain; up to 256 rows take 2.5 to 5.5
+// us, a load's, a reduction's and a store's latency.
 #include "spg_gemm_common.h"
 #include "spg_norm.h"
 #include "spg_quant_common.h"
@@ -451,7 +454,8 @@ hipError_t launch_team(const NormArgs &a, hipStream_t s)
 // before the first product); a lane keeps its columns' weights and sums of dw
 // in registers.  Every workgroup leaves one partial sum of dw, which a second
 // launch adds in the workgroups' order.  Partial sums lie as the lanes hold
-// them: element i of vector t + TEAM v at (i V + v) TEAM + t.
+// them: element i of vector t + TEAM v at (i V + v) TEAM + t.  4096 x 2048 (67 MB)
+// takes 15.4 us, 4.4 TB/s, and its partial sums (512 of 2048, in the caches) 3.9.
 template <int TEAM, int V, int U>
 __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_backward_kernel(const NormGradArgs a)
 {
@@ -633,13 +637,24 @@ int64_t norm_grad_width(int64_t H)
 hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
 {
     const int64_t H = a.H;
-    // (128-element groups are 16 lanes)
-    if (H <= 64 && a.output != SPG_NORM_E4M3_BLOCK128) return launch_team<8, 1, 4>(a, s);
+    // Few lanes a row where rows are short; a lane's vectors side by side where
+    // they are long, until a row's lanes stand in the way of other rows' loads
+    // (us, row scales / 128-element scales):
+    //   44440 x 128   16 lanes, 4 rows at once 12.4 / 12.5, 2 11.8 / 12.1, 1 10.6 / 11.6
+    //   500000 x 128  84.0 / 108, 82.4 / 106, 87.7 / 101
+    //   4096 x 2048   64 x 4 vectors 13.8 / 17.0, 256 x 1 14.2 / 18.9
+    //   4096 x 5120   256 x 3 32.8 / 41.7, 512 x 2 34.7 / 41.4, 1024 x 1 46 / 49
+    //   4096 x 8192   256 x 4 47.4 / 63.6, 512 x 2 46.6 / 60.7, 1024 x 1 52.7 / 61.1
+    // Few rows leave compute units idle, and one vector a lane has the shortest
+    // way (the kernel alone): 16 x 2048 64 x 4 4.6 / 5.2, 256 x 1 3.7 / 3.6 (1024 rows:
+    // with the launch 6.6 / 8.0, 6.3 / 6.9); 16 x 5120 256 x 3 4.8 / 5.0, 1024 x 1 4.8 /
+    // 4.6; 512 x 5120, with the launch, 6.9 / 8.0, 8.1 / 8.5.
+    if (H <= 64 && a.output != SPG_NORM_E4M3_BLOCK128) return launch_team<8, 1, 4>(a, s);    // (a group is 16 lanes)
     if (H <= 128) return launch_team<16, 1, 2>(a, s);
     if (H <= 256) return launch_team<16, 2, 1>(a, s);
     if (H <= 512) return launch_team<16, 4, 1>(a, s);
     if (H <= 1024) return launch_team<64, 2, 1>(a, s);
-    if (a.R <= 256 && H <= 2048) return launch_team<256, 1, 1>(a, s);
+    if (a.R <= 1024 && H <= 2048) return launch_team<256, 1, 1>(a, s);
     if (H <= 2048) return launch_team<64, 4, 1>(a, s);
     if (a.R <= 256 && H <= 8192) return launch_team<1024, 1, 1>(a, s);
     if (H <= 4096) return launch_team<256, 2, 1>(a, s);
