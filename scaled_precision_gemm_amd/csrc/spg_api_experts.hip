@@ -243,7 +243,7 @@ int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
     if (d->experts > 1 && d->stride_o < extent(d->N, d->ldo, d->K)) return SPG_EINVAL;
     if (add && d->experts > 1 && d->stride_a < extent(d->N, d->lda, d->K)) return SPG_EINVAL;
     // tiles are counted in 32 bits
-    if ((d->experts * cdiv(d->N, 128) + 8) * cdiv(d->K, kDwTile) >= kMaxIndex / kDwMaxSlices) return SPG_EUNSUPPORTED;
+    if ((d->experts * cdiv(d->N, 128) + 64) * cdiv(d->K, kDwTile) >= kMaxIndex / kDwMaxSlices) return SPG_EUNSUPPORTED;
     return SPG_OK;
 }
 
@@ -312,6 +312,12 @@ SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const i
     a.div_n = make_fastdiv(a.tiles_n);
     a.div_k = make_fastdiv(a.tiles_k);
     a.div_slice = make_fastdiv((uint32_t)a.slices);
+    // two or four rows of tiles of an expert to an XCD where all eight get eight
+    // such units (us, bf16: 64 experts' 2048 x 2048 over 32768 gathered rows, 1 / 2 /
+    // 4 / 8 rows 333 / 325 / 319 / 327; 16 experts' over 16384, 128 rows of tiles, 144 /
+    // 136 / 147 / 187; one expert's 16 rows of tiles 875 / 879 / 1650)
+    const int64_t rows_of_tiles = d->experts * p.slices * p.tiles_n;
+    a.unit = p.tiles_n >= 4 && rows_of_tiles >= 256 ? 2 : p.tiles_n >= 2 && rows_of_tiles >= 128 ? 1 : 0;
     return launch_grouped_dw(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 

@@ -18,6 +18,7 @@ struct GroupedDwArgs {
     int32_t slices;                     // parts of every expert's rows, summed by a second launch
     int32_t tile_n;                     // tiles of tile_n (128 or 256) n x 256 k
     uint32_t tiles_n, tiles_k;          // tiles of one expert
+    int32_t unit;                       // 2^unit rows of tiles are dealt to an XCD together
     FastDiv div_k, div_n, div_slice;    // by tiles_k, tiles_n, slices
 };
 constexpr int kDwTile = 256;             // k of a tile

@@ -27,7 +27,7 @@
 // What bounds it: long sums the power limit, 32768 rows x 4096 x 4096 870 us, 1.27
 // PFLOP/s, MFMAs busy 68 % at 1.63 GHz (without the copies 720 us, 82 % at 1.645;
 // three, four or five slots, and copies that all hit the L2, alike).  64 experts'
-// 2048 x 2048 over 512 rows each, 310-340 us, 38 %: sixteen stages of 1570 cycles
+// 2048 x 2048 over 512 rows each, 290-320 us, 40 %: sixteen stages of 1570 cycles
 // a tile and 5400 for its end, whose output of 537 MB takes 103 us at the memory's
 // rate; fewer cycles there (no zeroing of accumulators, an epilogue in two
 // regions) lower the clock, not the time.  Few rows an expert: the output at 5.2
@@ -105,11 +105,10 @@ struct DwTile {
 };
 
 // Tile i of this XCD.  Tiles come in the order expert (most rows first among
-// each 64), slice, row of tiles, tile.  A row of tiles (which share their panel
-// of dY) stays on one XCD and the rows are dealt to the XCDs in turn, so every
-// XCD gets its share of every expert, however many rows that one has; eight
-// rows of tiles later it begins with the next XCD, so that an XCD does not read
-// the same columns of every expert.
+// each 64), slice, row of tiles, tile.  2^unit consecutive rows of tiles stay on
+// one XCD, whose L2 then reads an expert's X once for all of them; they are dealt
+// to the XCDs in turn, from the first to the last and back, so that all get
+// about as much, however uneven the experts.
 template <int OUT, int MIN>
 __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, uint32_t i)
 {
@@ -117,7 +116,8 @@ __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, 
     const uint32_t j = fdiv(i, a.div_k);                          // rows of tiles of this XCD before it
     DwTile t;
     t.tk = i - j * a.tiles_k;
-    const uint32_t row = j * 8u + ((xcd + j) & 7u);
+    const uint32_t u = j >> a.unit;
+    const uint32_t row = ((u * 8u + ((u & 1u) ? 7u - xcd : xcd)) << a.unit) + (j & ((1u << a.unit) - 1u));
     const uint32_t es = fdiv(row, a.div_n);
     t.tn = row - es * a.tiles_n;
     const int place = (int)fdiv(es, a.div_slice);
@@ -576,7 +576,8 @@ hipError_t launch_tiles(const GroupedDwArgs &a, hipStream_t s)
 {
     // one workgroup per compute unit (of the 256 of an MI355X), or as many on
     // each XCD as it has tiles
-    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, most = (rows + 7) / 8 * a.tiles_k;
+    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, units = (rows + (1 << a.unit) - 1) >> a.unit;
+    const int64_t most = ((units + 7) / 8 << a.unit) * a.tiles_k;
     const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
     if (a.slices == 1) return a.out_fp32 ? launch_out<TN, kOutFp32>(a, grid, s) : launch_out<TN, kOutBf16>(a, grid, s);
     hipError_t e = launch_out<TN, kOutPartial>(a, grid, s);

@@ -126,6 +126,20 @@ def test_more_tiles_than_compute_units(spg, counts, N, K, gather):
     run(spg, counts, N, K, gather, seed=N, tail=3, head=1)
 
 
+@pytest.mark.parametrize("gather", [False, True], ids=["in_order", "gathered"])
+@pytest.mark.parametrize("counts,N,K", [([40, 0, 70] * 23, 1288, 264), ([300, 1, 64, 0] * 17, 1032, 520), ([50] * 43, 776, 264),
+                                        ([0] * 31 + [900] + [0] * 33, 2048, 264)])
+def test_rows_of_tiles_dealt_together(spg, counts, N, K, gather):
+    # two or four rows of tiles an XCD, across experts' borders, the last unit not whole
+    run(spg, counts, N, K, gather, seed=K, tail=2)
+
+
+@pytest.mark.parametrize("R,N,K,E", [(32768, 2048, 256, 1), (16384, 1024, 256, 2)])
+def test_parts_dealt_together(spg, R, N, K, E):
+    assert spg.grouped_dw_workspace(R, E, N, K) is not None
+    run(spg, [R] if E == 1 else [R - 77, 77], N, K, E == 2, F32, seed=E)
+
+
 @pytest.mark.parametrize("last", [1, 33, 97, 129, 161, 1025, 1057, 1153])
 def test_chunks_of_row_numbers(spg, last):
     # 1024 rows a chunk: tiles that end right behind a border, followed by others
