@@ -168,6 +168,48 @@ def test_nan_and_infinity_stay_in_their_row(spg, H):
     assert not bool(torch.isfinite(g.scale[:, 5]).any()) and not bool(torch.isfinite(g.scale[-1, 40]))
 
 
+@pytest.mark.parametrize("w0", [0.0, 1.0])
+@pytest.mark.parametrize("output", ["e4m3_row", "e4m3_block128"])
+def test_codes_of_fp32_weights(spg, output, w0):
+    # products that 32 bits do not hold: zero rows, both ends of the range, weights that overflow y
+    for std in (1e-38, 1e-10, 1e19, 5e37):
+        run(spg, 9, 1040, output, wt=F32, w0=w0, std=std, residual=False, normed=True)
+    for R, H in ((5, 16), (9, 208), (300, 400), (7, 1040), (1100, 2048), (9, 4096), (5, 9216), (3, 20000)):
+        run(spg, R, H, output, wt=F32, w0=w0, normed=True, seed=H)
+    x, w = rand((6, 2048), 1), rand((2048,), 2, dtype=F32)
+    x[2] = 0.0
+    x[3, 128:] = -0.0
+    y = ref_forward(x, w, None, 1e-6, w0)[2]
+    g = spg.rms_norm(x, w, output=output, weight_offset=w0)
+    check_codes(spg, g.out, g.scale, y, output)
+    big = torch.full((2048,), 3e38, device="cuda")
+    g = spg.rms_norm(x, big, output=output, weight_offset=w0)     # some |h rstd| of every other row are over 1.2
+    rows = g.scale if output == "e4m3_row" else g.scale.amax(0)
+    assert bool(torch.isinf(rows[[0, 1, 4, 5]]).all()) and float(rows[2]) == 0.0
+
+
+@pytest.mark.parametrize("w0", [0.0, 1.0])
+@pytest.mark.parametrize("H", [256, 1040, 2048, 5120, 16384])
+def test_nan_and_infinity_with_fp32_weights(spg, H, w0):
+    x, w = rand((70, H), 3), rand((H,), 4, dtype=F32)
+    y = ref_forward(x, w, None, 1e-6, w0)[2]
+    bad = [5, 40]
+    x[5, H // 2] = float("nan")
+    x[40, H - 1] = float("inf")
+    keep = [i for i in range(70) if i not in bad]
+    g = spg.rms_norm(x, w, output="e4m3_row", weight_offset=w0)
+    check_codes(spg, g.out[keep], g.scale[keep], y[keep], "e4m3_row")
+    assert not bool(torch.isfinite(g.scale[bad]).any())
+    g = spg.rms_norm(x, w, output="e4m3_block128", weight_offset=w0)
+    check_codes(spg, g.out[keep], g.scale[:, keep].contiguous(), y[keep], "e4m3_block128")
+    assert not bool(torch.isfinite(g.scale[:, 5]).any()) and not bool(torch.isfinite(g.scale[-1, 40]))
+    # a weight that is no number: its group alone
+    w[H - 1] = float("nan")
+    x = rand((3, H), 5)
+    g = spg.rms_norm(x, w, output="e4m3_block128", weight_offset=w0)
+    assert not bool(torch.isfinite(g.scale[-1]).any()) and bool(torch.isfinite(g.scale[:-1]).all())
+
+
 @pytest.mark.parametrize("output", ["bf16", "e4m3_row", "e4m3_block128"])
 @pytest.mark.parametrize("R,H", [(3, 1040), (300, 2048), (70, 128)])
 def test_strides_and_guards(spg, R, H, output):
