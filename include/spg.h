@@ -569,12 +569,12 @@ int expert_combine_backward(const void *grad_out, int64_t ldg, const void *y, in
  *          SPG_NORM_E4M3_BLOCK128 : the same per 128 elements of a row: A of
  *                                   SPG_FMT_E4M3_BLOCK128; scale [ceil(H /
  *                                   128), R], group-major
- * y is fp32 and is rounded once, to the output's type (the codes are not those
- * of the rounded bf16 y); the squares are summed in 64 bits.  A row that
- * holds a NaN or an infinity, or whose y overflows fp32, gets a scale (of its
- * row, or of every group that such a y is in) that is NaN or infinite.  Codes
- * of an all-zero row or group are signed zeros with scale 0.  A row of zeros with
- * eps = 0 is 0 times infinity: NaN.
+ * y is rounded once, to the output's type (the codes are not those of the rounded
+ * bf16 y, and their quotient is by the unrounded scale); the squares are summed in
+ * 64 bits.  A row that holds a NaN or an infinity, or whose y overflows fp32,
+ * gets a scale (of its row, or of every group that such a y is in) that is NaN or
+ * infinite.  Codes of an all-zero row or group are signed zeros with scale 0.  A
+ * row of zeros with eps = 0 is 0 times infinity: NaN.
  *   x, residual : bf16 [R, H], row strides ldx, ldr; residual or NULL
  *   weight   : [H], bf16 or (weight_fp32) fp32, contiguous
  *   h        : bf16 [R, H], row stride ldh: with a residual required, without

@@ -253,6 +253,36 @@ def test_large_operands(spg):
     assert bool((out[:299] == 0).all())
 
 
+def test_gathered_to_the_last_row_below_the_limit(spg):
+    # X of 2^30 - 2048 elements: byte offsets up to 2^31
+    T, K, N = (1 << 19) - 1, 2048, 264
+    x = torch.empty((T, K), dtype=BF, device="cuda")
+    at = [T - 1, 0, T - 2, T // 2, T - 1, T - 33, T, 1 << 30]      # the last two stand for zeros
+    dy, rows = rand((len(at), N), 1), i32(at)
+    for i, r in enumerate(sorted(set(at[:6]))):
+        x[r] = rand((K,), 10 + i)
+    out = spg.gemm_grouped_dw(dy, x, i32([0, 3, 8]), rows=rows, dtype=F32)
+    some = torch.stack([x[r] if r < T else torch.zeros_like(x[0]) for r in at])
+    y, S = ref(dy, some, [0, 3, 8])
+    check(out, y, S, 5)
+
+
+def test_most_experts(spg):
+    # 65536 experts in groups of 64 sorted by their rows; nearly all without any
+    E, N, K, R = 65536, 8, 16, 3000
+    counts = np.zeros(E, dtype=np.int64)
+    np.add.at(counts, np.random.default_rng(1).integers(0, E, 300), 10)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    dy, x = rand((R, N), 1), rand((R, K), 2)
+    add = rand((E, N, K), 3)
+    out = spg.gemm_grouped_dw(dy, x, i32(off), add=add)
+    full = np.nonzero(counts)[0]
+    y, S = ref(dy, x, np.concatenate([[0], np.cumsum(counts[full])]), None, add[torch.as_tensor(full, device="cuda")])
+    check(out[torch.as_tensor(full, device="cuda")], y, S, int(counts.max()))
+    empty = torch.as_tensor(counts == 0, device="cuda")
+    assert torch.equal(out[empty], add[empty])
+
+
 def test_captured_and_replayed_with_other_routings(spg):
     E, N, K, T, top = 8, 264, 512, 100, 2
     dy, x = rand((T * top, N), 1), rand((T, K), 2)
