@@ -312,12 +312,24 @@ SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const i
     a.div_n = make_fastdiv(a.tiles_n);
     a.div_k = make_fastdiv(a.tiles_k);
     a.div_slice = make_fastdiv((uint32_t)a.slices);
-    // two or four rows of tiles of an expert to an XCD where all eight get eight
-    // such units (us, bf16: 64 experts' 2048 x 2048 over 32768 gathered rows, 1 / 2 /
-    // 4 / 8 rows 333 / 325 / 319 / 327; 16 experts' over 16384, 128 rows of tiles, 144 /
-    // 136 / 147 / 187; one expert's 16 rows of tiles 875 / 879 / 1650)
+    // Units of four rows of tiles, or two, and about eight tiles of a row, where
+    // every XCD gets eight of them, or one expert's tiles, which are alike, come out
+    // even; else single rows of tiles (us, bf16: 64 experts' 8 x 8 tiles over 32768
+    // gathered rows, units of 1 / 2 / 4 / 8 rows 333 / 325 / 319 / 327; 16 experts'
+    // over 16384 rows, 128 rows of tiles, 144 / 136 / 147 / 187; one expert's 16 x 16
+    // over 32768 rows 848, 4 x 8 835; 32 x 32 over 8192 rows 855, 4 x 8 832).
     const int64_t rows_of_tiles = d->experts * p.slices * p.tiles_n;
-    a.unit = p.tiles_n >= 4 && rows_of_tiles >= 256 ? 2 : p.tiles_n >= 2 && rows_of_tiles >= 128 ? 1 : 0;
+    int32_t parts = 0;
+    while ((p.tiles_k >> parts) % 2 == 0 && (p.tiles_k >> parts) > 8) ++parts;
+    for (int32_t n = 2; n >= 1 && a.unit_n == 0; --n) {
+        const int64_t units = cdiv(rows_of_tiles, 1 << n) << parts;
+        const bool even = d->experts == 1 && rows_of_tiles % (1 << n) == 0 && units % 8 == 0;
+        if (p.tiles_n >= (1 << n) && (units >= 64 || even)) {
+            a.unit_n = n;
+            a.unit_k = parts;
+        }
+    }
+    a.div_width = make_fastdiv(a.tiles_k >> a.unit_k);
     return launch_grouped_dw(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 

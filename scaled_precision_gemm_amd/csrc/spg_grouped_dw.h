@@ -18,8 +18,9 @@ struct GroupedDwArgs {
     int32_t slices;                     // parts of every expert's rows, summed by a second launch
     int32_t tile_n;                     // tiles of tile_n (128 or 256) n x 256 k
     uint32_t tiles_n, tiles_k;          // tiles of one expert
-    int32_t unit;                       // 2^unit rows of tiles are dealt to an XCD together
+    int32_t unit_n, unit_k;             // dealt to an XCD together: tiles_k / 2^unit_k tiles of 2^unit_n rows of tiles
     FastDiv div_k, div_n, div_slice;    // by tiles_k, tiles_n, slices
+    FastDiv div_width;                  // by tiles_k / 2^unit_k
 };
 constexpr int kDwTile = 256;             // k of a tile
 constexpr int kDwMaxSlices = 16;

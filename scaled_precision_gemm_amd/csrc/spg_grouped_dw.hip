@@ -105,19 +105,21 @@ struct DwTile {
 };
 
 // Tile i of this XCD.  Tiles come in the order expert (most rows first among
-// each 64), slice, row of tiles, tile.  2^unit consecutive rows of tiles stay on
-// one XCD, whose L2 then reads an expert's X once for all of them; they are dealt
-// to the XCDs in turn, from the first to the last and back, so that all get
-// about as much, however uneven the experts.
+// each 64), slice, row of tiles, tile.  Units of 2^unit_n consecutive rows of
+// tiles, each row cut into 2^unit_k parts, stay on one XCD, whose L2 then reads the
+// unit's X and dY once for all of its tiles; units are dealt to the XCDs in turn,
+// from the first to the last and back, so that all get about as much, however
+// uneven the experts.
 template <int OUT, int MIN>
 __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, uint32_t i)
 {
     const uint32_t xcd = blockIdx.x & 7u;
-    const uint32_t j = fdiv(i, a.div_k);                          // rows of tiles of this XCD before it
+    const uint32_t width = a.tiles_k >> a.unit_k;
+    const uint32_t j = fdiv(i, a.div_width);                      // units' rows of this XCD before it
+    const uint32_t turn = j >> a.unit_n, u = turn * 8u + ((turn & 1u) ? 7u - xcd : xcd);
     DwTile t;
-    t.tk = i - j * a.tiles_k;
-    const uint32_t u = j >> a.unit;
-    const uint32_t row = ((u * 8u + ((u & 1u) ? 7u - xcd : xcd)) << a.unit) + (j & ((1u << a.unit) - 1u));
+    t.tk = i - j * width + (u & ((1u << a.unit_k) - 1u)) * width;
+    const uint32_t row = ((u >> a.unit_k) << a.unit_n) + (j & ((1u << a.unit_n) - 1u));
     const uint32_t es = fdiv(row, a.div_n);
     t.tn = row - es * a.tiles_n;
     const int place = (int)fdiv(es, a.div_slice);
@@ -576,8 +578,8 @@ hipError_t launch_tiles(const GroupedDwArgs &a, hipStream_t s)
 {
     // one workgroup per compute unit (of the 256 of an MI355X), or as many on
     // each XCD as it has tiles
-    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, units = (rows + (1 << a.unit) - 1) >> a.unit;
-    const int64_t most = ((units + 7) / 8 << a.unit) * a.tiles_k;
+    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, units = ((rows + (1 << a.unit_n) - 1) >> a.unit_n) << a.unit_k;
+    const int64_t most = ((units + 7) / 8 << a.unit_n) * (a.tiles_k >> a.unit_k);
     const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
     if (a.slices == 1) return a.out_fp32 ? launch_out<TN, kOutFp32>(a, grid, s) : launch_out<TN, kOutBf16>(a, grid, s);
     hipError_t e = launch_out<TN, kOutPartial>(a, grid, s);

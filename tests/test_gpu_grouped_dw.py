@@ -134,6 +134,14 @@ def test_rows_of_tiles_dealt_together(spg, counts, N, K, gather):
     run(spg, counts, N, K, gather, seed=K, tail=2)
 
 
+@pytest.mark.parametrize("gather", [False, True], ids=["in_order", "gathered"])
+@pytest.mark.parametrize("counts,N,K", [([130], 4096, 4096), ([130], 2048, 4096), ([99], 2056, 4096), ([70], 4096, 8192),
+                                        ([40, 0, 130, 33, 1, 64, 7], 4096, 4096), ([20] * 9, 2312, 4104), ([33], 1024, 8200)])
+def test_parts_of_rows_of_tiles(spg, counts, N, K, gather):
+    # wide outputs: a row of tiles in two or four parts, or whole, on several XCDs
+    run(spg, counts, N, K, gather, seed=N, tail=1)
+
+
 @pytest.mark.parametrize("R,N,K,E", [(32768, 2048, 256, 1), (16384, 1024, 256, 2)])
 def test_parts_dealt_together(spg, R, N, K, E):
     assert spg.grouped_dw_workspace(R, E, N, K) is not None
