@@ -24,9 +24,9 @@
 //    serves any routing.  Workgroups stay and take tile after tile, copying the
 //    next one's first stages under the last one's end.
 //
-// What bounds it: long sums the power limit, 32768 rows x 4096 x 4096 870 us, 1.27
+// What bounds it: long sums the power limit, 32768 rows x 4096 x 4096 835-865 us, 1.3
 // PFLOP/s, MFMAs busy 68 % at 1.63 GHz (without the copies 720 us, 82 % at 1.645;
-// three, four or five slots, and copies that all hit the L2, alike).  64 experts'
+// with copies that all hit the L2 800; three, four or five slots alike).  64 experts'
 // 2048 x 2048 over 512 rows each, 290-320 us, 40 %: sixteen stages of 1570 cycles
 // a tile and 5400 for its end, whose output of 537 MB takes 103 us at the memory's
 // rate; fewer cycles there (no zeroing of accumulators, an epilogue in two
