@@ -190,40 +190,6 @@ SPG_EXPORT int gemm_grouped(void *out, const void *A, const float *sa, const voi
 
 namespace {
 
-// Tiles of 256 n x 256 k; 128 n where those would leave half of the compute
-// units (256 on an MI355X) idle (fp32, us: 4096 x 2048 over 4000 rows 97 -> 76, 8
-// experts of 1024 x 512 and 1024 rows 28.5 -> 23.7; 5120 x 5120 over 4096 rows, 400
-// tiles, 221 -> 265).  Those experts' rows are cut into s parts, at most one a unit:
-// a tile's walk takes rows / 76 us, which s divides, the second launch 3 us, and
-// every partial tile 0.06 (512 x 512 over 4096 rows, 8 tiles: s = 1 58 us, 4 23, 8
-// 19, 16 20; 2048 x 2048 over 4096 rows, 128 tiles: 1 65, 2 53; over 1024 rows 22.7
-// and 29.6).
-struct DwPlan {
-    int32_t tile_n, slices;
-    int64_t tiles_n, tiles_k, tiles;
-};
-DwPlan dw_plan(const spg_grouped_dw_desc *d)
-{
-    DwPlan p = {256, 1, cdiv(d->N, 256), cdiv(d->K, kDwTile), 0};
-    if (d->experts * p.tiles_n * p.tiles_k <= 128) {
-        p.tile_n = 128;
-        p.tiles_n = cdiv(d->N, 128);
-    }
-    p.tiles = d->experts * p.tiles_n * p.tiles_k;
-    if (p.tiles == 0) return p;
-    const int64_t rows = d->rows / d->experts, units = 256 / p.tiles;
-    const int64_t most = units < kDwMaxSlices ? units : kDwMaxSlices;
-    int64_t best = rows * 100 / 76;                         // hundredths of a us
-    for (int64_t s = 2; s <= most; ++s) {
-        const int64_t t = rows * 100 / (76 * s) + 300 + 6 * p.tiles * s;
-        if (t < best) {
-            best = t;
-            p.slices = (int32_t)s;
-        }
-    }
-    return p;
-}
-
 int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
 {
     if (!d) return SPG_EINVAL;
@@ -251,9 +217,11 @@ int validate_dw(const spg_grouped_dw_desc *d, bool gathered, bool add)
 
 SPG_EXPORT size_t gemm_grouped_dw_workspace_bytes(const spg_grouped_dw_desc *d)
 {
-    if (validate_dw(d, false, false) != SPG_OK) return 0;
-    const DwPlan p = dw_plan(d);
-    return p.slices > 1 ? (size_t)p.tiles * p.slices * p.tile_n * kDwTile * sizeof(float) : 0;
+    if (validate_dw(d, false, false) != SPG_OK || d->N == 0 || d->K == 0) return 0;
+    GroupedDwArgs a;
+    plan_grouped_dw(*d, a);
+    const size_t tiles = (size_t)d->experts * a.tiles_n * a.tiles_k;
+    return a.slices > 1 ? tiles * a.slices * a.tile_n * kDwTile * sizeof(float) : 0;
 }
 
 SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const int32_t *offsets, const int32_t *row_index,
@@ -304,32 +272,7 @@ SPG_EXPORT int gemm_grouped_dw(void *out, const void *dY, const void *X, const i
     const int64_t line = d->out_fp32 ? 32 : 64;
     a.lines = ((uintptr_t)out & 127u) == 0 && d->ldo % line == 0 && d->stride_o % line == 0 &&
               (!add || (((uintptr_t)add & 127u) == 0 && d->lda % line == 0 && d->stride_a % line == 0));
-    const DwPlan p = dw_plan(d);
-    a.slices = p.slices;
-    a.tile_n = p.tile_n;
-    a.tiles_n = (uint32_t)p.tiles_n;
-    a.tiles_k = (uint32_t)p.tiles_k;
-    a.div_n = make_fastdiv(a.tiles_n);
-    a.div_k = make_fastdiv(a.tiles_k);
-    a.div_slice = make_fastdiv((uint32_t)a.slices);
-    // Units of four rows of tiles, or two, and about eight tiles of a row, where
-    // every XCD gets eight of them, or one expert's tiles, which are alike, come out
-    // even; else single rows of tiles (us, bf16: 64 experts' 8 x 8 tiles over 32768
-    // gathered rows, units of 1 / 2 / 4 / 8 rows 333 / 325 / 319 / 327; 16 experts'
-    // over 16384 rows, 128 rows of tiles, 144 / 136 / 147 / 187; one expert's 16 x 16
-    // over 32768 rows 848, 4 x 8 835; 32 x 32 over 8192 rows 855, 4 x 8 832).
-    const int64_t rows_of_tiles = d->experts * p.slices * p.tiles_n;
-    int32_t parts = 0;
-    while ((p.tiles_k >> parts) % 2 == 0 && (p.tiles_k >> parts) > 8) ++parts;
-    for (int32_t n = 2; n >= 1 && a.unit_n == 0; --n) {
-        const int64_t units = cdiv(rows_of_tiles, 1 << n) << parts;
-        const bool even = d->experts == 1 && rows_of_tiles % (1 << n) == 0 && units % 8 == 0;
-        if (p.tiles_n >= (1 << n) && (units >= 64 || even)) {
-            a.unit_n = n;
-            a.unit_k = parts;
-        }
-    }
-    a.div_width = make_fastdiv(a.tiles_k >> a.unit_k);
+    plan_grouped_dw(*d, a);
     return launch_grouped_dw(a, (hipStream_t)stream) == hipSuccess ? SPG_OK : SPG_EHIP;
 }
 

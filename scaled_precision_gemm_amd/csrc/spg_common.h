@@ -102,7 +102,10 @@ struct FastDiv {
 };
 
 // n / d for n < 2^31 with a FastDiv of d (multiply-high, add, shift).
-__device__ __forceinline__ uint32_t fdiv_q(uint32_t n, const FastDiv &f) { return (__umulhi(n, f.m) + n) >> f.s; }
+__host__ __device__ __forceinline__ uint32_t fdiv_q(uint32_t n, const FastDiv &f)
+{
+    return ((uint32_t)((uint64_t)n * f.m >> 32) + n) >> f.s;
+}
 
 struct GemmArgs {
     void *out;

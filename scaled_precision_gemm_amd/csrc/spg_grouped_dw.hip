@@ -104,26 +104,16 @@ struct DwTile {
     int nk, np;
 };
 
-// Tile i of this XCD.  Tiles come in the order expert (most rows first among
-// each 64), slice, row of tiles, tile.  Units of 2^unit_n consecutive rows of
-// tiles, each row cut into 2^unit_k parts, stay on one XCD, whose L2 then reads the
-// unit's X and dY once for all of its tiles; units are dealt to the XCDs in turn,
-// from the first to the last and back, so that all get about as much, however
-// uneven the experts.
+// Tile i of this XCD's list (dw_place).
 template <int OUT, int MIN>
 __device__ __forceinline__ DwTile dw_tile(const GroupedDwArgs &a, DwExperts &w, uint32_t i)
 {
-    const uint32_t xcd = blockIdx.x & 7u;
-    const uint32_t width = a.tiles_k >> a.unit_k;
-    const uint32_t j = fdiv(i, a.div_width);                      // units' rows of this XCD before it
-    const uint32_t turn = j >> a.unit_n, u = turn * 8u + ((turn & 1u) ? 7u - xcd : xcd);
+    const DwPlace at = dw_place(a, blockIdx.x & 7u, i);
+    const int place = (int)at.place;
     DwTile t;
-    t.tk = i - j * width + (u & ((1u << a.unit_k) - 1u)) * width;
-    const uint32_t row = ((u >> a.unit_k) << a.unit_n) + (j & ((1u << a.unit_n) - 1u));
-    const uint32_t es = fdiv(row, a.div_n);
-    t.tn = row - es * a.tiles_n;
-    const int place = (int)fdiv(es, a.div_slice);
-    t.slice = (int)(es - (uint32_t)place * (uint32_t)a.slices);
+    t.tk = at.tk;
+    t.tn = at.tn;
+    t.slice = (int)at.slice;
     t.e = -1;
     t.r0 = t.r1 = 0;
     t.nk = 0;
@@ -160,12 +150,9 @@ __global__ __launch_bounds__(kDwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
     // ---- this workgroup's tiles: one of every `step` of its XCD's, from the
     // front and from the back in turn: with the experts in the order of their
     // rows, all workgroups get about as much
-    const uint32_t step = gridDim.x >> 3, first_item = blockIdx.x >> 3;
     DwExperts experts = dw_experts(a, 0);
     uint32_t round = 0;
-    auto tile = [&](uint32_t k) {
-        return dw_tile<OUT, kMin>(a, experts, k * step + ((k & 1) ? step - 1 - first_item : first_item));
-    };
+    auto tile = [&](uint32_t k) { return dw_tile<OUT, kMin>(a, experts, dw_item(gridDim.x, blockIdx.x, k)); };
     DwTile cur = tile(0);
     if (cur.e < 0) return;
     DwTile nxt = tile(++round);
@@ -576,11 +563,7 @@ hipError_t launch_out(const GroupedDwArgs &a, unsigned grid, hipStream_t s)
 template <int TN>
 hipError_t launch_tiles(const GroupedDwArgs &a, hipStream_t s)
 {
-    // one workgroup per compute unit (of the 256 of an MI355X), or as many on
-    // each XCD as it has tiles
-    const int64_t rows = (int64_t)a.E * a.slices * a.tiles_n, units = ((rows + (1 << a.unit_n) - 1) >> a.unit_n) << a.unit_k;
-    const int64_t most = ((units + 7) / 8 << a.unit_n) * (a.tiles_k >> a.unit_k);
-    const unsigned grid = (unsigned)(8 * (most < 32 ? most : 32));
+    const unsigned grid = dw_grid(a);
     if (a.slices == 1) return a.out_fp32 ? launch_out<TN, kOutFp32>(a, grid, s) : launch_out<TN, kOutBf16>(a, grid, s);
     hipError_t e = launch_out<TN, kOutPartial>(a, grid, s);
     if (e != hipSuccess) return e;

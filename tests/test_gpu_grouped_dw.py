@@ -339,3 +339,23 @@ def test_two_streams(spg):
                 got[i].append(spg.gemm_grouped_dw(*args[i]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["in_order", "gathered"])
+@pytest.mark.parametrize("counts,N,K", [([40], 3584, 28672), ([33], 3328, 28672), ([33, 0, 7], 1280, 32768), ([9, 1, 0, 40, 3], 1280, 20480)])
+def test_wide_outputs_are_whole(spg, counts, N, K, gather):
+    # rows of tiles in eight parts and more, the last unit of rows of tiles not whole; every element written
+    E, R = len(counts), sum(counts) + 2
+    off, T = np.concatenate([[0], np.cumsum(counts)]), R // 2 if gather else R
+    dy, x = rand((R, N), 1), rand((T, K), 2)
+    rows = np.random.default_rng(N).integers(0, T, R) if gather else None
+    idx = None if rows is None else i32(rows)
+    out = torch.full((E, N, K), float("nan"), dtype=BF, device="cuda")
+    spg.gemm_grouped_dw(dy, x, i32(off), rows=idx, out=out)
+    y, S = ref(dy, x, off, rows)
+    check(out, y, S, max(counts))
+    # a second chunk, added in place
+    first = out.clone()
+    spg.gemm_grouped_dw(dy, x, i32(off), rows=idx, add=out, out=out)
+    y, S = ref(dy, x, off, rows, first)
+    check(out, y, S, max(counts) + 1)
