@@ -1066,10 +1066,10 @@ def rms_norm(x, weight, residual=None, output="bf16", eps=1e-6, weight_offset=0.
     [ceil(H/128), R], one per 128 elements of a row: the activations of
     gemm_scaled and gemm_grouped in these formats (y is rounded once, to the
     codes); H % 16 == 0.  normed (True, or a bf16 [R, H] tensor to write to)
-    asks for bf16(y) beside the codes.  h is the new residual stream, None
-    without a residual; it may be written over x or the residual (h=x,
-    h=residual), and so may a bf16 out or normed.  rstd=True keeps fp32 [R]
-    1 / sqrt(..) for rms_norm_backward."""
+    asks for bf16(y) beside the codes; False and None do not.  h is the new
+    residual stream, None without a residual; it may be written over x or the
+    residual (h=x, h=residual), and so may a bf16 out or normed.  rstd=True
+    keeps fp32 [R] 1 / sqrt(..) for rms_norm_backward."""
     def check():
         _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D bf16 tensor")
         dev = x.device
@@ -1082,7 +1082,7 @@ def rms_norm(x, weight, residual=None, output="bf16", eps=1e-6, weight_offset=0.
         _norm_weight(weight, H, dev)
         coded = output != "bf16"
         _need(not coded or H % 16 == 0, "rows of codes must be a multiple of 16 elements")
-        _need(coded or normed is False, "a bf16 output is normed itself")
+        _need(coded or not given and not normed, "a bf16 output is normed itself")
         _need(coded or scale is None, "a bf16 output has no scale")
         if residual is not None:
             _like("residual", residual, (R, H), torch.bfloat16, dev)
@@ -1105,8 +1105,10 @@ def rms_norm(x, weight, residual=None, output="bf16", eps=1e-6, weight_offset=0.
         return d, coded, want
 
     given = isinstance(normed, torch.Tensor)
-    d, coded, want = _checked(("norm", _sig(x), _sig(weight), _sig(residual), output, eps, weight_offset,
-                               _sig(normed) if given else bool(normed), _sig(out), _sig(scale), _sig(h)), check)
+    # (types beside the numbers: 0.5 equals what is refused, a Fraction for one)
+    d, coded, want = _checked(("norm", _sig(x), _sig(weight), _sig(residual), output, eps, type(eps), weight_offset,
+                               type(weight_offset), _sig(normed) if given else bool(normed), _sig(out), _sig(scale), _sig(h)),
+                              check)
     # (empty_like takes 1.2 us of host time where new_empty takes 1.8; on a
     # contiguous tensor both are contiguous)
     like = torch.empty_like if x.is_contiguous() else _new_like
@@ -1164,7 +1166,7 @@ def rms_norm_backward(grad_out, h, weight, rstd, grad_residual=None, weight_offs
         return d, lib.rms_norm_backward_workspace_bytes(R, H) if grad_weight else 0
 
     d, nws = _checked(("norm backward", _sig(grad_out), _sig(h), _sig(weight), _sig(rstd), _sig(grad_residual),
-                       weight_offset, _sig(grad_x), grad_weight), check)
+                       weight_offset, type(weight_offset), _sig(grad_x), grad_weight, type(grad_weight)), check)
     if grad_x is None:
         grad_x = (torch.empty_like if grad_out.is_contiguous() else _new_like)(grad_out)
     ws = _order_ws(workspace, nws, grad_out)

@@ -1,6 +1,8 @@
 """GPU tests of rms_norm and rms_norm_backward against plain implementations
 in 64 bits.
 """
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -425,3 +427,34 @@ def test_two_streams(spg):
     for i in range(2):
         for out in got[i]:
             assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+
+
+def test_options_are_read_alike_whatever_call_came_before(spg):
+    # two calls with tensors of the same shapes, that differ in one option alone
+    def both(refused, call, a, b):
+        for i, pair in enumerate(((a, b), (b, a))):
+            for option in pair:
+                if option in refused and any(type(option) is type(r) for r in refused):
+                    with pytest.raises(ValueError):
+                        call(i, option)
+                else:
+                    call(i, option)
+
+    w = rand((64,), 1)
+    xs = iter([[rand((n + i, 64), n + i) for i in range(2)] for n in range(1, 40, 2)])
+    for a, b in ((False, None), (False, 0)):                      # no bf16 beside a bf16 output
+        x = next(xs)
+        both([], lambda i, o: spg.rms_norm(x[i], w, normed=o), a, b)
+        x = next(xs)
+        both([], lambda i, o: spg.rms_norm(x[i], w, output="e4m3_row", normed=o), a, b)
+    for a, b in ((False, True), (False, 1)):
+        x = next(xs)
+        both([b], lambda i, o: spg.rms_norm(x[i], w, normed=o), a, b)
+    for b in (np.float32(0.5), Fraction(1, 2), 0.5 + 0j):         # equal to a plain number, and none
+        x = next(xs)
+        both([b], lambda i, o: spg.rms_norm(x[i], w, eps=o), 0.5, b)
+        both([b], lambda i, o: spg.rms_norm(x[i], w, weight_offset=o), 0.5, b)
+        both([b], lambda i, o: spg.rms_norm_backward(x[i], x[i], w, torch.ones(len(x[i]), device="cuda"), weight_offset=o), 0.5, b)
+    for a, b in ((True, 1), (False, 0)):
+        x = next(xs)
+        both([b], lambda i, o: spg.rms_norm_backward(x[i], x[i], w, torch.ones(len(x[i]), device="cuda"), grad_weight=o), a, b)
