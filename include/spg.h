@@ -444,7 +444,10 @@ int spg_grouped_tile_rows(const spg_grouped_desc *d, int epilogue);
  * N % 8 == 0, K % 8 == 0, 1 <= experts <= 65536.  The order of the sums depends
  * on the sizes and offsets alone: the same call gives the same bits.  Each
  * element within 2^-8 |y| (bf16; 2^-24 fp32) + 2^-12 S of the exact value y, S
- * the sum of |products|, and |add|.
+ * the sum of |products|, and |add|; for an expert of more than 16384 rows 2^-12
+ * becomes rows 2^-26: every eight products join the fp32 sum with a rounding of
+ * their own (2^20 rows that are all alike came out 2^-9 S off, random ones of one
+ * sign 2^-15 S, of both 2^-24 S).
  */
 typedef struct spg_grouped_dw_desc {
     int64_t rows, x_rows, N, K;

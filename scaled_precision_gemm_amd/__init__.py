@@ -812,7 +812,8 @@ def gemm_grouped_dw(dY, X, offsets, rows=None, add=None, out=None, dtype=torch.b
     """The weight gradients of gemm_grouped's products, from bf16 operands:
     out[e] = add[e] + sum over r in [offsets[e], offsets[e + 1]) of dY[r]^T
     X[rows[r]] (X[r] without rows), [experts, N, K] in `dtype` (bf16 or fp32);
-    fp32 sums, one rounding.
+    fp32 sums, one rounding at their end (an expert of far more than 16384 rows
+    that are alike is better cut into calls that add in fp32).
 
     dY bf16 [R, N] in expert order; X bf16 [T, K]; offsets int32 [experts + 1]
     and rows int32 [R] as expert_route returns them (an index outside X stands

@@ -359,3 +359,26 @@ def test_wide_outputs_are_whole(spg, counts, N, K, gather):
     spg.gemm_grouped_dw(dy, x, i32(off), rows=idx, add=out, out=out)
     y, S = ref(dy, x, off, rows, first)
     check(out, y, S, max(counts) + 1)
+
+
+@pytest.mark.parametrize("kind", ["alike", "outlier", "random"])
+@pytest.mark.parametrize("R", [16384, 32768 + 16, 131072, 1 << 20, (1 << 21) - 40])
+@pytest.mark.parametrize("E", [1, 129], ids=["in_parts", "whole"])
+def test_long_sums(spg, R, E, kind):
+    # sums whose roundings all fall the same way: rows that are alike, and rows each below half a step of a first
+    # one's product.  Per element half a step of fp32, and per eight products one rounding of the sum so far,
+    # 2^-24 of it, with up to 2^-4 of a step lost where they are aligned: rows / 8 of them, 1.125 2^-24 S each,
+    # below rows 2^-26 S (rows in parts: at most 16 further ones, below 2^-19 S, within what is left of that)
+    dy, x = rand((R, 8), 1), rand((R, 16), 2)
+    if kind != "random":
+        dy.fill_(1 + 7 / 128 if kind == "alike" else 0.124)
+        x.fill_(1 + 9 / 128 if kind == "alike" else 1.0)
+    if kind == "outlier":
+        dy[0], x[0] = 4096.0, 4096.0
+    off = [0] + [R] * E
+    assert (spg.grouped_dw_workspace(R, E, 8, 16) is None) == (E > 1)
+    out = spg.gemm_grouped_dw(dy, x, i32(off), dtype=F32)
+    y, S = torch.matmul(dy.double().t(), x.double()), torch.matmul(dy.double().abs().t(), x.double().abs())
+    off_by = (out[0].double() - y).abs()
+    assert bool((off_by <= 2.0 ** -24 * y.abs() + max(2.0 ** -12, R * 2.0 ** -26) * S).all()), float((off_by / S).max())
+    assert not bool(out[1:].any())
