@@ -121,7 +121,7 @@ int run_gradients(const spg_gradient *list, int64_t count, bool clip, double max
     const Range outs[] = {{norm, 4}, {ws, (int64_t)need}};
     const int o = overlaps(list, count, clip, outs, 2);
     if (o != SPG_OK) return o;
-    float *const factor = clip ? (float *)ws : nullptr;
+    GradFactor *const factor = clip ? (GradFactor *)ws : nullptr;
     double *const partials = (double *)((uint8_t *)ws + kHead);
     const hipStream_t s = (hipStream_t)stream;
     int64_t at = 0;

@@ -23,11 +23,19 @@ struct GradTensors {
     int32_t count;
 };
 
+// What gradients are scaled by: f 2^e, e = 0 but where that is below fp32's normal
+// range (f then in [1/2, 1)).
+struct GradFactor {
+    float f;
+    int32_t e;
+};
+
 hipError_t launch_grad_sums(const GradTensors &t, double *partials, hipStream_t s);
 // norm[0] = the root of the partial sums' sum; factor[0], where given, what scales the gradients
-hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, float *factor, hipStream_t s);
+hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, GradFactor *factor,
+                            hipStream_t s);
 // By *factor; or, partials given, by the factor of their sum (parts of them), and norm[0] where given as above.
-hipError_t launch_grad_scale(const GradTensors &t, const float *factor, const double *partials, int64_t parts, double max_norm,
+hipError_t launch_grad_scale(const GradTensors &t, const GradFactor *factor, const double *partials, int64_t parts, double max_norm,
                              float *norm, hipStream_t s);
 
 inline int64_t grad_parts(int64_t chunks) { return chunks < kGradWorkgroups ? chunks : kGradWorkgroups; }

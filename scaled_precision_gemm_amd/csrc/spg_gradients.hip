@@ -4,6 +4,9 @@
 //   n = sqrt(sum over all tensors of g^2)        64-bit sums
 //   g' = g (n > max ? max / n : 1)               fp32, one rounding to g's type
 //
+// max / n is a 64-bit quotient, held as an fp32 number and a power of two: below
+// fp32's normal range it would lose bits that g', of a large g, still has.
+//
 // A stream: every gradient is read for the sum and, where it is scaled, read
 // and written once more: 336 million bf16 elements in nine tensors take 149 us
 // for the sums and 228 for the scaling, 2.0 GB at 5.3 TB/s, what a copy reaches.
@@ -136,13 +139,16 @@ __global__ __launch_bounds__(kThreads) void grad_sums_kernel(const GradTensors t
 
 // What scales gradients of norm n.  A norm that is not finite scales nothing:
 // the caller sees it.
-__device__ __forceinline__ float factor_of(double n, double max_norm)
+__device__ __forceinline__ GradFactor factor_of(double n, double max_norm)
 {
-    return n > max_norm && n < __builtin_inf() ? (float)(max_norm / n) : 1.0f;
+    const double q = n > max_norm && n < __builtin_inf() ? max_norm / n : 1.0;
+    const int e = q > 0.0 && q < 0x1p-126 ? __builtin_amdgcn_frexp_exp(q) : 0;
+    return GradFactor{(float)__builtin_amdgcn_ldexp(q, -e), e};
 }
+__device__ __forceinline__ float scaled(float g, const GradFactor &f) { return __builtin_amdgcn_ldexpf(g * f.f, f.e); }
 
 __global__ __launch_bounds__(1024) void grad_norm_kernel(const double *partials, int64_t parts, double max_norm, float *norm,
-                                                          float *factor)
+                                                          GradFactor *factor)
 {
     __shared__ double lds[16];
     double s = 0.0;
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double *partials,
 }
 
 template <bool BF16>
-__device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float f)
+__device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, const GradFactor &f)
 {
     constexpr int W = BF16 ? 8 : 4, SIZE = BF16 ? 2 : 4;
     const uint8_t *b = (const uint8_t *)p;
@@ -171,8 +177,8 @@ __device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float
             uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                w[k] = BF16 ? gemm::pack_bf16x2(bf16_lo(w[k]) * f, bf16_hi(w[k]) * f)
-                            : __float_as_uint(__uint_as_float(w[k]) * f);
+                w[k] = BF16 ? gemm::pack_bf16x2(scaled(bf16_lo(w[k]), f), scaled(bf16_hi(w[k]), f))
+                            : __float_as_uint(scaled(__uint_as_float(w[k]), f));
             if (v < vecs) {
                 if (BF16) {
                     *reinterpret_cast<Raw16 *>(o + (int64_t)v * 16) = Raw16{{w[0], w[1], w[2], w[3]}};
@@ -188,17 +194,17 @@ __device__ __forceinline__ void chunk_scale(const void *p, void *q, int n, float
     const int at = vecs * W + (int)threadIdx.x;
     if (at < n) {
         if (BF16)
-            *(uint16_t *)(o + (int64_t)at * SIZE) = (uint16_t)f32_to_bf16(bf16_lo(*(const uint16_t *)(b + (int64_t)at * SIZE)) * f);
+            *(uint16_t *)(o + (int64_t)at * SIZE) = (uint16_t)f32_to_bf16(scaled(bf16_lo(*(const uint16_t *)(b + (int64_t)at * SIZE)), f));
         else
-            *(float *)(o + (int64_t)at * SIZE) = *(const float *)(b + (int64_t)at * SIZE) * f;
+            *(float *)(o + (int64_t)at * SIZE) = scaled(*(const float *)(b + (int64_t)at * SIZE), f);
     }
 }
 
-__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTensors t, const float *factor, const double *partials,
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTensors t, const GradFactor *factor, const double *partials,
                                                               int64_t parts, double max_norm, float *norm)
 {
     __shared__ double lds[kThreads / 64];
-    float f;
+    GradFactor f;
     if (partials) {
         double s = 0.0;
         for (int64_t i = threadIdx.x; i < parts; i += kThreads) s += partials[i];
@@ -210,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const GradTensors 
     }
     for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const int i = find_tensor(t, c);
-        if (f == 1.0f && t.src[i] == t.dst[i]) continue;        // nothing changes
+        if (f.f == 1.0f && t.src[i] == t.dst[i]) continue;        // nothing changes
         const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
         const int n = (int)min(t.n[i] - at, kGradChunk);
         if (t.bf16[i])
@@ -229,13 +235,14 @@ hipError_t launch_grad_sums(const GradTensors &t, double *partials, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, float *factor, hipStream_t s)
+hipError_t launch_grad_norm(const double *partials, int64_t parts, double max_norm, float *norm, GradFactor *factor,
+                            hipStream_t s)
 {
     grad_norm_kernel<<<1, 1024, 0, s>>>(partials, parts, max_norm, norm, factor);
     return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const GradTensors &t, const float *factor, const double *partials, int64_t parts, double max_norm,
+hipError_t launch_grad_scale(const GradTensors &t, const GradFactor *factor, const double *partials, int64_t parts, double max_norm,
                              float *norm, hipStream_t s)
 {
     const unsigned grid = (unsigned)grad_parts(t.first[t.count]);

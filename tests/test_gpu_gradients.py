@@ -196,3 +196,20 @@ def test_same_bits_and_two_streams(spg):
                 got[k].append(spg.gradient_norm(sets[k]))
     torch.cuda.synchronize()
     assert all(torch.equal(n, want[k]) for k in range(2) for n in got[k])
+
+
+@pytest.mark.parametrize("size", [1000, 9_000_000], ids=["few_parts", "many_parts"])
+@pytest.mark.parametrize("std,limit", [(1e36, 1.0), (1e37, 1e-3), (1e36, 1e-10), (1e37, 1e-30), (1e30, 1e-36)])
+def test_factors_below_the_normal_range(spg, std, limit, size):
+    # max_norm / norm from 2^-124, the last normal ones, down to 2^-234, of gradients whose scaled values are
+    # ordinary numbers and small ones
+    for dtype in (F32, BF):
+        grads = [rand(size, 1, std, dtype), rand(77, 2, std, dtype)]
+        n = norm_of(grads)
+        assert 2.0 ** -235 < limit / n < 2.0 ** -124
+        before = [g.clone() for g in grads]
+        out = [torch.full_like(g, 7.0) for g in grads]
+        spg.clip_gradients(grads, limit, out=out)
+        check_scaled(out, before, n, limit)
+        spg.clip_gradients(grads, limit)
+        assert all(torch.equal(a, b) for a, b in zip(grads, out))
