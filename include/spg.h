@@ -646,8 +646,10 @@ int rms_norm_backward(const void *grad_out, const void *h, const void *grad_resi
  * squares are formed and added in 64 bits.
  * clip_gradients - the same, and dst = src f for every tensor, f = n > max_norm ?
  * max_norm / n : 1 (24 bits of it, also below fp32's normal range), one product
- * in fp32 rounded to the tensor's type.  Where n is not finite, f = 1: the
- * gradients stay as they are, and the caller sees norm.
+ * in fp32 rounded to the tensor's type.  n is held in 64 bits, where it is NaN or
+ * infinite only if a gradient is: then f = 1, the gradients stay as they are, and
+ * norm is NaN or infinite.  An n past fp32 makes norm infinite as well, but the
+ * gradients are scaled by it.
  *   list     : `count` tensors (host memory, read during the call); src and dst
  *              hold n contiguous elements, bf16 or fp32, aligned as one element;
  *              n may be 0 (pointers are not looked at).  gradient_norm ignores dst

@@ -1243,8 +1243,10 @@ def clip_gradients(grads, max_norm, out=None, workspace=None):
     """Scales the tensors of the list `grads` in place (or into the tensors of
     the list `out`, of the same types and numbers of elements) by max_norm / norm where their
     norm, as gradient_norm gives it, is over max_norm; returns the norm before,
-    fp32 [1] on their device.  Where the norm is not finite the gradients stay
-    as they are.  The tensors must not share memory."""
+    fp32 [1] on their device.  Where a gradient is NaN or infinite, and the
+    norm with it, the gradients stay as they are.  (Finite gradients whose norm
+    is past fp32 return infinity too, and are scaled.)  The tensors must not
+    share memory."""
     _need(isinstance(max_norm, (int, float)) and math.isfinite(max_norm) and max_norm >= 0,
           "max_norm must be a finite number, not below 0")
     return _gradients(lib.clip_gradients, "clip_gradients", grads, out, workspace, float(max_norm))

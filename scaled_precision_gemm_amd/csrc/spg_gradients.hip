@@ -137,8 +137,8 @@ __global__ __launch_bounds__(kThreads) void grad_sums_kernel(const GradTensors t
     if (threadIdx.x == 0) partials[blockIdx.x] = s;
 }
 
-// What scales gradients of norm n.  A norm that is not finite scales nothing:
-// the caller sees it.
+// What scales gradients of norm n.  A 64-bit norm that is not finite (a gradient
+// is NaN or infinite) scales nothing: the caller sees it.
 __device__ __forceinline__ GradFactor factor_of(double n, double max_norm)
 {
     const double q = n > max_norm && n < __builtin_inf() ? max_norm / n : 1.0;

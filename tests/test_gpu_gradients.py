@@ -213,3 +213,17 @@ def test_factors_below_the_normal_range(spg, std, limit, size):
         check_scaled(out, before, n, limit)
         spg.clip_gradients(grads, limit)
         assert all(torch.equal(a, b) for a, b in zip(grads, out))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1000, 9_000_000], ids=["few_parts", "many_parts"])
+def test_an_infinite_norm_tells_two_things(spg, n, dtype):
+    # finite gradients whose norm is past fp32's range: scaled.  An infinite one among them: left as they are
+    g, out = torch.full((n,), 2.0 ** 127, dtype=dtype, device="cuda"), torch.zeros(n, dtype=dtype, device="cuda")
+    assert math.isinf(float(spg.gradient_norm([g])))
+    assert math.isinf(float(spg.clip_gradients([g], 1.0, out=[out])))
+    check_scaled([out], [g], norm_of([g]), 1.0)
+    before = g.clone()
+    g[n // 2] = before[n // 2] = math.inf
+    assert math.isinf(float(spg.clip_gradients([g], 1.0))) and torch.equal(g, before)
+    assert math.isinf(float(spg.clip_gradients([g], 1.0, out=[out]))) and torch.equal(out, before)
