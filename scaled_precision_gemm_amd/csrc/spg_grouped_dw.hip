@@ -24,14 +24,20 @@
 //    serves any routing.  Workgroups stay and take tile after tile, copying the
 //    next one's first stages under the last one's end.
 //
-// What bounds it: long sums the power limit, 32768 rows x 4096 x 4096 835-865 us, 1.3
-// PFLOP/s, MFMAs busy 68 % at 1.63 GHz (without the copies 720 us, 82 % at 1.645;
-// with copies that all hit the L2 800; three, four or five slots alike).  64 experts'
-// 2048 x 2048 over 512 rows each, 290-320 us, 40 %: sixteen stages of 1570 cycles
-// a tile and 5400 for its end, whose output of 537 MB takes 103 us at the memory's
-// rate; fewer cycles there (no zeroing of accumulators, an epilogue in two
-// regions) lower the clock, not the time.  Few rows an expert: the output at 5.2
-// TB/s.
+// What bounds it (cycles of the shader clock and that clock, stamped in the same
+// launches): long sums the power limit, 32768 rows x 4096 x 4096 840-880 us, 1.3
+// PFLOP/s: 1275 cycles a stage, MFMAs 1024 of them, at 1.61 GHz (three, four or
+// five slots alike).  64 experts' 2048 x 2048 over 32768 gathered rows, 330 us, its
+// stages: a tile takes 37300 cycles at 1.93 GHz, 45 % MFMAs.  Of its 16.5 stages the
+// two behind an epilogue take 2190 each, the next two 1820, the others 1740 (with
+// copies that all hit the L2 1540); the epilogue 3500 and 1540 waiting before it,
+// 2470 to the next tile's first stage.  Equal experts, rows in order: 1410 a stage at
+// 1.72 GHz, 290-315 us.  128 x 256 tiles, 4096 x 2048 over 4000 rows: 920 a stage, MFMAs
+// 512, at 1.78-1.83 GHz (copies from the L2: 900).  So most of what stages wait for
+// lies between LDS and registers.  Added fp32 gradients: the epilogue, 31000-36000
+// cycles a tile, the memory's rate.  Few rows an expert: the output at 5.2 TB/s.
+// Gathered, added, fp32 tiles of 256 x 256 spill 8 registers (64 x 2048 x 2048 over 32768
+// rows 540 us, of which 2.3 GB at the memory's rate are 440).
 #include "spg_gemm_common.h"
 #include "spg_grouped_dw.h"
 

@@ -17,7 +17,7 @@
 // vectors of eight elements; a lane's loads are all in flight before the first
 // square.  With a residual and row scales 4096 x 5120 (147 MB) takes 30 us, 4.9
 // TB/s, and 500000 x 128 82 us, 5.4 TB/s: the memory's rate.  44440 x 128 in bf16
-// (23 MB) takes 8 us, half of it start and drain; up to 256 rows take 2.5 to 5.5
+// (23 MB) takes 8 us, half of it start and drain; up to 256 rows take 2.5 to 5.9
 // us, a load's, a reduction's and a store's latency.
 #include "spg_gemm_common.h"
 #include "spg_norm.h"
@@ -645,11 +645,16 @@ __global__ __launch_bounds__(1024) void norm_dw_reduce_kernel(const float *parti
 }
 
 // Calls f(team, vectors, rows at once) for rows of H elements: one vector a
-// lane up to 8192 elements, where the registers leave room for rows at once and
-// waves (us, 4096 x 2048: 64 lanes x 4 vectors x 2 rows 24.8, 256 x 1 x 4 19.1;
+// lane from 1024 to 8192 elements, where the registers leave room for rows at once
+// and waves (us, 4096 x 2048: 64 lanes x 4 vectors x 2 rows 24.8, 256 x 1 x 4 19.1;
 // 1111 x 8192: 256 x 4 x 2 35.7, 1024 x 1 x 2 25.3, four rows at once spill; 4096
 // x 4096: 512 x 1 x 2 32.0, x 4 37.5, 256 x 2 x 2 33.1; 4096 x 5120: 256 x 3 x 2
-// 43.4, 1024 x 1 x 2 43.5).  Rows past 16384 elements spill registers.
+// 43.4, 1024 x 1 x 2 43.5).  Shorter rows, with added gradients, in a captured graph:
+// 500000 x 64: 8 x 1 x 4 53, x 2 55, 16 x 1 x 2 86; 500000 x 128: 16 x 1 x 4 97, x 2 101,
+// 8 x 2 x 2 98; 100000 x 256: 16 x 2 x 2 44, x 1 45, 64 x 1 x 4 55; 32768 x 1024: 64 x 2 x 2
+// 53.5, x 1 56, x 4 62.5, 256 x 1 x 4 74; 32768 x 512: 16 x 4 x 2, which takes 296 registers
+// and leaves one wave a SIMD, 38, x 1 30.5, 64 x 1 x 4 30.  Rows past 16384 elements
+// spill registers: 1024 x 32768 207, 1024 x 16384 40.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>
@@ -689,16 +694,19 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
     const int64_t H = a.H;
     // Few lanes a row where rows are short; a lane's vectors side by side where
     // they are long, until a row's lanes stand in the way of other rows' loads
-    // (us, row scales / 128-element scales):
-    //   44440 x 128   16 lanes, 4 rows at once 12.4 / 12.5, 2 11.8 / 12.1, 1 10.6 / 11.6
-    //   500000 x 128  84.0 / 108, 82.4 / 106, 87.7 / 101
-    //   4096 x 2048   64 x 4 vectors 13.8 / 17.0, 256 x 1 14.2 / 18.9
-    //   4096 x 5120   256 x 3 32.8 / 41.7, 512 x 2 34.7 / 41.4, 1024 x 1 46 / 49
-    //   4096 x 8192   256 x 4 47.4 / 63.6, 512 x 2 46.6 / 60.7, 1024 x 1 52.7 / 61.1
+    // (us in a captured graph, a residual added, row scales / 128-element scales):
+    //   44440 x 128   16 lanes, 4 rows at once 13.0 / 12.5, 2 12.6 / 12.2, 1 11.3 / 10.9
+    //   500000 x 128  84.5 / 83.5, 84.5 / 82.6, 89.1 / 87.2
+    //   4096 x 2048   64 x 4 vectors 14.4 / 14.3, 256 x 1 14.4 / 14.1
+    //   4096 x 4096   256 x 2 26.5 / 27.2, 512 x 1 29.2 / 28.5, 1024 x 1 42.7 / 41.3
+    //   4096 x 5120   256 x 3 32.6 / 34.0, 512 x 2 34.7 / 35.8, 1024 x 1 46.0 / 45.6
+    //   4096 x 8192   256 x 4 47.7 / 49.6, 512 x 2 47.4 / 49.4, 1024 x 1 53.8 / 53.1
     // Few rows leave compute units idle, and one vector a lane has the shortest
-    // way (the kernel alone): 16 x 2048 64 x 4 4.6 / 5.2, 256 x 1 3.7 / 3.6 (1024 rows:
-    // with the launch 6.6 / 8.0, 6.3 / 6.9); 16 x 5120 256 x 3 4.8 / 5.0, 1024 x 1 4.8 /
-    // 4.6; 512 x 5120, with the launch, 6.9 / 8.0, 8.1 / 8.5.
+    // way: 16 x 2048 64 x 4 4.8 / 5.1, 256 x 1 3.5 / 3.4 (1024 rows 6.2 / 6.4, 5.8 / 5.7;
+    // 2048 rows 9.2 / 9.6, 10.0 / 9.8); 16 x 5120 256 x 3 4.6 / 4.6, 1024 x 1 4.3 / 4.1
+    // (512 rows 6.8 / 7.0, 7.9 / 7.6); 16 x 8192 256 x 4 5.3 / 5.4, 1024 x 1 4.7 / 4.6.  Up to
+    // 4096 elements half of those 1024 lanes hold nothing, and the way is no shorter:
+    // 16 x 4096 256 x 2 4.1 / 4.1, 512 x 1 3.7 / 3.7, 1024 x 1 4.3 / 4.0.
     if (H <= 64 && a.output != SPG_NORM_E4M3_BLOCK128) return launch_team<8, 1, 4>(a, s);    // (a group is 16 lanes)
     if (H <= 128) return launch_team<16, 1, 2>(a, s);
     if (H <= 256) return launch_team<16, 2, 1>(a, s);
