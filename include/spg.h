@@ -587,9 +587,9 @@ int expert_combine_backward(const void *grad_out, int64_t ldg, const void *y, in
  *   q, scale : codes [R, H], row stride ldq, 16-byte aligned rows, H % 16 == 0;
  *              NULL for SPG_NORM_BF16
  *   rstd     : fp32 [R] for the gradients, or NULL
- * bf16 rows need no alignment.  1 <= H <= 32768; R below 2^26 up to H = 2048,
- * 2^24 up to 8192, 2^22 beyond (else SPG_EUNSUPPORTED); R == 0 is a no-op; eps
- * >= 0 and weight_offset are finite.  h and normed may each be x or residual
+ * bf16 rows need no alignment.  1 <= H <= 32768; R below 2^26 up to H = 512, 2^26 -
+ * 3 up to 2048, 2^24 up to 8192, 2^22 beyond (else SPG_EUNSUPPORTED); R == 0 is a
+ * no-op; eps >= 0 and weight_offset are finite.  h and normed may each be x or residual
  * itself (the same pointer and row stride); any other overlap of an output
  * with another or with an input is SPG_EINVAL.  One launch, no workspace.
  */
@@ -622,7 +622,7 @@ int rms_norm(const void *x, const void *residual, const void *weight, void *h, v
  *   grad_weight : fp32 [H], written whole (zeros for R == 0), or NULL
  *   ws       : device workspace of at least rms_norm_backward_workspace_bytes(R,
  *              H) with grad_weight (any contents; 4-byte aligned)
- * Limits as rms_norm; other overlaps are SPG_EINVAL.  Sums in fp32, in an order
+ * Limits as rms_norm (R below 2^26 up to H = 2048); other overlaps are SPG_EINVAL.  Sums in fp32, in an order
  * that R and H alone decide: the same call gives the same bits.
  */
 typedef struct spg_norm_grad_desc {

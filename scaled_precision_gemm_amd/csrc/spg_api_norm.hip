@@ -10,8 +10,11 @@ using namespace spg;
 
 namespace {
 
-// Rows of one launch: below 2^32 threads with the team each row length takes.
+// Rows with the team each row length takes: some 2^32 threads.
 int64_t max_rows(int64_t H) { return INT64_C(1) << (H <= 2048 ? 26 : H <= 8192 ? 24 : 22); }
+// Rows of 64 lanes, four a workgroup: the last one of 2^24 workgroups would make
+// 2^32 threads, more than a launch takes.
+bool launchable(int64_t R, int64_t H) { return H <= 512 || H > 2048 || R <= (INT64_C(1) << 26) - 4; }
 
 int validate_norm_size(int64_t R, int64_t H)
 {
@@ -39,6 +42,7 @@ SPG_EXPORT int rms_norm(const void *x, const void *residual, const void *weight,
     const int v = validate_norm_size(d->R, d->H);
     if (v != SPG_OK) return v;
     const int64_t R = d->R, H = d->H;
+    if (!launchable(R, H)) return SPG_EUNSUPPORTED;
     if (d->output != SPG_NORM_BF16 && d->output != SPG_NORM_E4M3_ROW && d->output != SPG_NORM_E4M3_BLOCK128) return SPG_EINVAL;
     if (!(d->eps >= 0.0) || !isfinite(d->eps) || !isfinite(d->weight_offset)) return SPG_EINVAL;
     const bool coded = d->output != SPG_NORM_BF16;

@@ -150,3 +150,14 @@ def test_backward_binding_refusals(kw):
     with pytest.raises((ValueError, TypeError)) as e:
         spg.rms_norm_backward(**args)
     assert "CUDA" not in str(e.value)
+
+
+@pytest.mark.parametrize("H,most", [(513, 2 ** 26 - 4), (1024, 2 ** 26 - 4), (2048, 2 ** 26 - 4), (2049, 2 ** 24 - 1), (32768, 2 ** 22 - 1)])
+def test_rows_of_a_launch(H, most):
+    # 64 lanes a row and four rows a workgroup up to 2048 elements: 2^26 - 3 rows would be 2^32 threads, one too many
+    # for a launch.  (Nothing is launched here: the calls without an input are refused behind the sizes' check)
+    for output in (0, 1) if H % 16 == 0 else (0,):
+        assert norm(output=output, H=H, R=most + 1) == EUNSUP
+        assert norm(output=output, H=H, R=most, x=None) == EINVAL
+    # the gradients walk over their rows
+    assert backward(H=H, R=(2 ** 26 if H <= 2048 else 2 ** 24 if H <= 8192 else 2 ** 22) - 1, dy=None) == EINVAL
